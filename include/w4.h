@@ -426,6 +426,231 @@ w4_status w4_selftest_bounded_wait(uint32_t *status, w4_stream_t stream);
 w4_status w4_stream_read(const void *src, size_t bytes, int mode, uint32_t *out,
                          w4_stream_t stream);
 
+/* ======================================================================
+ * Rotary positions, a paged key-value cache and attention over it: what a
+ * decoder layer does between its qkv product and its o product.  (The paged
+ * cache and its decode attention: "Building an LLM Inference Runtime ...",
+ * section "The Stack Architecture: A One-Page Overview"; partial results over
+ * pieces of the length, joined by their log-sum-exp: "CodeAlign-Runtime",
+ * section "Level 4"; 1..8 new tokens: "qengine", section "How it works".)
+ *
+ * Like the products, every call below enqueues work on `stream`, allocates
+ * nothing, checks its arguments on the host and can be captured in a CUDA
+ * graph.  The structures are host memory, read during the call.  Positions,
+ * lengths and block tables are device memory and are checked by the kernels:
+ * what is out of range is left out and recorded in the caller's error word
+ * (device uint32, may be NULL; the kernels only ever set bits of it):
+ */
+#define W4_KV_ERR_POSITION 1u    /* a position past the rotation table or the block table */
+#define W4_KV_ERR_PAGE 2u        /* a page number outside the pool */
+#define W4_KV_ERR_SEQUENCE 4u    /* a sequence number outside the block table */
+#define W4_KV_ERR_LENGTH 8u      /* a length past the block table (it is cut to it) */
+#define W4_KV_ERR_WAIT 16u       /* a kernel gave up waiting for its own copies */
+
+/* A bfloat16 tensor [tokens][heads][head_dim] whose last dimension is
+ * contiguous; strides in elements (may be those of a slice of a wider row,
+ * such as the q heads of a fused qkv product). */
+typedef struct w4_heads {
+    void *data;                  /* device; only read where the call takes it as an input */
+    int64_t token_stride;
+    int64_t head_stride;
+} w4_heads;
+
+/* Which values of a head form a pair: i and i + rotary_dim/2, or 2i and 2i+1. */
+#define W4_ROPE_HALF 0
+#define W4_ROPE_INTERLEAVED 1
+
+/* A table of rotations: (cos, sin) pairs, float [rows][rotary_dim/2][2], row p
+ * for position p.  Filled by w4_rope_table, or by the caller. */
+typedef struct w4_rotation {
+    const float *table;          /* device, 16-byte aligned */
+    int rows;
+    int rotary_dim;              /* even; the first rotary_dim values of a head are rotated */
+    int layout;                  /* W4_ROPE_HALF or W4_ROPE_INTERLEAVED */
+} w4_rotation;
+
+/* How frequencies are scaled for contexts longer than the trained one. */
+#define W4_ROPE_SCALE_NONE 0     /* f_i = base^(-2i/rotary_dim) */
+#define W4_ROPE_SCALE_LINEAR 1   /* f_i / factor */
+#define W4_ROPE_SCALE_BASE 2     /* base * factor^(rotary_dim/(rotary_dim-2)) instead of base */
+#define W4_ROPE_SCALE_PARTS 3    /* between f_i / factor, for pairs that make at most low_turns
+                                    turns in original_context positions, and f_i, for those that
+                                    make at least high_turns; linear in the turns between */
+typedef struct w4_rope_spec {
+    int rotary_dim;              /* even, 2..512 */
+    int scaling;
+    double base;                 /* > 0 */
+    double factor;               /* > 0 (ignored by W4_ROPE_SCALE_NONE) */
+    double original_context;     /* W4_ROPE_SCALE_PARTS: > 0 */
+    double low_turns;            /* W4_ROPE_SCALE_PARTS: low_turns < high_turns */
+    double high_turns;
+    double amplitude;            /* cos and sin are multiplied by it (1: a plain rotation) */
+} w4_rope_spec;
+
+/*
+ * Fills rows 0..rows-1 of a rotation table: amplitude * (cos, sin)(p * f_i).
+ * The angle p * f_i is reduced to a fraction of a turn in 64-bit integers, so
+ * its error does not grow with p (each entry is within 1 ulp of the exact
+ * value of the double-precision f_i).
+ *   table : device, float [rows][rotary_dim/2][2], 16-byte aligned
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_CUDA.
+ */
+w4_status w4_rope_table(const w4_rope_spec *spec, int rows, float *table, w4_stream_t stream);
+
+/*
+ * y[t][h] = x[t][h] with its first rotary_dim values rotated by the table's
+ * row positions[t]; for a pair (a, b): (a c - b s, b c + a s), every operation
+ * rounded to fp32 once, the results rounded to bfloat16 once; the other
+ * values of the head are copied.  A negative position -p rotates back by row
+ * p: that is the transposed map, so it turns gradients of y into gradients
+ * of x.
+ *   x, y      : device, 2-byte aligned.  y may be x (same strides); otherwise
+ *               they must not overlap.  Rows that are 16-byte aligned (data,
+ *               strides, rotary_dim a multiple of 16) go by 16-byte accesses.
+ *   tokens    : >= 0 (0: nothing is done);  heads >= 1
+ *   head_dim  : 1..1024, at least rotary_dim
+ *   positions : device int32 [tokens]; a token whose |position| is not a row
+ *               of the table is left out (W4_KV_ERR_POSITION)
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (2^31 or more blocks of
+ * work), W4_ERR_CUDA.
+ */
+w4_status w4_rope(const w4_heads *x, const w4_heads *y, int tokens, int heads, int head_dim,
+                  const int32_t *positions, const w4_rotation *rotation, uint32_t *error,
+                  w4_stream_t stream);
+
+/* Storage formats of a paged cache. */
+#define W4_KV_BF16 0
+#define W4_KV_INT8 1
+#define W4_KV_INT4 2
+
+/*
+ * Paged key-value cache.  The pool is an array of records; a record holds the
+ * keys and values of 16 consecutive tokens of one key/value head:
+ *   record of (page p, head h, tokens 16i..16i+15 of the page) =
+ *     number (p * kv_heads + h) * (page_tokens / 16) + i
+ * so the record of 16 tokens is one contiguous copy, whatever the page size.
+ * With D = head_dim and r = 0..15 a token of the record, its bytes are
+ *   keys    16 rows of D values, row r for token r
+ *     bf16: 2D bytes a row; the 16-byte piece c of a row is stored as piece c ^ (r & 7)
+ *     int8: D bytes a row; for D = 128, piece c is stored as piece c ^ (4 * (r & 1))
+ *     int4: D/2 bytes a row; value d is nibble d & 1 of byte d / 2
+ *   values
+ *     bf16: as the keys
+ *     int8: value d of token r is byte d/32 * 512 + L * 16 + (d/8 % 4) * 4 + B
+ *     int4: value d of token r is nibble (d/8 & 1) of byte
+ *           d/64 * 512 + L * 16 + (d/16 % 4) * 4 + B
+ *           with L = 4 * (d & 7) + (r & 7) / 2 and B = 2 * (r & 1) + r / 8:
+ *           the order in which the tensor cores' lanes take them
+ *   int8, int4: then 16 key and 16 value descriptors, uint32: binary16 scale
+ *           s | zero point z << 16
+ * for 64 D bytes (bf16), 32 D + 128 (int8) or 16 D + 128 (int4) in all.
+ * A token's key (value) of a head is one group, quantised as by
+ * W4_QUANT_ASYMMETRIC with Q = 255 or 15 levels, in fp32, each operation
+ * rounded to nearest even: lo = min(0, min x), hi = max(0, max x),
+ * s = binary16((hi - lo) / Q) (at most 65504), z = clamp(rint(-lo / s), 0, Q),
+ * q = clamp(rint(x / s) + z, 0, Q), read back as (q - z) * s; s = 0 stores
+ * z = q = 0.  An infinite value is held as the largest that the scale reaches,
+ * NaN as 0; bf16 caches keep both.
+ */
+typedef struct w4_kv_cache {
+    void *pool;                  /* device, 128-byte aligned, w4_kv_pool_bytes() bytes */
+    int format;                  /* W4_KV_* */
+    int kv_heads;                /* >= 1 */
+    int head_dim;                /* 64 or 128 */
+    int page_tokens;             /* a multiple of 16 */
+    int pages;                   /* >= 1 */
+    uint32_t *error;             /* device error word, 4-byte aligned, or NULL */
+} w4_kv_cache;
+
+/* Block table: pages[b * stride + i] is the page with tokens i * page_tokens ..
+ * (i+1) * page_tokens - 1 of sequence b. */
+typedef struct w4_block_table {
+    const int32_t *pages;        /* device int32 */
+    int seqs;                    /* rows, >= 1 */
+    int width;                   /* pages a row, >= 1 */
+    int64_t stride;              /* row stride, >= width */
+} w4_block_table;
+
+/* Bytes of a pool (pool, error and block contents are not looked at).
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim). */
+w4_status w4_kv_pool_bytes(const w4_kv_cache *cache, size_t *bytes);
+
+/*
+ * Writes new tokens into the cache, rotating q and k on the way: the one
+ * launch between the qkv product and the attention.  Token t is at
+ * positions[t] of sequence seq_ids[t]; no two tokens of a call may name the
+ * same place, and other tokens of the records that are touched stay as they
+ * are.  k is rotated in fp32 and quantised from there; v is taken as it is.
+ *   k, v      : device [tokens][kv_heads][head_dim], rows 16-byte aligned
+ *   q, q_out  : device [tokens][q_heads][head_dim], rows 16-byte aligned, or
+ *               both NULL; q_out may be q; ignored without a rotation
+ *   positions : device int32 [tokens]; a negative one marks padding: the token
+ *               is left out
+ *   seq_ids   : device int32 [tokens], or NULL: tokens is a multiple of
+ *               table->seqs and every sequence has tokens / seqs consecutive ones
+ *   rotation  : NULL for none; rotary_dim a multiple of 16, at most head_dim
+ * A token that is out of range (position, sequence, page) is left out whole,
+ * its q too, and recorded in cache->error.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim, tokens * heads
+ * >= 2^31), W4_ERR_CUDA.
+ */
+w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_heads *v,
+                       const w4_heads *q, const w4_heads *q_out, int q_heads, int tokens,
+                       const int32_t *positions, const int32_t *seq_ids,
+                       const w4_block_table *table, const w4_rotation *rotation,
+                       w4_stream_t stream);
+
+/*
+ * Reads tokens back, in any order: k_out[t], v_out[t] = the cached key and
+ * value of positions[t] of sequence seq_ids[t], (q - z) * s rounded once to
+ * bfloat16.  Tokens that are negative or out of range are left out as above.
+ * Arguments as for w4_kv_append; k_out or v_out may be NULL.
+ */
+w4_status w4_kv_read(const w4_kv_cache *cache, const w4_heads *k_out, const w4_heads *v_out,
+                     int tokens, const int32_t *positions, const int32_t *seq_ids,
+                     const w4_block_table *table, w4_stream_t stream);
+
+/* Bytes of workspace for w4_paged_attn on the current device: it depends on
+ * head_dim and the SM count only.  Errors: W4_ERR_INVALID_ARG,
+ * W4_ERR_UNSUPPORTED, W4_ERR_CUDA. */
+w4_status w4_paged_attn_workspace_bytes(const w4_kv_cache *cache, size_t *bytes);
+
+/*
+ * Attention of the last `tokens` tokens of every sequence over its cache.
+ * lens[b] counts the cached tokens of sequence b, the new ones included: new
+ * token i is at position p = lens[b] - tokens + i and sees the keys
+ * j <= p, and j > p - window where window > 0.  With the row of q of token
+ * b * tokens + i and head h, and the key/value head h / (q_heads / kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,
+ *   lse = ln sum_j exp(scale * q . k_j)
+ * A row that sees no key (lens[b] = 0, or p < 0) gives out = 0, lse = -inf.
+ * What the pool holds past lens[b] is never looked at (it may be NaN).
+ * Products on the tensor cores: bf16 operands for a bf16 cache, exact codes
+ * against fp16 for the quantised ones; scores, maxima, sums and outputs are
+ * fp32; probabilities enter the second product as bf16 (fp16).  The sums'
+ * order depends on the lengths, the window and the device only, never on
+ * which block finishes first: repeated calls give the same bits.
+ *   q      : device [seqs * tokens][q_heads][head_dim] bf16, rows 16-byte aligned
+ *   out    : device [seqs * tokens][q_heads][head_dim] bf16, rows 16-byte aligned
+ *            (w4_paged_attn_f32: float, rows 16-byte aligned)
+ *   lse    : device float [seqs * tokens][q_heads], or NULL
+ *   tokens : 1..8;  q_heads : a multiple of kv_heads
+ *   lens   : device int32 [table->seqs]; negative counts as 0
+ *   scale  : finite; usually head_dim^-0.5
+ *   window : 0 for none
+ *   workspace : device, 256-byte aligned, zero before its first use; calls that
+ *            overlap on the device must not share one (as for w4_gemv_ws)
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim), W4_ERR_CUDA.
+ */
+w4_status w4_paged_attn(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                        int q_heads, int tokens, const int32_t *lens,
+                        const w4_block_table *table, float scale, int window, float *lse,
+                        void *workspace, size_t workspace_bytes, w4_stream_t stream);
+w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                            int q_heads, int tokens, const int32_t *lens,
+                            const w4_block_table *table, float scale, int window, float *lse,
+                            void *workspace, size_t workspace_bytes, w4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,8 @@ import importlib
 _BINDING_NAMES = {
     "W4Error", "Status", "repacked_sizes", "repack", "dequant", "gemv", "gemv_f32",
     "PackedWeight", "pack", "status_string", "library_path", "check_header",
+    "RopeTable", "rope", "rope_table", "PagedCache", "kv_pool_bytes", "kv_append", "kv_read",
+    "paged_attn", "paged_attn_f32", "paged_attn_workspace_bytes",
 }
 
 

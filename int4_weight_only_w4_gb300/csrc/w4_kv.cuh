@@ -1,0 +1,175 @@
+// Record layout of the paged key-value cache (include/w4.h, "Paged key-value
+// cache") and the launches of the kernels that use it.  Internal to libw4.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "w4_internal.cuh"
+
+namespace w4 {
+
+constexpr int kRecTokens = 16;    // tokens of a record = keys of one tensor-core tile
+
+// Byte offsets inside a record of format FMT (W4_KV_*) and head dimension D.
+template <int FMT, int D>
+struct KvLayout {
+    static constexpr int kBits = FMT == W4_KV_BF16 ? 16 : FMT == W4_KV_INT8 ? 8 : 4;
+    static constexpr int kLevels = FMT == W4_KV_INT8 ? 255 : 15;
+    static constexpr int kRow = D * kBits / 8;              // bytes of a token's key
+    static constexpr int kPart = kRecTokens * kRow;         // bytes of all keys (values)
+    static constexpr int kMeta = 2 * kPart;                 // descriptors of the keys
+    static constexpr int kMetaV = kMeta + 4 * kRecTokens;   // descriptors of the values
+    static constexpr int kBytes = FMT == W4_KV_BF16 ? kMeta : kMeta + 8 * kRecTokens;
+
+    // Byte of value d of token r's key, from the start of the record (int4:
+    // nibble d & 1 of it).
+    __host__ __device__ static constexpr int key(int r, int d) {
+        if (FMT == W4_KV_BF16) return r * kRow + (((d >> 3) ^ (r & 7)) << 4) + (d & 7) * 2;
+        if (FMT == W4_KV_INT8)
+            return r * kRow + (((d >> 4) ^ (D == 128 ? (r & 1) << 2 : 0)) << 4) + (d & 15);
+        return r * kRow + (d >> 1);
+    }
+    // The same of its value (int4: nibble (d >> 3) & 1 of it).
+    __host__ __device__ static constexpr int value(int r, int d) {
+        if (FMT == W4_KV_BF16) return kPart + key(r, d);
+        const int lane = 4 * (d & 7) + ((r & 7) >> 1), byte = 2 * (r & 1) + (r >> 3);
+        if (FMT == W4_KV_INT8)
+            return kPart + (d >> 5) * 512 + lane * 16 + ((d >> 3) & 3) * 4 + byte;
+        return kPart + (d >> 6) * 512 + lane * 16 + ((d >> 4) & 3) * 4 + byte;
+    }
+};
+
+inline int kv_record_bytes(int format, int head_dim) {
+    return format == W4_KV_BF16 ? 64 * head_dim
+           : format == W4_KV_INT8 ? 32 * head_dim + 128
+                                  : 16 * head_dim + 128;
+}
+
+// What the kernels need of w4_kv_cache and w4_block_table.
+struct KvPool {
+    char *records;
+    int kv_heads;
+    int page_records;     // records of a page and head
+    int page_tokens;
+    int pages;
+    uint32_t *error;
+    const int32_t *table;
+    int seqs;
+    int width;
+    long long stride;
+};
+
+struct Heads {
+    char *data;
+    long long token_stride;    // in elements
+    long long head_stride;
+};
+
+struct Rotation {
+    const float *table;        // NULL: none
+    int rows;
+    int pairs;                 // rotary_dim / 2
+    int layout;
+};
+
+// Tokens of w4_kv_append and w4_kv_read: token t is at positions[t] of
+// sequence seq_ids[t], or of t / per_seq without seq_ids.
+struct TokenList {
+    const int32_t *positions;
+    const int32_t *seq_ids;
+    int tokens;
+    int per_seq;
+};
+
+cudaError_t launch_rope_table(const unsigned long long *turns, int pairs, double amplitude,
+                              int rows, float *table, cudaStream_t stream);
+cudaError_t launch_rope(const Heads &x, const Heads &y, int tokens, int heads, int head_dim,
+                        const int32_t *positions, const Rotation &rot, uint32_t *error,
+                        bool wide, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const Heads &k,
+                             const Heads &v, const Heads &q, const Heads &q_out, int q_heads,
+                             const TokenList &list, const Rotation &rot, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,
+                           const Heads &v, const TokenList &list, int num_sms,
+                           cudaStream_t stream);
+
+struct AttnArgs {
+    KvPool pool;
+    Heads q, out;
+    float *lse;
+    const int32_t *lens;
+    int q_heads;
+    int group;       // query heads per key/value head
+    int tokens;      // new tokens per sequence
+    float scale;
+    int window;      // 0: none
+    void *workspace;
+};
+size_t attn_workspace_bytes(int head_dim, int num_sms);
+cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, bool f32_out,
+                              int num_sms, cudaStream_t stream);
+
+// Launch with programmatic stream serialisation: the grid may start while the
+// previous kernel of the stream drains; every kernel launched this way calls
+// griddepcontrol.wait before it touches memory that another kernel writes.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void begin_after_previous() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Where token t of a list is kept: the first record of its page for head 0,
+// and the token's place; false (and a bit of the error word) if it is
+// nowhere, false without one for padding.
+struct TokenPlace {
+    long long page_record;     // page * kv_heads * page_records
+    int in_page;               // token of the page
+    int position;
+};
+
+__device__ __forceinline__ bool kv_place(const KvPool &pool, const TokenList &list, int t,
+                                         int rotation_rows, TokenPlace *at) {
+    const int pos = list.positions[t];
+    if (pos < 0) return false;
+    const int seq = list.seq_ids ? list.seq_ids[t] : t / list.per_seq;
+    uint32_t bad = 0;
+    int page = 0;
+    const int slot = pos / pool.page_tokens;
+    if (seq < 0 || seq >= pool.seqs)
+        bad = W4_KV_ERR_SEQUENCE;
+    else if (slot >= pool.width || pos >= rotation_rows)
+        bad = W4_KV_ERR_POSITION;
+    else {
+        page = pool.table[seq * pool.stride + slot];
+        if (page < 0 || page >= pool.pages) bad = W4_KV_ERR_PAGE;
+    }
+    if (bad) {
+        if (pool.error) atomicOr(pool.error, bad);
+        return false;
+    }
+    at->page_record = (long long)page * pool.kv_heads * pool.page_records;
+    at->in_page = pos - slot * pool.page_tokens;
+    at->position = pos;
+    return true;
+}
+#endif
+
+}  // namespace w4

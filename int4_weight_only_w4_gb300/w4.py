@@ -396,3 +396,289 @@ def pack_swiglu(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
     repack_swiglu(qweight, scales, zeros, K, I, qo, so, zo, stream)
     check_header_swiglu(qo[:HEADER_BYTES].cpu().numpy().tobytes(), K, I)
     return PackedSwiGLU(K, I, qo, so, zo)
+
+
+# ---- rotary positions, the paged key-value cache and attention over it ---------
+
+ROPE_HALF = 0             # W4_ROPE_HALF
+ROPE_INTERLEAVED = 1      # W4_ROPE_INTERLEAVED
+ROPE_SCALE_NONE = 0       # W4_ROPE_SCALE_NONE
+ROPE_SCALE_LINEAR = 1     # W4_ROPE_SCALE_LINEAR
+ROPE_SCALE_BASE = 2       # W4_ROPE_SCALE_BASE
+ROPE_SCALE_PARTS = 3      # W4_ROPE_SCALE_PARTS
+KV_BF16 = 0               # W4_KV_BF16
+KV_INT8 = 1               # W4_KV_INT8
+KV_INT4 = 2               # W4_KV_INT4
+KV_ERR_POSITION = 1       # W4_KV_ERR_POSITION
+KV_ERR_PAGE = 2           # W4_KV_ERR_PAGE
+KV_ERR_SEQUENCE = 4       # W4_KV_ERR_SEQUENCE
+KV_ERR_LENGTH = 8         # W4_KV_ERR_LENGTH
+KV_ERR_WAIT = 16          # W4_KV_ERR_WAIT
+RECORD_TOKENS = 16        # tokens of a cache record; page sizes are multiples of it
+
+_I64 = ctypes.c_int64
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("table", _P), ("rows", _I), ("rotary_dim", _I), ("layout", _I)]
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("rotary_dim", _I), ("scaling", _I), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pool", _P), ("format", _I), ("kv_heads", _I), ("head_dim", _I),
+                ("page_tokens", _I), ("pages", _I), ("error", _P)]
+
+
+class _BlockTable(ctypes.Structure):
+    _fields_ = [("pages", _P), ("seqs", _I), ("width", _I), ("stride", _I64)]
+
+
+_rope_table = _decl("w4_rope_table", _ST, _P, _I, _P, _P)
+_rope = _decl("w4_rope", _ST, _P, _P, _I, _I, _I, _P, _P, _P, _P)
+_kv_pool_bytes = _decl("w4_kv_pool_bytes", _ST, _P, ctypes.POINTER(ctypes.c_size_t))
+_kv_append = _decl("w4_kv_append", _ST, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P)
+_kv_read = _decl("w4_kv_read", _ST, _P, _P, _P, _I, _P, _P, _P, _P)
+_paged_attn_workspace_bytes = _decl("w4_paged_attn_workspace_bytes", _ST, _P,
+                                    ctypes.POINTER(ctypes.c_size_t))
+_ATTN_ARGS = (_P, _P, _P, _I, _I, _P, _P, ctypes.c_float, _I, _P, _P, ctypes.c_size_t, _P)
+_paged_attn = _decl("w4_paged_attn", _ST, *_ATTN_ARGS)
+_paged_attn_f32 = _decl("w4_paged_attn_f32", _ST, *_ATTN_ARGS)
+
+
+def _heads(t, dtype=torch.bfloat16) -> _Heads | None:
+    """[tokens, heads, head_dim] with a contiguous last dimension, as w4_heads."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dtype != dtype or t.dim() != 3:
+        raise ValueError(f"expected a {dtype} tensor [tokens, heads, head_dim]")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return _Heads(t.data_ptr(), st, sh)
+
+
+def _int32(t, n: int, what: str) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what}: expected {n} int32 values")
+    return _ptr(t)
+
+
+def _block_table(t) -> _BlockTable:
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("block table: expected a CUDA int32 tensor [seqs, pages]")
+    return _BlockTable(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def rope_table(spec: dict, rows: int, table, stream=None) -> None:
+    """w4_rope_table: fill `table`, float32 [rows, rotary_dim/2, 2] on the
+    device.  spec: the fields of w4_rope_spec (missing ones: no scaling,
+    factor 1, amplitude 1)."""
+    full = dict(scaling=ROPE_SCALE_NONE, factor=1.0, original_context=0.0, low_turns=0.0,
+                high_turns=0.0, amplitude=1.0)
+    full.update(spec)
+    s = _RopeSpec(**full)
+    if table.dtype != torch.float32 or table.numel() != rows * s.rotary_dim:
+        raise ValueError("table: expected float32 [rows, rotary_dim/2, 2]")
+    _ok(_rope_table(ctypes.byref(s), rows, _ptr(table), _stream(stream, table)),
+        "w4_rope_table")
+
+
+def rope(x, y, positions, rotation: "RopeTable", error=None, stream=None) -> None:
+    """w4_rope: y[t, h] = x[t, h] rotated by row positions[t] of the table
+    (y may be x; a negative position rotates back)."""
+    T, H, D = x.shape
+    if y.shape != x.shape:
+        raise ValueError("y: expected the shape of x")
+    _ok(_rope(ctypes.byref(_heads(x)), ctypes.byref(_heads(y)), T, H, D,
+              _int32(positions, T, "positions"), ctypes.byref(rotation.struct), _ptr(error),
+              _stream(stream, x)), "w4_rope")
+
+
+def kv_pool_bytes(fmt: int, kv_heads: int, head_dim: int, page_tokens: int, pages: int) -> int:
+    """Bytes of a paged cache's pool."""
+    c, n = _KvCache(None, fmt, kv_heads, head_dim, page_tokens, pages, None), ctypes.c_size_t()
+    _ok(_kv_pool_bytes(ctypes.byref(c), ctypes.byref(n)), "w4_kv_pool_bytes")
+    return n.value
+
+
+def kv_append(cache: "PagedCache", k, v, positions, table, seq_ids=None, q=None, q_out=None,
+              rotation: "RopeTable | None" = None, stream=None) -> None:
+    """w4_kv_append: write tokens into the cache, rotating k and q (into q_out)."""
+    T = k.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k, v: expected {shape}")
+    if q is not None and (q.shape[0] != T or q.shape[2] != cache.head_dim or q_out is None
+                          or q_out.shape != q.shape):
+        raise ValueError("q, q_out: expected [tokens, q_heads, head_dim]")
+    _ok(_kv_append(cache.ref, _ref(_heads(k)), _ref(_heads(v)), _ref(_heads(q)),
+                   _ref(_heads(q_out)), 0 if q is None else q.shape[1], T,
+                   _int32(positions, T, "positions"), _int32(seq_ids, T, "seq_ids"),
+                   _ref(_block_table(table)), _ref(rotation and rotation.struct),
+                   _stream(stream, k)), "w4_kv_append")
+
+
+def kv_read(cache: "PagedCache", k_out, v_out, positions, table, seq_ids=None,
+            stream=None) -> None:
+    """w4_kv_read: the cached keys and values of the listed tokens, bfloat16."""
+    T = positions.numel()
+    for x in (k_out, v_out):
+        if x is not None and x.shape != (T, cache.kv_heads, cache.head_dim):
+            raise ValueError("k_out, v_out: expected [tokens, kv_heads, head_dim]")
+    _ok(_kv_read(cache.ref, _ref(_heads(k_out)), _ref(_heads(v_out)), T,
+                 _int32(positions, T, "positions"), _int32(seq_ids, T, "seq_ids"),
+                 _ref(_block_table(table)), _stream(stream, positions)), "w4_kv_read")
+
+
+def paged_attn_workspace_bytes(cache: "PagedCache") -> int:
+    """Bytes of workspace that paged_attn needs on the current device."""
+    n = ctypes.c_size_t()
+    _ok(_paged_attn_workspace_bytes(cache.ref, ctypes.byref(n)), "w4_paged_attn_workspace_bytes")
+    return n.value
+
+
+def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, workspace, stream):
+    T, H, D = q.shape
+    B = table.shape[0]
+    if T % B or D != cache.head_dim or out.shape != q.shape:
+        raise ValueError("q, out: expected [seqs * tokens, q_heads, head_dim]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != T * H):
+        raise ValueError("lse: expected float32 [seqs * tokens, q_heads]")
+    _ok(fn(cache.ref, ctypes.byref(_heads(q)), ctypes.byref(_heads(out, dtype)), H, T // B,
+           _int32(lens, B, "lens"), ctypes.byref(_block_table(table)),
+           D ** -0.5 if scale is None else scale, window, _ptr(lse), _ptr(workspace),
+           workspace.numel() * workspace.element_size(), _stream(stream, q)), where)
+
+
+def paged_attn(cache: "PagedCache", q, out, lens, table, workspace, scale=None, window: int = 0,
+               lse=None, stream=None) -> None:
+    """w4_paged_attn: out[b * tokens + i] (bfloat16) = attention of the new
+    token i of sequence b over its cached tokens."""
+    _attn(_paged_attn, "w4_paged_attn", torch.bfloat16, cache, q, out, lens, table, scale,
+          window, lse, workspace, stream)
+
+
+def paged_attn_f32(cache: "PagedCache", q, out, lens, table, workspace, scale=None,
+                   window: int = 0, lse=None, stream=None) -> None:
+    """w4_paged_attn_f32: as paged_attn, fp32 result."""
+    _attn(_paged_attn_f32, "w4_paged_attn_f32", torch.float32, cache, q, out, lens, table, scale,
+          window, lse, workspace, stream)
+
+
+class RopeTable:
+    """A table of rotations: float32 [rows, rotary_dim/2, 2] (cos, sin) pairs
+    on the device, and which values of a head form a pair."""
+
+    def __init__(self, table: torch.Tensor, layout: int = ROPE_HALF):
+        if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32:
+            raise ValueError("table: expected float32 [rows, rotary_dim/2, 2]")
+        self.table, self.layout = table, layout
+        self.struct = _Rotation(_ptr(table), table.shape[0], 2 * table.shape[1], layout)
+
+    @classmethod
+    def make(cls, rows: int, rotary_dim: int, base: float, layout: int = ROPE_HALF, device=None,
+             stream=None, **scaling) -> "RopeTable":
+        """A table filled by w4_rope_table; scaling: scaling, factor,
+        original_context, low_turns, high_turns, amplitude of w4_rope_spec."""
+        t = torch.empty((rows, rotary_dim // 2, 2), dtype=torch.float32,
+                        device=device if device is not None else "cuda")
+        rope_table(dict(rotary_dim=rotary_dim, base=base, **scaling), rows, t, stream)
+        return cls(t, layout)
+
+    def apply(self, x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor | None = None,
+              error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x [tokens, heads, head_dim] bfloat16, rotated; out may be x."""
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        rope(x, out, positions, self, error, stream)
+        return out
+
+
+class PagedCache:
+    """A paged key-value cache over a caller's pool (a contiguous CUDA tensor
+    of kv_pool_bytes() bytes).  Its calls record what is out of range in
+    `error` (one int32 on the device; see check()).  attend() uses the cache's
+    own workspace unless it is given one: calls that overlap on the device
+    need one each."""
+
+    def __init__(self, pool: torch.Tensor, fmt: int, kv_heads: int, head_dim: int,
+                 page_tokens: int = RECORD_TOKENS, error: torch.Tensor | None = None):
+        per_page = kv_pool_bytes(fmt, kv_heads, head_dim, page_tokens, 1)
+        nbytes = pool.numel() * pool.element_size()
+        if nbytes == 0 or nbytes % per_page:
+            raise ValueError(f"pool: expected a multiple of {per_page} bytes")
+        self.pool, self.format = pool, fmt
+        self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
+        self.pages = nbytes // per_page
+        self.error = torch.zeros(1, dtype=torch.int32, device=pool.device) if error is None \
+            else error
+        self._struct = _KvCache(_ptr(pool), fmt, kv_heads, head_dim, page_tokens, self.pages,
+                                _ptr(self.error))
+        self.ref = ctypes.byref(self._struct)
+        self.workspace = None
+
+    @classmethod
+    def make(cls, pages: int, fmt: int, kv_heads: int, head_dim: int,
+             page_tokens: int = RECORD_TOKENS, device=None) -> "PagedCache":
+        """A cache with a pool of its own (allocated by torch, zero-filled)."""
+        n = kv_pool_bytes(fmt, kv_heads, head_dim, page_tokens, pages)
+        return cls(torch.zeros(n, dtype=torch.uint8,
+                               device=device if device is not None else "cuda"),
+                   fmt, kv_heads, head_dim, page_tokens)
+
+    def append(self, k, v, positions, table, seq_ids=None, q=None, q_out=None, rope=None,
+               stream=None) -> None:
+        kv_append(self, k, v, positions, table, seq_ids, q, q_out, rope, stream)
+
+    def read(self, positions, table, seq_ids=None, k=None, v=None, stream=None):
+        shape = (positions.numel(), self.kv_heads, self.head_dim)
+        if k is None:
+            k = torch.zeros(shape, dtype=torch.bfloat16, device=self.pool.device)
+        if v is None:
+            v = torch.zeros(shape, dtype=torch.bfloat16, device=self.pool.device)
+        kv_read(self, k, v, positions, table, seq_ids, stream)
+        return k, v
+
+    def new_workspace(self) -> torch.Tensor:
+        """A zero-filled workspace for attend()."""
+        return torch.zeros(paged_attn_workspace_bytes(self), dtype=torch.uint8,
+                           device=self.pool.device)
+
+    def attend(self, q, lens, table, scale=None, window: int = 0, out=None, lse=None,
+               workspace=None, stream=None):
+        """Attention of the new tokens; returns (out bfloat16, lse float32)."""
+        if workspace is None:
+            if self.workspace is None:
+                self.workspace = self.new_workspace()
+            workspace = self.workspace
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        paged_attn(self, q, out, lens, table, workspace, scale, window, lse, stream)
+        return out, lse
+
+    def check(self) -> None:
+        """Raise W4Error if a call recorded an error (synchronises), and clear it."""
+        bits = int(self.error.item())
+        if bits:
+            self.error.zero_()
+            raise W4Error(Status.INVALID_ARG, f"paged cache (error word {bits})")
