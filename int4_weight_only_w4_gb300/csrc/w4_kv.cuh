@@ -99,6 +99,7 @@ struct AttnArgs {
     KvPool pool;
     Heads q, out;
     float *lse;
+    bool f32_out;    // out is float, not bfloat16
     const int32_t *lens;
     int q_heads;
     int group;       // query heads per key/value head
@@ -108,8 +109,8 @@ struct AttnArgs {
     void *workspace;
 };
 size_t attn_workspace_bytes(int head_dim, int num_sms);
-cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, bool f32_out,
-                              int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, int num_sms,
+                              cudaStream_t stream);
 
 // Launch with programmatic stream serialisation: the grid may start while the
 // previous kernel of the stream drains; every kernel launched this way calls

@@ -119,6 +119,7 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     a.q = heads_of(q);
     a.out = heads_of(out);
     a.lse = lse;
+    a.f32_out = f32_out;
     a.lens = lens;
     a.q_heads = q_heads;
     a.group = q_heads / cache->kv_heads;
@@ -126,7 +127,7 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     a.scale = scale;
     a.window = window;
     a.workspace = workspace;
-    return cuda_status(w4::launch_paged_attn(a, cache->format, cache->head_dim, f32_out, sms,
+    return cuda_status(w4::launch_paged_attn(a, cache->format, cache->head_dim, sms,
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
