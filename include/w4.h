@@ -640,7 +640,8 @@ w4_status w4_paged_attn_workspace_bytes(const w4_kv_cache *cache, size_t *bytes)
  *   window : 0 for none
  *   workspace : device, 256-byte aligned, zero before its first use; calls that
  *            overlap on the device must not share one (as for w4_gemv_ws)
- * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim), W4_ERR_CUDA.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, or a table
+ * and heads that allow 2^31 or more visits of records), W4_ERR_CUDA.
  */
 w4_status w4_paged_attn(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
                         int q_heads, int tokens, const int32_t *lens,

@@ -51,6 +51,7 @@ struct KvPool {
     char *records;
     int kv_heads;
     int page_records;     // records of a page and head
+    int page_shift;       // its log2, or -1
     int page_tokens;
     int pages;
     uint32_t *error;

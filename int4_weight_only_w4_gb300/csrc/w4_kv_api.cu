@@ -69,6 +69,9 @@ w4::KvPool pool_of(const w4_kv_cache *c, const w4_block_table *t) {
     p.records = static_cast<char *>(c->pool);
     p.kv_heads = c->kv_heads;
     p.page_records = c->page_tokens / w4::kRecTokens;
+    p.page_shift = -1;
+    for (int s = 0; s < 17; ++s)
+        if (p.page_records == 1 << s) p.page_shift = s;
     p.page_tokens = c->page_tokens;
     p.pages = c->pages;
     p.error = c->error;
@@ -109,6 +112,14 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
         return W4_ERR_INVALID_ARG;
     if ((long long)table->width * cache->page_tokens >= (1LL << 31) ||
         (long long)table->seqs * q_heads * tokens >= (1LL << 31))
+        return W4_ERR_UNSUPPORTED;
+    // records that the call could visit, counted in 32 bits
+    const long long row_tiles = ((long long)tokens * (q_heads / cache->kv_heads) + 63) / 64;
+    const long long longest =
+        (long long)table->width * (cache->page_tokens / w4::kRecTokens) + 1;
+    if (longest * table->seqs >= (1LL << 31) ||
+        longest * table->seqs * cache->kv_heads >= (1LL << 31) ||
+        longest * table->seqs * cache->kv_heads * row_tiles >= (1LL << 31))
         return W4_ERR_UNSUPPORTED;
     const int sms = device_sms();
     if (sms <= 0) return W4_ERR_CUDA;

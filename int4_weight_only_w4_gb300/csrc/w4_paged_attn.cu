@@ -24,16 +24,15 @@
 // p s_v = exp2(y + log2 s_v - m), m taken over that sum, so that p fits
 // binary16 whatever the scales are.
 //
-// Schedule.  The blocks, one per SM, divide the records among themselves from
-// the lengths on the device.  With at most half as many heads (sequence x
-// key/value head) as blocks, every head is cut into equal parts, as many as
-// fit the grid, and a block takes one.  With more heads, block c takes records
-// [c W / G, (c + 1) W / G) of the list (sequence, head, record): its stretch
-// may cover several heads, the first and the last of them in part.  The parts
-// of a head are joined by the block that finishes it last, in block order.
-// In a block the warps form KG groups of QG: a group takes every KG-th record
-// through its own ring of bulk copies (one record is one copy), and its QG
-// warps hold 8 rows each.
+// Schedule.  The blocks, one per SM, divide the list (sequence, head, record)
+// evenly among themselves, from the lengths on the device: block c takes the
+// records from cut c to cut c + 1.  A cut that would leave only a few records
+// of a head on one side moves to the head's border, so short heads stay whole.
+// The pieces of a cut head are joined by the block that finishes it last, in
+// block order.  In a block, one warp issues the copies, a record a bulk copy,
+// running ahead over the block's whole stretch; the others form KG groups of
+// QG: a group takes every KG-th record through its own ring, and its QG warps
+// hold 8 NT rows each.
 #include <atomic>
 
 #include "w4_device.cuh"
@@ -42,22 +41,22 @@
 namespace w4 {
 namespace {
 
-constexpr int kAttnWarps = 16, kAttnThreads = 32 * kAttnWarps;
-constexpr int kRowsMax = 64;           // rows of a block: 8 a warp, up to 8 warps a group
-constexpr int kRingBytes = 196608;     // shared by the groups; the join uses it in between
-constexpr int kMaxStages = 32;         // of one group's ring
+constexpr int kRowsMax = 64;           // rows of a block
+constexpr int kMaxWarps = 16;          // warps that compute
+constexpr int kMaxStages = 16;         // of one group's ring
 constexpr int kMaxGrid = 256;
+constexpr int kSharedBytes = 224256;   // rings and join: 219 of the 227 KB of a block
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen no key
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+__device__ __forceinline__ void ldsm4(uint32_t *r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+__device__ __forceinline__ void ldsm4_t(uint32_t *r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
@@ -71,6 +70,11 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -90,6 +94,11 @@ __device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
+}
+
+// Block-table column of record r of a sequence.
+__device__ __forceinline__ int page_slot(const KvPool &pool, int r) {
+    return pool.page_shift >= 0 ? r >> pool.page_shift : r / pool.page_records;
 }
 
 struct Seq {
@@ -112,151 +121,155 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
     return s;
 }
 
-// A warp's tile of 8 rows: its share of Q, and the running m, l, O.
-template <int FMT, int D>
+// A warp's NT tiles of 8 rows: its share of Q, and the running m, l, O.
+template <int FMT, int D, int NT>
 struct Tile {
     using L = KvLayout<FMT, D>;
     static constexpr int KS = D / 16;                     // k-steps of S, m-tiles of O
+    static constexpr int VREGS = L::kPart / 128;          // registers of a record's values
     static constexpr float kBias = FMT == W4_KV_BF16 ? 0.f : 6.f;
     static constexpr float kSlack = FMT == W4_KV_BF16 ? 8.f : 14.f;
 
-    uint32_t qf[KS][2];          // Q as the column operand
-    float o[KS][4];
-    float m[2], l[2];            // columns 2t, 2t + 1
-    float sc[2];                 // score factor of a column
+    uint32_t qf[NT][KS][2];      // Q as the column operand
+    float o[NT][KS][4];
+    float m[NT][2], l[NT][2];    // columns 2t, 2t + 1 of each tile
+    float sc[NT][2];             // score factor of a column
 
     // Which value of the head goes with half e of register i of k-step ks.
-    __device__ static int q_index(int ks, int i, int e, int t) {
+    __device__ static constexpr int q_index(int ks, int i, int e, int t) {
         if (FMT == W4_KV_BF16) return 16 * ks + 8 * i + 2 * t + e;
         if (FMT == W4_KV_INT8) return 64 * (ks >> 2) + 16 * t + 4 * (ks & 3) + i + 2 * e;
         return (D / 4) * t + 8 * (ks >> 1) + 2 * (ks & 1) + i + 4 * e;
     }
 
-    // row0: first row of the warp's tile; rows: rows that there are.
-    __device__ void load_q(const AttnArgs &a, int b, int h, int row0, int rows) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r = row0 + g;
-        const bool there = r < rows;
-        const int i = there ? r / a.group : 0, hq = there ? r - i * a.group : 0;
-        const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.q.data) +
-                                 (long long)(b * a.tokens + i) * a.q.token_stride +
-                                 (long long)(h * a.group + hq) * a.q.head_stride;
-        if constexpr (FMT == W4_KV_BF16) {
+    // row0: first row of the warp's tiles; rows: rows that there are.
+    __device__ __forceinline__ void load_q(const AttnArgs &a, int b, int h, int row0, int rows) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+        for (int n = 0; n < NT; ++n) {
+            const int r = row0 + 8 * n + g;
+            const bool there = r < rows;
+            const int i = there ? r / a.group : 0, hq = there ? r - i * a.group : 0;
+            const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.q.data) +
+                                     (long long)(b * a.tokens + i) * a.q.token_stride +
+                                     (long long)(h * a.group + hq) * a.q.head_stride;
+            if constexpr (FMT == W4_KV_BF16) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    qf[ks][j] =
-                        there ? *reinterpret_cast<const uint32_t *>(q + q_index(ks, j, 0, t)) : 0u;
-            sc[0] = sc[1] = a.scale * kLog2e;
-        } else {
-            // a lane's values lie in runs of RUN
-            constexpr int RUN = FMT == W4_KV_INT8 ? 16 : D / 4, NRUN = D / 4 / RUN;
-            uint4 raw[NRUN * RUN / 8];
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int x = 0; x < NRUN * RUN / 8; ++x)
-                raw[x] = there ? *reinterpret_cast<const uint4 *>(
-                                     q + (x / (RUN / 8)) * 64 + RUN * t + (x % (RUN / 8)) * 8)
-                               : make_uint4(0u, 0u, 0u, 0u);
-            const auto value = [&](int ks, int j, int e) {
-                const int d = q_index(ks, j, e, 0);       // of lane t = 0
-                const int at = (d / 64) * (FMT == W4_KV_INT8 ? RUN : 0) + d % 64;
-                const uint4 v = raw[at / 8];
-                const uint32_t w = at % 8 < 2 ? v.x : at % 8 < 4 ? v.y : at % 8 < 6 ? v.z : v.w;
-                return __uint_as_float(at & 1 ? w & 0xFFFF0000u : w << 16);
-            };
-            float top = 0.f;
+                    for (int j = 0; j < 2; ++j)
+                        qf[n][ks][j] =
+                            there ? *reinterpret_cast<const uint32_t *>(q + q_index(ks, j, 0, t))
+                                  : 0u;
+                sc[n][0] = sc[n][1] = a.scale * kLog2e;
+            } else {
+                // a lane's values lie in runs of RUN
+                constexpr int RUN = FMT == W4_KV_INT8 ? 16 : D / 4, PIECES = D / 32;
+                uint4 raw[PIECES];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+                for (int x = 0; x < PIECES; ++x)
+                    raw[x] = there ? *reinterpret_cast<const uint4 *>(
+                                         q + (x / (RUN / 8)) * 64 + RUN * t + (x % (RUN / 8)) * 8)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+                const auto value = [&](int ks, int j, int e) {
+                    const int d = q_index(ks, j, e, 0);   // of lane t = 0
+                    const int at = (d / 64) * (FMT == W4_KV_INT8 ? RUN : 0) + d % 64;
+                    const uint4 v = raw[at / 8];
+                    const uint32_t w =
+                        at % 8 < 2 ? v.x : at % 8 < 4 ? v.y : at % 8 < 6 ? v.z : v.w;
+                    return __uint_as_float(at & 1 ? w & 0xFFFF0000u : w << 16);
+                };
+                float top = 0.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    top = fmaxf(top, fmaxf(fabsf(value(ks, j, 0)), fabsf(value(ks, j, 1))));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // a power of two that brings the largest |q| into [2^14, 2^15):
-            // q is exact in binary16 down to 2^-28 of it
-            int e = 0;
-            if (top > 0.f && top < INFINITY)
-                e = 14 - max(-86, (int)(__float_as_uint(top) >> 23) - 127);
-            const float up = __int_as_float((127 + e) << 23);
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+                    for (int j = 0; j < 2; ++j)
+                        top = fmaxf(top, fmaxf(fabsf(value(ks, j, 0)), fabsf(value(ks, j, 1))));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                // a power of two that brings the largest |q| into [2^14, 2^15):
+                // q is exact in binary16 down to 2^-28 of it
+                int e = 0;
+                if (top > 0.f && top < INFINITY)
+                    e = 14 - max(-86, (int)(__float_as_uint(top) >> 23) - 127);
+                const float up = __int_as_float((127 + e) << 23);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    qf[ks][j] = pack_half(value(ks, j, 0) * up, value(ks, j, 1) * up);
-            const float f = a.scale * kLog2e * __int_as_float((127 - e) << 23);
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) sc[c] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t + c));
+                    for (int j = 0; j < 2; ++j)
+                        qf[n][ks][j] = pack_half(value(ks, j, 0) * up, value(ks, j, 1) * up);
+                const float f = a.scale * kLog2e * __int_as_float((127 - e) << 23);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    sc[n][c] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t + c));
+            }
         }
     }
 
-    __device__ void clear() {
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[k][c] = 0.f;
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) m[c] = kNone, l[c] = 0.f;
+                for (int c = 0; c < 4; ++c) o[n][k][c] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) m[n][c] = kNone, l[n][c] = 0.f;
+        }
     }
 
-    // Operands of four codes (two of key pair `lo`, two of the next): bytes 0, 2
-    // and 1, 3 of a word of 8-bit codes; minus[]: -(1024 + z) of their keys.
+    // Operands of four codes: bytes 0, 2 of a word of 8-bit codes, or the low
+    // (high) nibbles of bytes 0, 2; minus: -(1024 + z) of their keys (high
+    // nibbles: (1024 + 16 u) / 16 - (64 + z)).
     __device__ static uint32_t even(uint32_t w, uint32_t minus) {
         return half2_add(and_or(w, 0x00FF00FFu, 0x64006400u), minus);
     }
     __device__ static uint32_t low(uint32_t w, uint32_t minus) {
         return half2_add(and_or(w, 0x000F000Fu, 0x64006400u), minus);
     }
-    // high nibbles: (1024 + 16 u) / 16 - (64 + z)
     __device__ static uint32_t high(uint32_t w, uint32_t minus) {
         return half2_fma(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, minus);
     }
 
     // One record in shared memory, its first key j0.  edge: some row does not
     // see all of it.
-    __device__ void record(const AttnArgs &a, uint32_t rec, int j0, bool edge, int len, int row0,
-                           int rows) {
+    __device__ __forceinline__ void record(const AttnArgs &a, uint32_t rec, int j0, bool edge,
+                                           int len, int row0, int rows) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        float s[4];
+        float s[NT][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                s[c] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
         // ---- S^T = K Q^T
-        uint32_t mk[2], zk[2], zk16[2];      // keys g, g + 8: -(1024 + z), -(64 + z), twice each
-        if constexpr (FMT != W4_KV_BF16) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                mk[r] = lds32(rec + L::kMeta + 4 * (g + 8 * r));
-                const uint32_t z = __byte_perm(mk[r], 0u, 0x4242);
-                zk[r] = z | 0xE400E400u;
-                zk16[r] = half2_add(zk[r], 0x63806380u);  // + 960
-            }
-        }
+        uint32_t mk[2], mv[2], mt[2][2], vraw[VREGS];
         if constexpr (FMT == W4_KV_BF16) {
-            const int r = ((lane >> 3) & 1) * 8 + (lane & 7), hi = lane >> 4;
+            // piece 2 ks + hi of a row is stored at ^ (row & 7): only four
+            // addresses differ, the others are 128 bytes on
+            const uint32_t row = rec + (lane & 15) * L::kRow, x = lane & 7, hi = lane >> 4;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t k4[4];
-                ldsm4(k4, rec + r * L::kRow + (((2 * ks + hi) ^ (r & 7)) << 4));
-                    mma_bf16_16816(s, k4[0], k4[1], k4[2], k4[3], qf[ks][0], qf[ks][1]);
-            }
-        } else if constexpr (FMT == W4_KV_INT8) {
+            for (int ks = 0; ks < 4; ++ks) {
+                const uint32_t at = row + (((2 * ks + hi) ^ x) << 4);
+                uint32_t k4[D / 64][4];
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                uint32_t w0[4], w1[4];
-                const int piece = D == 128 ? (4 * i + t) ^ ((g & 1) << 2) : t;
-                lds128(w0, rec + g * L::kRow + piece * 16);
-                lds128(w1, rec + (g + 8) * L::kRow + piece * 16);
+                for (int y = 0; y < D / 64; ++y) ldsm4(k4[y], at + 128 * y);
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t a0 = even(w0[w], zk[0]), a1 = even(w1[w], zk[1]);
-                    const uint32_t a2 = even(w0[w] >> 8, zk[0]), a3 = even(w1[w] >> 8, zk[1]);
-                        mma_f16_16816(s, a0, a1, a2, a3, qf[4 * i + w][0],
-                                      qf[4 * i + w][1]);
-                }
+                for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_bf16_16816(s[n], k4[y][0], k4[y][1], k4[y][2], k4[y][3],
+                                       qf[n][ks + 4 * y][0], qf[n][ks + 4 * y][1]);
             }
         } else {
-            uint32_t w0[D / 32], w1[D / 32];
-            if constexpr (D == 128) {
+            uint32_t w0[D * L::kBits / 128], w1[D * L::kBits / 128];   // keys g, g + 8
+            if constexpr (FMT == W4_KV_INT8) {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const int piece = D == 128 ? (4 * i + t) ^ ((g & 1) << 2) : t;
+                    lds128(w0 + 4 * i, rec + g * L::kRow + piece * 16);
+                    lds128(w1 + 4 * i, rec + (g + 8) * L::kRow + piece * 16);
+                }
+            } else if constexpr (D == 128) {
                 lds128(w0, rec + g * L::kRow + t * 16);
                 lds128(w1, rec + (g + 8) * L::kRow + t * 16);
             } else {
@@ -264,135 +277,219 @@ struct Tile {
                 lds64(w1, rec + (g + 8) * L::kRow + t * 8);
             }
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t x0 = ks & 1 ? w0[ks >> 1] >> 8 : w0[ks >> 1];
-                const uint32_t x1 = ks & 1 ? w1[ks >> 1] >> 8 : w1[ks >> 1];
-                const uint32_t a0 = low(x0, zk[0]), a1 = low(x1, zk[1]);
-                const uint32_t a2 = high(x0, zk16[0]), a3 = high(x1, zk16[1]);
-                    mma_f16_16816(s, a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
+            for (int r = 0; r < 2; ++r) {
+                mk[r] = lds32(rec + L::kMeta + 4 * (g + 8 * r));
+                mv[r] = lds32(rec + L::kMetaV + 4 * (g + 8 * r));
+                lds64(mt[r], rec + L::kMetaV + 4 * (2 * t + 8 * r));
             }
+            uint32_t zk[2], zk16[2];      // -(1024 + z), -(64 + z) of keys g, g + 8, twice each
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                zk[r] = __byte_perm(mk[r], 0u, 0x4242) | 0xE400E400u;
+                zk16[r] = half2_add(zk[r], 0x63806380u);  // + 960
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a0, a1, a2, a3;
+                if constexpr (FMT == W4_KV_INT8) {
+                    a0 = even(w0[ks], zk[0]), a1 = even(w1[ks], zk[1]);
+                    a2 = even(w0[ks] >> 8, zk[0]), a3 = even(w1[ks] >> 8, zk[1]);
+                } else {
+                    const uint32_t x0 = ks & 1 ? w0[ks >> 1] >> 8 : w0[ks >> 1];
+                    const uint32_t x1 = ks & 1 ? w1[ks >> 1] >> 8 : w1[ks >> 1];
+                    a0 = low(x0, zk[0]), a1 = low(x1, zk[1]);
+                    a2 = high(x0, zk16[0]), a3 = high(x1, zk16[1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_f16_16816(s[n], a0, a1, a2, a3, qf[n][ks][0], qf[n][ks][1]);
+            }
+        }
+        // the values are on their way during the softmax
+        if constexpr (FMT == W4_KV_BF16) {
+            load_values(vraw, rec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < L::kPart / 512; ++i)
+                lds128(vraw + 4 * i, rec + L::kPart + i * 512 + lane * 16);
         }
         // ---- scores in units of log2; quantised: with log2 s_v added
         float inv[2] = {1.f, 1.f};                        // 1 / s_v of keys g, g + 8
         if constexpr (FMT == W4_KV_BF16) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[c] *= sc[c & 1];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[n][c] *= sc[n][c & 1];
         } else {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint32_t mv = lds32(rec + L::kMetaV + 4 * (g + 8 * r));
                 const float sk =
                     __half2float(__ushort_as_half((unsigned short)(mk[r] & 0xFFFFu)));
                 // a value's scale of 0 goes with codes of 0: any factor does
                 const float sv = fmaxf(
-                    __half2float(__ushort_as_half((unsigned short)(mv & 0xFFFFu))), 0x1p-24f);
-                const float lv = __log2f(sv);
+                    __half2float(__ushort_as_half((unsigned short)(mv[r] & 0xFFFFu))), 0x1p-24f);
+                const float lv = log2_fast(sv);
                 inv[r] = exp2_fast(-lv);
 #pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        s[2 * r + c] = fmaf(s[2 * r + c], sk * sc[c], lv);
+                        s[n][2 * r + c] = fmaf(s[n][2 * r + c], sk * sc[n][c], lv);
             }
         }
-        uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;    // keys 2t, 2t+1; 2t+8, 2t+9
         bool apart = false;       // a key that some rows see and some do not
         if (edge) {
 #pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int row = row0 + 2 * t + (c & 1), j = j0 + g + (c & 2) * 4;
-                    const int last = len - a.tokens + min(row, rows - 1) / a.group;
-                    if (j > last || (a.window > 0 && j <= last - a.window)) s[c] = -INFINITY;
+                    const int j = j0 + g + (c & 2) * 4;
+                    const int last = len - a.tokens + token_of(a, n, c & 1, row0, rows);
+                    if (j > last || (a.window > 0 && j <= last - a.window)) s[n][c] = -INFINITY;
                 }
             if constexpr (FMT == W4_KV_BF16) {
                 // values of keys that no row sees must not meet the product
                 const int lo = a.window > 0 ? len - a.tokens - a.window : -1;
-                const auto seen = [&](int k) { return j0 + k < len && j0 + k > lo; };
-                keep0 = (seen(2 * t) ? 0xFFFFu : 0u) | (seen(2 * t + 1) ? 0xFFFF0000u : 0u);
-                keep1 = (seen(2 * t + 8) ? 0xFFFFu : 0u) | (seen(2 * t + 9) ? 0xFFFF0000u : 0u);
-                apart = a.tokens > 1;
+                uint32_t keep[2];
+                kept_keys(j0, lo, len - 1, keep);
+                bool finite = true;
+#pragma unroll
+                for (int x = 0; x < VREGS; ++x) {
+                    const uint32_t v = vraw[x] &= keep[(x >> 1) & 1];
+                    finite &= (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
+                }
+                apart = a.tokens > 1 && __any_sync(0xFFFFFFFFu, !finite);
             }
         }
         // ---- a reference near the maximum: moved only when a score passes it by kSlack
         bool over = false;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) over |= s[c] > m[c & 1] + kSlack;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                over |= fmaxf(s[n][c], s[n][c + 2]) > m[n][c] + kSlack;
         if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float top = fmaxf(s[c], s[c + 2]);
+                    float top = fmaxf(s[n][c], s[n][c + 2]);
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    const float now = fmaxf(m[c], top - kBias);
-                    const float f = exp2_fast(m[c] - now);
-                    m[c] = now;
-                    l[c] *= f;
+                    const float now = fmaxf(m[n][c], top - kBias);
+                    const float f = exp2_fast(m[n][c] - now);
+                    m[n][c] = now;
+                    l[n][c] *= f;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
-                        o[k][c] *= f;
-                        o[k][c + 2] *= f;
+                        o[n][k][c] *= f;
+                        o[n][k][c + 2] *= f;
                     }
                 }
         }
         // ---- probabilities, their sums, and P^T as the column operand
-        uint32_t p[2];
-        {
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                s[c] = exp2_fast(s[c] - m[c & 1]);
-                l[c & 1] = fmaf(s[c], inv[c >> 1], l[c & 1]);
+                s[n][c] = exp2_fast(s[n][c] - m[n][c & 1]);
+                l[n][c & 1] = fmaf(s[n][c], inv[c >> 1], l[n][c & 1]);
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                p[r] = transposed(FMT == W4_KV_BF16 ? pack_bf16(s[2 * r], s[2 * r + 1])
-                                                       : pack_half(s[2 * r], s[2 * r + 1]));
+                p[n][r] = transposed(FMT == W4_KV_BF16 ? pack_bf16(s[n][2 * r], s[n][2 * r + 1])
+                                                       : pack_half(s[n][2 * r], s[n][2 * r + 1]));
         }
         // ---- O^T += V^T P^T
         if constexpr (FMT == W4_KV_BF16) {
-            const int r = (lane >> 4) * 8 + (lane & 7), hi = (lane >> 3) & 1;
-            const uint32_t base = rec + L::kPart + r * L::kRow;
-            if (apart && __any_sync(0xFFFFFFFFu, !finite_values(base, r, hi, keep0, keep1))) {
-                tokens_apart(a, base, r, hi, j0, len, row0, rows, p);
+            if (apart) {
+                tokens_apart(a, vraw, j0, len, row0, rows, p);
                 return;
             }
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                uint32_t v4[4];
-                ldsm4_t(v4, base + (((2 * k + hi) ^ (r & 7)) << 4));
-                if (edge) v4[0] &= keep0, v4[1] &= keep0, v4[2] &= keep1, v4[3] &= keep1;
-                    mma_bf16_16816(o[k], v4[0], v4[1], v4[2], v4[3], p[0], p[1]);
-            }
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_bf16_16816(o[n][k], vraw[4 * k], vraw[4 * k + 1], vraw[4 * k + 2],
+                                   vraw[4 * k + 3], p[n][0], p[n][1]);
         } else {
-            uint32_t zlo[2], zhi[2];                      // minus (1024 + z), (64 + z)
+            uint32_t zlo[2], zhi[2];                      // -(1024 + z), -(64 + z)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                uint32_t mv[2];
-                lds64(mv, rec + L::kMetaV + 4 * (2 * t + 8 * r));
-                const uint32_t z = __byte_perm(mv[0], mv[1], 0x7632) & 0x00FF00FFu;
-                zlo[r] = z | 0xE400E400u;
-                zhi[r] = half2_add(zlo[r], 0x63806380u);  // + 960
+                zlo[r] = (__byte_perm(mt[r][0], mt[r][1], 0x7632) & 0x00FF00FFu) | 0xE400E400u;
+                zhi[r] = half2_add(zlo[r], 0x63806380u);
             }
 #pragma unroll
-            for (int i = 0; i < L::kPart / 512; ++i) {
-                uint32_t w[4];
-                lds128(w, rec + L::kPart + i * 512 + lane * 16);
+            for (int k = 0; k < KS; ++k) {
+                uint32_t a0, a1, a2, a3;
                 if constexpr (FMT == W4_KV_INT8) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t u = w[2 * x], v = w[2 * x + 1];
-                        const uint32_t a0 = even(u, zlo[0]), a1 = even(v, zlo[0]);
-                        const uint32_t a2 = even(u >> 8, zlo[1]), a3 = even(v >> 8, zlo[1]);
-                            mma_f16_16816(o[2 * i + x], a0, a1, a2, a3, p[0], p[1]);
-                    }
+                    const uint32_t u = vraw[2 * k], v = vraw[2 * k + 1];
+                    a0 = even(u, zlo[0]), a1 = even(v, zlo[0]);
+                    a2 = even(u >> 8, zlo[1]), a3 = even(v >> 8, zlo[1]);
                 } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t u = w[x], v = w[x] >> 8;
-                        const uint32_t a0 = low(u, zlo[0]), a1 = high(u, zhi[0]);
-                        const uint32_t a2 = low(v, zlo[1]), a3 = high(v, zhi[1]);
-                            mma_f16_16816(o[4 * i + x], a0, a1, a2, a3, p[0], p[1]);
-                    }
+                    const uint32_t u = vraw[k], v = vraw[k] >> 8;
+                    a0 = low(u, zlo[0]), a1 = high(u, zhi[0]);
+                    a2 = low(v, zlo[1]), a3 = high(v, zhi[1]);
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_f16_16816(o[n][k], a0, a1, a2, a3, p[n][0], p[n][1]);
             }
+        }
+    }
+
+    // bf16: all values of a record as the row operand.
+    __device__ __forceinline__ static void load_values(uint32_t (&v)[VREGS], uint32_t rec) {
+        const int lane = threadIdx.x & 31, x = lane & 7, hi = (lane >> 3) & 1;
+        const uint32_t row = rec + L::kPart + ((lane >> 4) * 8 + x) * L::kRow;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int y = 0; y < D / 64; ++y)
+                ldsm4_t(v + 4 * (k + 4 * y), row + (((2 * k + hi) ^ x) << 4) + 128 * y);
+    }
+
+    // New token of column 2t + c of tile n.
+    __device__ static int token_of(const AttnArgs &a, int n, int c, int row0, int rows) {
+        return min(row0 + 8 * n + 2 * ((int)threadIdx.x & 3) + c, rows - 1) / a.group;
+    }
+
+    // Masks of the keys 2t, 2t + 1 and 2t + 8, 2t + 9 of a record that lie in
+    // (lo, last].
+    __device__ static void kept_keys(int j0, int lo, int last, uint32_t (&keep)[2]) {
+        const int t = threadIdx.x & 3;
+        const auto seen = [&](int k) { return j0 + k <= last && j0 + k > lo; };
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            keep[r] = (seen(2 * t + 8 * r) ? 0xFFFFu : 0u) |
+                      (seen(2 * t + 8 * r + 1) ? 0xFFFF0000u : 0u);
+    }
+
+    // The second product where a value that is not finite lies among keys that
+    // some tokens see and others do not: 0 * inf would reach the rows that do
+    // not see it, so each token's rows get a product of their own over the
+    // keys that they see.
+    __device__ __forceinline__ void tokens_apart(const AttnArgs &a, const uint32_t (&v)[VREGS],
+                                              int j0, int len, int row0, int rows,
+                                              const uint32_t (&p)[NT][2]) {
+        for (int i = 0; i < a.tokens; ++i) {
+            const int last = len - a.tokens + i;
+            uint32_t keep[2];
+            kept_keys(j0, a.window > 0 ? last - a.window : -1, last, keep);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float d[4] = {o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]};
+                    mma_bf16_16816(d, v[4 * k] & keep[0], v[4 * k + 1] & keep[0],
+                                   v[4 * k + 2] & keep[1], v[4 * k + 3] & keep[1], p[n][0],
+                                   p[n][1]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (token_of(a, n, c & 1, row0, rows) == i) o[n][k][c] = d[c];
+                }
         }
     }
 
@@ -412,53 +509,6 @@ struct Tile {
         uint32_t r;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
         return r;
-    }
-
-    // Whether the kept values that this lane takes are all finite.
-    __device__ static bool finite_values(uint32_t base, int r, int hi, uint32_t keep0,
-                                         uint32_t keep1) {
-        bool ok = true;
-        for (int k = 0; k < KS; ++k) {
-            uint32_t v4[4];
-            ldsm4_t(v4, base + (((2 * k + hi) ^ (r & 7)) << 4));
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t v = v4[i] & (i < 2 ? keep0 : keep1);
-                ok &= (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
-            }
-        }
-        return ok;
-    }
-
-    // The second product where a value that is not finite lies among keys that
-    // some tokens see and others do not: 0 * inf would reach the rows that do
-    // not see it, so each token's rows get a product of their own over the
-    // keys that they see.
-    __device__ void tokens_apart(const AttnArgs &a, uint32_t base, int r, int hi, int j0, int len,
-                                 int row0, int rows, const uint32_t (&p)[2]) {
-        const int t = threadIdx.x & 3;
-        for (int i = 0; i < a.tokens; ++i) {
-            const int last = len - a.tokens + i, lo = a.window > 0 ? last - a.window : -1;
-            const auto seen = [&](int k) { return j0 + k <= last && j0 + k > lo; };
-            const uint32_t k0 =
-                (seen(2 * t) ? 0xFFFFu : 0u) | (seen(2 * t + 1) ? 0xFFFF0000u : 0u);
-            const uint32_t k1 =
-                (seen(2 * t + 8) ? 0xFFFFu : 0u) | (seen(2 * t + 9) ? 0xFFFF0000u : 0u);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                uint32_t v4[4];
-                ldsm4_t(v4, base + (((2 * k + hi) ^ (r & 7)) << 4));
-                {
-                    float d[4] = {o[k][0], o[k][1], o[k][2], o[k][3]};
-                    mma_bf16_16816(d, v4[0] & k0, v4[1] & k0, v4[2] & k1, v4[3] & k1, p[0],
-                                   p[1]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int row = row0 + 2 * t + (c & 1);
-                        if (min(row, rows - 1) / a.group == i) o[k][c] = d[c];
-                    }
-                }
-            }
-        }
     }
 };
 
@@ -493,384 +543,457 @@ __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) 
     o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
 }
 
-// A block's stretch of the list.
-struct Share {
-    int b;                 // sequence of the first piece
-    int item;              // head (x row tile) of the first piece in it
-    int u0;                // first record of that
-    long long units;       // records to go (over all pieces)
-    int parts;             // parts of every head, or 0: the stretch may cover several heads
-    int part;              // which of them this is
-    long long work;        // all records of the list
-    long long at;          // the stretch's start in the list
-    int blocks;            // blocks that have a stretch
+// Start of stretch c of `work` records over `blocks` blocks.
+__device__ __forceinline__ int stretch(int work, int blocks, int c) {
+    const int q = work / blocks;
+    return q * c + (int)((unsigned)(work - q * blocks) * (unsigned)c / (unsigned)blocks);
+}
+
+// A place in the list of records (the host refuses lists of 2^31).
+struct Cut {
+    int b, item, u;        // sequence, head (x row tile) of it, record of that
 };
 
-// Every warp works it out for itself, without a barrier.  false: nothing to do.
-__device__ bool share_of(const AttnArgs &a, int row_tiles, int least, Share *s) {
-    const int lane = threadIdx.x & 31, per_seq = a.pool.kv_heads * row_tiles;
-    const int each = (a.pool.seqs + 31) / 32;
-    const int b0 = min(lane * each, a.pool.seqs), b1 = min(b0 + each, a.pool.seqs);
-    const int grid = (int)gridDim.x;
-    long long mine = 0;
-    int longest = 0;
+// The list, as a warp sees it: lane i holds sequences [b0, b1), their items'
+// records are [before, before + mine) * per_seq.
+struct List {
+    int b0, b1, before, mine, per_seq, work;
+
+    __device__ __forceinline__ List(const AttnArgs &a, int row_tiles) {
+        const int lane = threadIdx.x & 31, each = (a.pool.seqs + 31) / 32;
+        per_seq = a.pool.kv_heads * row_tiles;
+        b0 = min(lane * each, a.pool.seqs), b1 = min(b0 + each, a.pool.seqs);
+        mine = 0;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) {
-        const int n = max(sequence(a, b).records, 1);
-        mine += n;
-        longest = max(longest, n);
-    }
-    long long upto = mine;                                    // inclusive scan
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, x);
-        if (lane >= x) upto += v;
-    }
-    s->work = __shfl_sync(0xFFFFFFFFu, upto, 31) * per_seq;
-    if ((long long)a.pool.seqs * per_seq * 2 <= grid) {
-        // parts of at most `size` records, the smallest that fit the grid
-        longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-        int size = max(least, (int)((s->work + grid - 1) / grid));
-        int cuts, before;
-        while (true) {
-            cuts = 0;
-            for (int b = b0; b < b1; ++b)
-                cuts += (max(sequence(a, b).records, 1) + size - 1) / size;
-            before = cuts;
+        for (int b = b0; b < b1; ++b) mine += max(sequence(a, b).records, 1);
+        int upto = mine;
+        if (a.pool.seqs > 1) {
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, before, x);
-                if (lane >= x) before += v;
+                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, x);
+                if (lane >= x) upto += v;
             }
-            if (__shfl_sync(0xFFFFFFFFu, before, 31) * per_seq <= grid || size >= longest) break;
-            size += max(1, size / 8);
         }
-        const int c = blockIdx.x;
-        before = (before - cuts) * per_seq;                   // parts before this lane's
-        const bool here = c >= before && c < before + cuts * per_seq;
-        int b = b0, parts = 1, n = 1;
+        before = upto - mine;
+        work = __shfl_sync(0xFFFFFFFFu, upto, a.pool.seqs > 1 ? 31 : 0) * per_seq;
+    }
+
+    // Place of record u of the list, moved to its head's border where fewer
+    // than `least` records would be cut off.
+    __device__ __forceinline__ Cut cut(const AttnArgs &a, int u, int least) const {
+        const bool here = u >= before * per_seq && u < (before + mine) * per_seq;
+        int b = b0, n = 1, in = u - before * per_seq;
         if (here)
             for (;; ++b) {
                 n = max(sequence(a, b).records, 1);
-                parts = (n + size - 1) / size;
-                if (c < before + parts * per_seq) break;
-                before += parts * per_seq;
+                if (in < n * per_seq) break;
+                in -= n * per_seq;
             }
         const unsigned found = __ballot_sync(0xFFFFFFFFu, here);
-        if (!found) return false;
-        const int src = __ffs(found) - 1;
-        s->b = __shfl_sync(0xFFFFFFFFu, b, src);
-        s->parts = __shfl_sync(0xFFFFFFFFu, parts, src);
+        const int src = found ? __ffs(found) - 1 : 0;
+        Cut c;
+        c.b = __shfl_sync(0xFFFFFFFFu, b, src);
         n = __shfl_sync(0xFFFFFFFFu, n, src);
-        const int in = c - __shfl_sync(0xFFFFFFFFu, before, src);
-        s->item = in / s->parts;
-        s->part = in - s->item * s->parts;
-        s->u0 = (int)((long long)n * s->part / s->parts);
-        s->units = (long long)n * (s->part + 1) / s->parts - s->u0;
-        s->at = 0;
-        s->blocks = grid;
-        return true;
-    }
-    s->parts = s->part = 0;
-    s->blocks = (int)min((long long)grid, s->work);
-    if ((int)blockIdx.x >= s->blocks) return false;
-    s->at = s->work * blockIdx.x / s->blocks;
-    s->units = s->work * (blockIdx.x + 1) / s->blocks - s->at;
-    long long before = (upto - mine) * per_seq;
-    const bool here = s->at >= before && s->at < upto * per_seq;
-    int b = b0, n = 1;
-    if (here)
-        for (;; ++b) {
-            n = max(sequence(a, b).records, 1);
-            if (s->at < before + (long long)n * per_seq) break;
-            before += (long long)n * per_seq;
+        in = __shfl_sync(0xFFFFFFFFu, in, src);
+        if (!found) {                                         // the list's end
+            c.b = a.pool.seqs, c.item = 0, c.u = 0;
+            return c;
         }
-    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
-    s->b = __shfl_sync(0xFFFFFFFFu, b, src);
-    n = __shfl_sync(0xFFFFFFFFu, n, src);
-    const long long in = s->at - __shfl_sync(0xFFFFFFFFu, before, src);
-    s->item = (int)(in / n);
-    s->u0 = (int)(in - (long long)s->item * n);
-    return true;
+        c.item = in / n;
+        c.u = in - c.item * n;
+        if (c.u < least || n - c.u < least) {
+            if (2 * c.u > n && ++c.item == per_seq) c.item = 0, ++c.b;
+            c.u = 0;
+        }
+        return c;
+    }
+};
+
+// Barrier over the warps that compute.
+template <int WARPS>
+__device__ __forceinline__ void warps_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
 // The block that finished a head last joins its n pieces, those of blocks c0 ..
-// c0 + n - 1, in that order.  buf: the ring's shared memory.
-template <int D>
-__device__ void join_pieces(const AttnArgs &a, int c0, int n, int b, int h, int tile0, int rows,
-                            int block_rows, float *buf) {
+// c0 + n - 1, in that order.
+template <int D, int WARPS>
+__device__ __forceinline__ void join_pieces(const AttnArgs &a, int c0, int n, int b, int h,
+                                         int tile0, int there, float *buf) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int there = min(block_rows, rows - tile0);
-    float *fac = buf, *mx = buf + n * kRowsMax, *sum = mx + kRowsMax, *half = sum + kRowsMax;
-    for (int r = warp; r < there; r += kAttnWarps) {          // a warp per row: factors
-        float m = kNone;
-        for (int c = lane; c < n; c += 32)
-            m = fmaxf(m, __ldcg(&slot_of<D>(a, c0 + c, c == 0)[kRowsMax * D + r]));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-        float l = 0.f;
-        for (int c = lane; c < n; c += 32) {
-            const float *s = slot_of<D>(a, c0 + c, c == 0);
-            const float f = exp2_fast(__ldcg(&s[kRowsMax * D + r]) - m);
-            fac[c * kRowsMax + r] = f;
-            l = fmaf(f, __ldcg(&s[kRowsMax * D + kRowsMax + r]), l);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
-        if (lane == 0) mx[r] = m, sum[r] = l;
-    }
-    __syncthreads();
-    // two threads per 4 values take every other piece
+    // a thread takes 4 values; its first loads are under way while the factors
+    // are worked out
+    constexpr int THREADS = 32 * WARPS, AHEAD = 20;
+    float *fac = buf, *mx = buf + n * there, *sum = mx + kRowsMax;
     const int values = there * (D / 4);
-    for (int e0 = 0; e0 < values; e0 += kAttnThreads / 2) {
-        const int e = e0 + (tid & (kAttnThreads / 2 - 1)), side = tid / (kAttnThreads / 2);
-        const int r = e / (D / 4), d = e % (D / 4) * 4;
+    const auto piece = [&](int e, int c) {
+        return __ldcg(reinterpret_cast<const float4 *>(
+            &slot_of<D>(a, c0 + c, c == 0)[e / (D / 4) * D + e % (D / 4) * 4]));
+    };
+    float4 early[AHEAD];
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x)
+        early[x] = tid < values && x < n ? piece(tid, x) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = warp; r < there; r += WARPS) {               // a warp per row: factors
+        float m = kNone, l = 0.f, m1 = kNone, l1 = 0.f;       // the first 64 stay in registers
+        const float *s = slot_of<D>(a, c0 + lane, lane == 0) + kRowsMax * D + r;
+        const float *s1 = slot_of<D>(a, c0 + lane + 32, false) + kRowsMax * D + r;
+        if (lane < n) m = __ldcg(s), l = __ldcg(s + kRowsMax);
+        if (lane + 32 < n) m1 = __ldcg(s1), l1 = __ldcg(s1 + kRowsMax);
+        float top = fmaxf(m, m1);
+        for (int c = lane + 64; c < n; c += 32)
+            top = fmaxf(top, __ldcg(slot_of<D>(a, c0 + c, false) + kRowsMax * D + r));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        const float f = exp2_fast(m - top), f1 = exp2_fast(m1 - top);
+        float total = fmaf(f, l, f1 * l1);
+        if (lane < n) fac[lane * there + r] = f;
+        if (lane + 32 < n) fac[(lane + 32) * there + r] = f1;
+        for (int c = lane + 64; c < n; c += 32) {
+            const float *s2 = slot_of<D>(a, c0 + c, false) + kRowsMax * D + r;
+            const float f2 = exp2_fast(__ldcg(s2) - top);
+            fac[c * there + r] = f2;
+            total = fmaf(f2, __ldcg(s2 + kRowsMax), total);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
+        if (lane == 0) mx[r] = top, sum[r] = total;
+    }
+    warps_sync<WARPS>();
+    for (int e = tid; e < values; e += THREADS) {
+        const int r = e / (D / 4);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e < values) {
-#pragma unroll 8
-            for (int c = side; c < n; c += 2)
-                add_scaled(o, fac[c * kRowsMax + r],
-                           __ldcg(reinterpret_cast<const float4 *>(
-                               &slot_of<D>(a, c0 + c, c == 0)[r * D + d])));
+        if (e >= THREADS) {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x)
+                if (x < n) early[x] = piece(e, x);
         }
-        float4 *other = reinterpret_cast<float4 *>(half) + (tid & (kAttnThreads / 2 - 1));
-        if (side) *other = o;
-        __syncthreads();
-        if (!side && e < values) {
-            add_scaled(o, 1.f, *other);
-            store_row(a, b, h, tile0 + r, d, o, mx[r], sum[r]);
-        }
-        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x)
+            if (x < n) add_scaled(o, fac[x * there + r], early[x]);
+#pragma unroll 16
+        for (int c = AHEAD; c < n; ++c) add_scaled(o, fac[c * there + r], piece(e, c));
+        store_row(a, b, h, tile0 + r, e % (D / 4) * 4, o, mx[r], sum[r]);
     }
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kAttnThreads, 1)
-attn_kernel(const AttnArgs a, const int row_tiles, const int QG, const int KG, const int stages) {
+// Warps that compute: with the one that copies 16 of 128 registers, or 12 of 168.
+template <int NT>
+__host__ __device__ constexpr int compute_warps() {
+    return NT == 1 ? 15 : 11;
+}
+
+// How a launch divides a block (host).
+struct Plan {
+    int row_tiles;     // blocks of rows per key/value head
+    int QG, KG;        // warps on a record, groups of them
+    int stages;        // records of a group's ring
+    int ring_bytes;    // of all rings
+};
+
+// A stretch's part of one head, as the copying warp tells the others.
+struct Piece {
+    int b;             // sequence; -1: no more pieces
+    int h, tile0;      // key/value head, first row
+    int u0, stop;      // records u0 .. stop - 1, from the sequence's first visible one
+    int len;
+    int whole;         // the head is not cut
+    int starts;        // the piece starts the head
+    int c0, pieces;    // cut: the head's first block, and how many pieces it has
+};
+
+// The copying warp: lane kg fills the ring of group kg.
+template <int FMT, int D, int WARPS>
+__device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan, int block_rows,
+                                             unsigned char *smem, uint64_t *full, uint64_t *empty,
+                                             int *first_key, Piece *piece, uint64_t *piece_full,
+                                             uint64_t *piece_empty) {
+    using L = KvLayout<FMT, D>;
+    const int lane = threadIdx.x & 31, KG = plan.KG, stages = plan.stages;
+    const List list(a, plan.row_tiles);
+    const int per_seq = list.per_seq;
+    // every head a block of its own while there are blocks, else parts of at
+    // least 4 records a group
+    const int blocks = min(min((int)gridDim.x, list.work),
+                           max(a.pool.seqs * per_seq, list.work / (4 * KG)));
+    const int least = min(4 * KG, max(KG, list.work / blocks / 8));
+    Cut c, to;
+    c.b = 0, c.item = 0, c.u = 0;
+    to = c;
+    if ((int)blockIdx.x < blocks) {
+        c = list.cut(a, stretch(list.work, blocks, blockIdx.x), least);
+        to = list.cut(a, stretch(list.work, blocks, blockIdx.x + 1), least);
+    }
+    int put = 0, used = 0, told = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    uint64_t *my_full = full + lane * stages, *my_empty = empty + lane * stages;
+    unsigned char *ring = smem + lane * stages * L::kBytes;
+    while (true) {
+        const bool more = c.b < to.b || c.item < to.item || c.u < to.u;
+        const Seq seq = sequence(a, more ? c.b : 0);
+        const int n_seq = max(seq.records, 1);
+        const bool last = c.b == to.b && c.item == to.item;
+        const int u1 = last ? to.u : n_seq, stop = min(u1, seq.records);
+        const int h = c.item / plan.row_tiles;
+        Piece p;
+        p.b = more ? c.b : -1;
+        p.h = h, p.tile0 = (c.item - h * plan.row_tiles) * block_rows;
+        p.u0 = c.u, p.stop = stop, p.len = seq.len;
+        p.whole = c.u == 0 && u1 == n_seq, p.starts = c.u == 0;
+        p.c0 = p.pieces = 0;
+        if (more && !p.whole) {
+            // the cuts inside this head, at least `least` records from its borders
+            const bool mine = c.b >= list.b0 && c.b < list.b1;
+            int head = list.before * per_seq + c.item * n_seq;
+            if (mine)
+                for (int x = list.b0; x < c.b; ++x)
+                    head += max(sequence(a, x).records, 1) * per_seq;
+            head = __shfl_sync(0xFFFFFFFFu, head, __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1);
+            const int lo = head + least, hi = head + n_seq - least;
+            int c_lo = (int)((long long)lo * blocks / list.work);
+            while (c_lo > 0 && stretch(list.work, blocks, c_lo) >= lo) --c_lo;
+            while (stretch(list.work, blocks, c_lo) < lo) ++c_lo;
+            int c_hi = (int)((long long)hi * blocks / list.work) + 1;
+            while (stretch(list.work, blocks, c_hi) > hi) --c_hi;
+            p.c0 = c_lo - 1, p.pieces = c_hi - c_lo + 2;
+        }
+        // tell the others, two pieces ahead at most
+        const int slot = told & 1;
+        if (told >= 2) mbar_wait(&piece_empty[slot], (told >> 1) + 1 & 1);
+        if (lane == 0) {
+            piece[slot] = p;
+            mbar_arrive(&piece_full[slot]);
+        }
+        ++told;
+        if (!more) break;
+
+        const int32_t *pages = a.pool.table + c.b * a.pool.stride;
+        constexpr int AHEAD = 4;
+        int page[AHEAD];
+        const auto fetch = [&](int x, int u) {
+            page[x] = u < stop && lane < KG ? pages[page_slot(a.pool, seq.first + u)] : 0;
+        };
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) fetch(x, c.u + lane + x * KG);
+        for (int u0 = c.u; u0 < stop; u0 += AHEAD * KG)
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                const int u = u0 + lane + x * KG, r = seq.first + u, pg = page[x];
+                fetch(x, u + AHEAD * KG);
+                if (lane >= KG || u >= stop || !ok) continue;
+                if (used >= stages) {
+                    ok = mbar_wait(&my_empty[put], phase);
+                    if (!ok) {                                // never in normal operation
+                        if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
+                        continue;
+                    }
+                    fence_proxy_async();
+                }
+                const bool valid = pg >= 0 && pg < a.pool.pages;
+                first_key[lane * stages + put] = valid ? r * kRecTokens : -1;
+                if (valid) {
+                    const char *src =
+                        a.pool.records +
+                        (((long long)pg * a.pool.kv_heads + h) * a.pool.page_records + r -
+                         page_slot(a.pool, r) * a.pool.page_records) * L::kBytes;
+                    mbar_expect_tx(&my_full[put], L::kBytes);
+                    bulk_g2s(ring + put * L::kBytes, src, L::kBytes, &my_full[put]);
+                } else {
+                    if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_PAGE);
+                    mbar_arrive(&my_full[put]);
+                }
+                used = min(used + 1, stages);
+                if (++put == stages) put = 0, phase ^= 1;
+            }
+        __syncwarp();
+        if (last) {
+            c = to;
+        } else {
+            c.u = 0;
+            if (++c.item == per_seq) c.item = 0, ++c.b;
+        }
+    }
+    // nothing of the block's own is under way when it ends
+    phase ^= 1;
+    for (int x = 0; x < used; ++x) {
+        if (--put < 0) put = stages - 1, phase ^= 1;
+        mbar_wait(&my_full[put], phase);
+    }
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(32 * (compute_warps<NT>() + 1), 1)
+attn_kernel(const AttnArgs a, const Plan plan) {
     extern __shared__ __align__(128) unsigned char smem[];
     using L = KvLayout<FMT, D>;
+    constexpr int WARPS = compute_warps<NT>();
     constexpr int OROW = D + 4;                               // floats; + 4: no bank conflicts
-    __shared__ uint64_t full[kAttnWarps * kMaxStages], empty[kAttnWarps * kMaxStages];
-    __shared__ float join_m[kAttnWarps * 8], join_l[kAttnWarps * 8];
+    __shared__ uint64_t full[kMaxWarps * kMaxStages], empty[kMaxWarps * kMaxStages];
+    __shared__ uint64_t piece_full[2], piece_empty[2];
+    __shared__ int first_key[kMaxWarps * kMaxStages];         // of a stage's record; -1: no page
+    __shared__ float join_m[kMaxWarps * 8 * NT], join_l[kMaxWarps * 8 * NT];
+    __shared__ Piece piece[2];
     __shared__ int is_last;
-    float *join_o = reinterpret_cast<float *>(smem);
+    const int block_rows = 8 * NT * plan.QG;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int kg = warp / QG, qg = warp - kg * QG;
-    const bool works = kg < KG;                               // QG may not divide 16
-    const int block_rows = 8 * QG;
-    for (int i = tid; i < KG * stages; i += kAttnThreads) {
+    for (int i = tid; i < plan.KG * plan.stages; i += 32 * (WARPS + 1)) {
         mbar_init(&full[i], 1);
-        mbar_init(&empty[i], QG);
+        mbar_init(&empty[i], plan.QG);
+    }
+    if (tid < 2) {
+        mbar_init(&piece_full[tid], 1);
+        mbar_init(&piece_empty[tid], WARPS);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     begin_after_previous();
+    if (warp == WARPS) {
+        copy_records<FMT, D, WARPS>(a, plan, block_rows, smem, full, empty, first_key, piece,
+                                    piece_full, piece_empty);
+        return;
+    }
 
-    Share share;
-    if (!share_of(a, row_tiles, 4 * KG, &share)) return;
-    const int rows = a.tokens * a.group, per_seq = a.pool.kv_heads * row_tiles;
-    const uint32_t ring = smem_addr(smem) + kg * stages * L::kBytes;
-    unsigned char *ring_ptr = smem + kg * stages * L::kBytes;
-    uint64_t *my_full = full + kg * stages, *my_empty = empty + kg * stages;
-    int get = 0, put = 0;                                     // stages next taken and filled
-    uint32_t get_phase = 0;
+    const int kg = warp / plan.QG, qg = warp - kg * plan.QG;
+    const bool works = kg < plan.KG;                          // QG may not divide WARPS
+    const uint32_t ring = smem_addr(smem) + kg * plan.stages * L::kBytes;
+    int get = 0;
+    uint32_t phase = 0;
     bool failed = false;
-    Tile<FMT, D> w;
-    int b = share.b, item = share.item, u0 = share.u0;
-    long long at = share.at;
-    while (share.units > 0) {
-        const Seq seq = sequence(a, b);
-        const int n_seq = max(seq.records, 1);
-        const int u1 = (int)min((long long)n_seq, u0 + share.units);
-        const int h = item / row_tiles, tile0 = (item - h * row_tiles) * block_rows;
-        const int row0 = tile0 + qg * 8;
-        // records u0 + kg, u0 + kg + KG, ... of this piece
-        const int stop = min(u1, seq.records);
-        const int n = works && stop > u0 + kg && !failed ? (stop - u0 - kg + KG - 1) / KG : 0;
-        const int rec0 = seq.first + u0 + kg;
-        const int32_t *pages = a.pool.table + b * a.pool.stride;
-        const auto page_at = [&](int i) {
-            if (i >= n) return -1;
-            const int page = pages[(rec0 + i * KG) / a.pool.page_records];
-            return page >= 0 && page < a.pool.pages ? page : -1;
-        };
-        int here = page_at(lane), next = page_at(32 + lane);
-        int batch = 0;                                        // here holds records 32 batch ..
-        const auto page_of = [&](int i) {
-            return __shfl_sync(0xFFFFFFFFu, (i >> 5) == batch ? here : next, i & 31);
-        };
-        // all lanes call; lane 0 of the group's first warp copies record i
-        const auto request = [&](int i) {
-            const int page = page_of(i);
-            if (qg == 0 && lane == 0) {
-                if (page < 0) {
-                    mbar_arrive(&my_full[put]);
-                    if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_PAGE);
-                } else {
-                    const int r = rec0 + i * KG;
-                    const char *src =
-                        a.pool.records +
-                        (((long long)page * a.pool.kv_heads + h) * a.pool.page_records +
-                         r % a.pool.page_records) * L::kBytes;
-                    mbar_expect_tx(&my_full[put], L::kBytes);
-                    bulk_g2s(ring_ptr + put * L::kBytes, src, L::kBytes, &my_full[put]);
+    Tile<FMT, D, NT> w;
+    for (int told = 0;; ++told) {
+        const Piece &p = piece[told & 1];
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&piece_full[told & 1], (told >> 1) & 1))) {
+            if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
+            return;                                           // every warp does
+        }
+        if (p.b < 0) return;
+        if (works) {
+            const int rows = a.tokens * a.group, row0 = p.tile0 + qg * 8 * NT;
+            w.load_q(a, p.b, p.h, row0, rows);
+            w.clear();
+            // every row sees all keys of [seen0, seen1)
+            const int len = p.len, seen1 = len - a.tokens + 1;
+            const int seen0 = a.window > 0 ? len - a.window : 0;
+            uint64_t *my_full = full + kg * plan.stages, *my_empty = empty + kg * plan.stages;
+            for (int u = p.u0 + kg; u < p.stop && !failed; u += plan.KG) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&my_full[get], phase))) {
+                    failed = true;                            // never in normal operation
+                    if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
+                    break;
                 }
-            }
-            if (++put == stages) put = 0;
-        };
-        if (qg == 0 && lane == 0) fence_proxy_async();
-        for (int i = 0; i < min(n, stages); ++i) request(i);
-        if (works) w.load_q(a, b, h, row0, rows);
-        w.clear();
-        int prev = 0;
-        uint32_t prev_phase = 0;
-        for (int i = 0; i < n; ++i) {
-            if ((i & 31) == 0 && i) {
-                here = next;
-                batch = i >> 5;
-                next = page_at(i + 32 + lane);
-            }
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&my_full[get], get_phase))) {
-                // never in normal operation: give up, after a bounded wait for
-                // what is still under way
-                failed = true;
-                if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
-                for (int x = 1; x < stages && i + x < n; ++x) {
-                    if (++get == stages) get = 0, get_phase ^= 1;
-                    mbar_wait(&my_full[get], get_phase);
-                }
-                break;
-            }
-            const int j0 = (rec0 + i * KG) * kRecTokens;
-            const bool edge = j0 + kRecTokens > seq.len - a.tokens + 1 ||
-                              (a.window > 0 && j0 < seq.len - a.window);
-            if (page_of(i) >= 0)
-                w.record(a, ring + get * L::kBytes, j0, edge, seq.len, row0, rows);
-            __syncwarp();
-            if (QG == 1) {
-                if (i + stages < n) {
-                    if (lane == 0) fence_proxy_async();
-                    request(i + stages);
-                }
-            } else {
+                const int j0 = first_key[kg * plan.stages + get];
+                if (j0 >= 0)
+                    w.record(a, ring + get * L::kBytes, j0, j0 + kRecTokens > seen1 || j0 < seen0,
+                             len, row0, rows);
+                __syncwarp();
                 if (lane == 0) mbar_arrive(&my_empty[get]);
-                // refill the stage of the record before: the others are done
-                // with it, or soon will be
-                if (i > 0 && i - 1 + stages < n) {
-                    // (a wait that gives up leaves the stage alone: the wait
-                    // for its next record then gives up too)
-                    if (qg != 0 ||
-                        __all_sync(0xFFFFFFFFu, mbar_wait(&my_empty[prev], prev_phase))) {
-                        if (qg == 0 && lane == 0) fence_proxy_async();
-                        request(i - 1 + stages);
-                    }
-                }
+                if (++get == plan.stages) get = 0, phase ^= 1;
             }
-            prev = get, prev_phase = get_phase;
-            if (++get == stages) get = 0, get_phase ^= 1;
         }
 
         // ---- join the groups of warps through shared memory
-        __syncthreads();
+        float *join_o = reinterpret_cast<float *>(smem + plan.ring_bytes);
         if (works) {
-            const int g = lane >> 2, t = lane & 3, r = kg * block_rows + qg * 8 + 2 * t;
+            const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float l = w.l[c];
+            for (int n = 0; n < NT; ++n) {
+                const int r = kg * block_rows + qg * 8 * NT + 8 * n + 2 * t;
 #pragma unroll
-                for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
-                if (g == 0) join_m[r + c] = w.m[c], join_l[r + c] = l;
+                for (int x = 0; x < 2; ++x) {
+                    float l = w.l[n][x];
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
+                    if (g == 0) join_m[r + x] = w.m[n][x], join_l[r + x] = l;
+                }
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        join_o[(r + (x & 1)) * OROW + 16 * k + g + (x & 2) * 4] = w.o[n][k][x];
             }
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    join_o[(r + (c & 1)) * OROW + 16 * k + g + (c & 2) * 4] = w.o[k][c];
         }
-        __syncthreads();
-        const bool whole = u0 == 0 && u1 == n_seq;
-        float *slot = slot_of<D>(a, blockIdx.x, u0 == 0);
-        for (int e = tid; e < block_rows * (D / 4); e += kAttnThreads) {
+        warps_sync<WARPS>();
+        const int there = min(block_rows, a.tokens * a.group - p.tile0);
+        float *slot = slot_of<D>(a, blockIdx.x, p.starts);
+        for (int e = tid; e < there * (D / 4); e += 32 * WARPS) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
-            if (tile0 + r >= rows) continue;
-            float m = join_m[r];
-            for (int k = 1; k < KG; ++k) m = fmaxf(m, join_m[k * block_rows + r]);
-            float l = 0.f;
+            float m = kNone, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < KG; ++k) {
-                const int at = k * block_rows + r;
-                const float f = exp2_fast(join_m[at] - m);
-                l = fmaf(f, join_l[at], l);
-                add_scaled(o, f, *reinterpret_cast<const float4 *>(&join_o[at * OROW + d]));
+            float mk[WARPS];
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) {
+                mk[k] = k < plan.KG ? join_m[k * block_rows + r] : kNone;
+                m = fmaxf(m, mk[k]);
             }
-            if (whole) {
-                store_row(a, b, h, tile0 + r, d, o, m, l);
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k)
+                if (k < plan.KG) {
+                    const int at = k * block_rows + r;
+                    const float f = exp2_fast(mk[k] - m);
+                    l = fmaf(f, join_l[at], l);
+                    add_scaled(o, f, *reinterpret_cast<const float4 *>(&join_o[at * OROW + d]));
+                }
+            if (p.whole) {
+                store_row(a, p.b, p.h, p.tile0 + r, d, o, m, l);
             } else {
                 *reinterpret_cast<float4 *>(&slot[r * D + d]) = o;
                 if (d == 0) slot[kRowsMax * D + r] = m, slot[kRowsMax * D + kRowsMax + r] = l;
             }
         }
-        if (!whole) {
-            int c0, pieces;
-            if (share.parts) {
-                c0 = blockIdx.x - share.part;
-                pieces = share.parts;
-            } else {
-                // the blocks whose stretches hold the head's first and last record
-                const long long first = at - u0, last = first + n_seq - 1;
-                const auto owner = [&](long long u) {
-                    int c = (int)(u * share.blocks / share.work);
-                    while (share.work * (c + 1) / share.blocks <= u) ++c;
-                    while (share.work * c / share.blocks > u) --c;
-                    return c;
-                };
-                c0 = owner(first);
-                pieces = owner(last) - c0 + 1;
-            }
-            uint32_t *counter = static_cast<uint32_t *>(a.workspace) + c0;
+        if (!p.whole) {
+            uint32_t *counter = static_cast<uint32_t *>(a.workspace) + p.c0;
             __threadfence();
-            __syncthreads();
-            if (tid == 0) is_last = atomicAdd(counter, 1u) == (uint32_t)(pieces - 1);
-            __syncthreads();
+            warps_sync<WARPS>();
+            if (tid == 0) is_last = atomicAdd(counter, 1u) == (uint32_t)(p.pieces - 1);
+            warps_sync<WARPS>();
             if (is_last) {
                 __threadfence();
                 if (tid == 0) *counter = 0u;
-                join_pieces<D>(a, c0, pieces, b, h, tile0, rows, block_rows, join_o);
+                join_pieces<D, WARPS>(a, p.c0, p.pieces, p.b, p.h, p.tile0, there, join_o);
             }
         }
-        __syncthreads();                                      // the ring's memory is free again
-        at += u1 - u0;
-        share.units -= u1 - u0;
-        u0 = 0;
-        if (u1 == n_seq && ++item == per_seq) item = 0, ++b;
+        warps_sync<WARPS>();                                  // the join's memory is free again
+        if (lane == 0) mbar_arrive(&piece_empty[told & 1]);
     }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    constexpr int bytes = KvLayout<FMT, D>::kBytes;
+    constexpr int bytes = KvLayout<FMT, D>::kBytes, WARPS = compute_warps<NT>();
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kRingBytes);
+        e = cudaFuncSetAttribute(attn_kernel<FMT, D, NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
     }
-    const int tiles = (a.tokens * a.group + 7) / 8, row_tiles = (tiles + 7) / 8;
-    const int QG = (tiles + row_tiles - 1) / row_tiles;
-    // groups of at least three stages (64-KB rings of bf16 records: 8 groups)
-    const int most = kRingBytes / (3 * bytes);
-    const int KG = kAttnWarps / QG < most ? kAttnWarps / QG : most;
-    int stages = kRingBytes / (KG * bytes);
-    if (stages > kMaxStages) stages = kMaxStages;
+    const int tiles = (a.tokens * a.group + 8 * NT - 1) / (8 * NT), most = kRowsMax / (8 * NT);
+    Plan p;
+    p.row_tiles = (tiles + most - 1) / most;
+    p.QG = (tiles + p.row_tiles - 1) / p.row_tiles;
+    // groups: as many as the warps allow with two records in a ring, three of
+    // the 8 KB of bf16 ones (with two, HBM was 9 % slower)
+    const int join_row = 8 * NT * p.QG * (D + 4) * 4, deep = bytes > 4224 ? 3 : 2;
+    p.KG = WARPS / p.QG;
+    while (p.KG > 1 && p.KG * (join_row + deep * bytes) > kSharedBytes) --p.KG;
+    p.stages = (kSharedBytes - p.KG * join_row) / (p.KG * bytes);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.ring_bytes = p.KG * p.stages * bytes;
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    return launch_overlapped(attn_kernel<FMT, D>, dim3(grid), dim3(kAttnThreads), kRingBytes,
-                             stream, a, row_tiles, QG, KG, stages);
+    return launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + 1)),
+                             kSharedBytes, stream, a, p);
+}
+
+// Two tiles a warp from 9 rows on: the operands of a record serve both.
+template <int FMT, int D>
+cudaError_t launch_rows(const AttnArgs &a, int num_sms, cudaStream_t stream) {
+    return a.tokens * a.group <= 8 ? launch<FMT, D, 1>(a, num_sms, stream)
+                                   : launch<FMT, D, 2>(a, num_sms, stream);
 }
 
 }  // namespace
@@ -883,12 +1006,12 @@ size_t attn_workspace_bytes(int head_dim, int num_sms) {
 cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, int num_sms,
                               cudaStream_t stream) {
     if (head_dim == 128)
-        return format == W4_KV_BF16   ? launch<W4_KV_BF16, 128>(a, num_sms, stream)
-               : format == W4_KV_INT8 ? launch<W4_KV_INT8, 128>(a, num_sms, stream)
-                                      : launch<W4_KV_INT4, 128>(a, num_sms, stream);
-    return format == W4_KV_BF16   ? launch<W4_KV_BF16, 64>(a, num_sms, stream)
-           : format == W4_KV_INT8 ? launch<W4_KV_INT8, 64>(a, num_sms, stream)
-                                  : launch<W4_KV_INT4, 64>(a, num_sms, stream);
+        return format == W4_KV_BF16   ? launch_rows<W4_KV_BF16, 128>(a, num_sms, stream)
+               : format == W4_KV_INT8 ? launch_rows<W4_KV_INT8, 128>(a, num_sms, stream)
+                                      : launch_rows<W4_KV_INT4, 128>(a, num_sms, stream);
+    return format == W4_KV_BF16   ? launch_rows<W4_KV_BF16, 64>(a, num_sms, stream)
+           : format == W4_KV_INT8 ? launch_rows<W4_KV_INT8, 64>(a, num_sms, stream)
+                                  : launch_rows<W4_KV_INT4, 64>(a, num_sms, stream);
 }
 
 }  // namespace w4
