@@ -45,6 +45,7 @@ constexpr int kRowsMax = 64;           // rows of a block
 constexpr int kMaxWarps = 16;          // warps that compute
 constexpr int kMaxStages = 16;         // of one group's ring
 constexpr int kMaxGrid = 256;
+constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not there: past any length
 constexpr int kSharedBytes = 224256;   // rings and join: 219 of the 227 KB of a block
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen no key
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -126,7 +127,6 @@ template <int FMT, int D, int NT>
 struct Tile {
     using L = KvLayout<FMT, D>;
     static constexpr int KS = D / 16;                     // k-steps of S, m-tiles of O
-    static constexpr int VREGS = L::kPart / 128;          // registers of a record's values
     static constexpr float kBias = FMT == W4_KV_BF16 ? 0.f : 6.f;
     static constexpr float kSlack = FMT == W4_KV_BF16 ? 8.f : 14.f;
 
@@ -231,8 +231,10 @@ struct Tile {
         return half2_fma(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, minus);
     }
 
-    // One record in shared memory, its first key j0.  edge: some row does not
-    // see all of it.
+    // One record in shared memory, its first key j0 (kAbsent: there is none).
+    // edge: some row does not see all of it.  (Two records a step, for more
+    // independent instructions, measured 4 to 30 % slower: it halves what the
+    // rings hold ahead.)
     __device__ __forceinline__ void record(const AttnArgs &a, uint32_t rec, int j0, bool edge,
                                            int len, int row0, int rows) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -242,14 +244,14 @@ struct Tile {
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
         // ---- S^T = K Q^T
-        uint32_t mk[2], mv[2], mt[2][2], vraw[VREGS];
+        uint32_t mk[2], mv[2];                            // descriptors of keys g, g + 8
         if constexpr (FMT == W4_KV_BF16) {
             // piece 2 ks + hi of a row is stored at ^ (row & 7): only four
             // addresses differ, the others are 128 bytes on
-            const uint32_t row = rec + (lane & 15) * L::kRow, x = lane & 7, hi = lane >> 4;
+            const uint32_t row = rec + (lane & 15) * L::kRow, swap = lane & 7, hi = lane >> 4;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                const uint32_t at = row + (((2 * ks + hi) ^ x) << 4);
+                const uint32_t at = row + (((2 * ks + hi) ^ swap) << 4);
                 uint32_t k4[D / 64][4];
 #pragma unroll
                 for (int y = 0; y < D / 64; ++y) ldsm4(k4[y], at + 128 * y);
@@ -262,29 +264,26 @@ struct Tile {
             }
         } else {
             uint32_t w0[D * L::kBits / 128], w1[D * L::kBits / 128];   // keys g, g + 8
+            const uint32_t r0 = rec + g * L::kRow, r1 = r0 + 8 * L::kRow;
             if constexpr (FMT == W4_KV_INT8) {
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                     const int piece = D == 128 ? (4 * i + t) ^ ((g & 1) << 2) : t;
-                    lds128(w0 + 4 * i, rec + g * L::kRow + piece * 16);
-                    lds128(w1 + 4 * i, rec + (g + 8) * L::kRow + piece * 16);
+                    lds128(w0 + 4 * i, r0 + piece * 16);
+                    lds128(w1 + 4 * i, r1 + piece * 16);
                 }
             } else if constexpr (D == 128) {
-                lds128(w0, rec + g * L::kRow + t * 16);
-                lds128(w1, rec + (g + 8) * L::kRow + t * 16);
+                lds128(w0, r0 + t * 16);
+                lds128(w1, r1 + t * 16);
             } else {
-                lds64(w0, rec + g * L::kRow + t * 8);
-                lds64(w1, rec + (g + 8) * L::kRow + t * 8);
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                mk[r] = lds32(rec + L::kMeta + 4 * (g + 8 * r));
-                mv[r] = lds32(rec + L::kMetaV + 4 * (g + 8 * r));
-                lds64(mt[r], rec + L::kMetaV + 4 * (2 * t + 8 * r));
+                lds64(w0, r0 + t * 8);
+                lds64(w1, r1 + t * 8);
             }
             uint32_t zk[2], zk16[2];      // -(1024 + z), -(64 + z) of keys g, g + 8, twice each
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+                mk[r] = lds32(rec + L::kMeta + 4 * (g + 8 * r));
+                mv[r] = lds32(rec + L::kMetaV + 4 * (g + 8 * r));
                 zk[r] = __byte_perm(mk[r], 0u, 0x4242) | 0xE400E400u;
                 zk16[r] = half2_add(zk[r], 0x63806380u);  // + 960
             }
@@ -305,13 +304,14 @@ struct Tile {
                     mma_f16_16816(s[n], a0, a1, a2, a3, qf[n][ks][0], qf[n][ks][1]);
             }
         }
-        // the values are on their way during the softmax
-        if constexpr (FMT == W4_KV_BF16) {
-            load_values(vraw, rec);
-        } else {
+        // quantised values are on their way during the softmax
+        uint32_t mt[2][2], vraw[FMT == W4_KV_BF16 ? 1 : L::kPart / 128];
+        if constexpr (FMT != W4_KV_BF16) {
 #pragma unroll
             for (int i = 0; i < L::kPart / 512; ++i)
                 lds128(vraw + 4 * i, rec + L::kPart + i * 512 + lane * 16);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) lds64(mt[r], rec + L::kMetaV + 4 * (2 * t + 8 * r));
         }
         // ---- scores in units of log2; quantised: with log2 s_v added
         float inv[2] = {1.f, 1.f};                        // 1 / s_v of keys g, g + 8
@@ -337,7 +337,8 @@ struct Tile {
                         s[n][2 * r + c] = fmaf(s[n][2 * r + c], sk * sc[n][c], lv);
             }
         }
-        bool apart = false;       // a key that some rows see and some do not
+        uint32_t keep[2];
+        bool apart = false;       // not finite, seen by some rows and not by others
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -349,35 +350,29 @@ struct Tile {
                 }
             if constexpr (FMT == W4_KV_BF16) {
                 // values of keys that no row sees must not meet the product
-                const int lo = a.window > 0 ? len - a.tokens - a.window : -1;
-                uint32_t keep[2];
-                kept_keys(j0, lo, len - 1, keep);
-                bool finite = true;
-#pragma unroll
-                for (int x = 0; x < VREGS; ++x) {
-                    const uint32_t v = vraw[x] &= keep[(x >> 1) & 1];
-                    finite &= (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
-                }
-                apart = a.tokens > 1 && __any_sync(0xFFFFFFFFu, !finite);
+                kept_keys(j0, a.window > 0 ? len - a.tokens - a.window : -1, len - 1, keep);
+                if (a.tokens > 1) apart = __any_sync(0xFFFFFFFFu, !finite_values(rec, keep));
             }
         }
         // ---- a reference near the maximum: moved only when a score passes it by kSlack
+        float top[NT][2];
         bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                over |= fmaxf(s[n][c], s[n][c + 2]) > m[n][c] + kSlack;
+            for (int c = 0; c < 2; ++c) {
+                top[n][c] = fmaxf(s[n][c], s[n][c + 2]);
+                over |= top[n][c] > m[n][c] + kSlack;
+            }
         if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float top = fmaxf(s[n][c], s[n][c + 2]);
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                    const float now = fmaxf(m[n][c], top - kBias);
+                        top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xFFFFFFFFu, top[n][c], x));
+                    const float now = fmaxf(m[n][c], top[n][c] - kBias);
                     const float f = exp2_fast(m[n][c] - now);
                     m[n][c] = now;
                     l[n][c] *= f;
@@ -405,15 +400,29 @@ struct Tile {
         // ---- O^T += V^T P^T
         if constexpr (FMT == W4_KV_BF16) {
             if (apart) {
-                tokens_apart(a, vraw, j0, len, row0, rows, p);
+                tokens_apart(a, rec, j0, len, row0, rows, p);
                 return;
             }
+            const uint32_t swap = lane & 7, hi = (lane >> 3) & 1;
+            const uint32_t row = rec + L::kPart + ((lane >> 4) * 8 + swap) * L::kRow;
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v4[D / 64][4];
+                const uint32_t at = row + (((2 * k + hi) ^ swap) << 4);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    mma_bf16_16816(o[n][k], vraw[4 * k], vraw[4 * k + 1], vraw[4 * k + 2],
-                                   vraw[4 * k + 3], p[n][0], p[n][1]);
+                for (int y = 0; y < D / 64; ++y) {
+                    ldsm4_t(v4[y], at + 128 * y);
+                    if (edge)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v4[y][i] &= keep[i >> 1];
+                }
+#pragma unroll
+                for (int y = 0; y < D / 64; ++y)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_bf16_16816(o[n][k + 4 * y], v4[y][0], v4[y][1], v4[y][2], v4[y][3],
+                                       p[n][0], p[n][1]);
+            }
         } else {
             uint32_t zlo[2], zhi[2];                      // -(1024 + z), -(64 + z)
 #pragma unroll
@@ -440,15 +449,28 @@ struct Tile {
         }
     }
 
-    // bf16: all values of a record as the row operand.
-    __device__ __forceinline__ static void load_values(uint32_t (&v)[VREGS], uint32_t rec) {
-        const int lane = threadIdx.x & 31, x = lane & 7, hi = (lane >> 3) & 1;
-        const uint32_t row = rec + L::kPart + ((lane >> 4) * 8 + x) * L::kRow;
+    // bf16: whether the kept values of a record that this lane takes are all
+    // finite.
+    __device__ static bool finite_values(uint32_t rec, const uint32_t (&keep)[2]) {
+        const int lane = threadIdx.x & 31;
+        bool ok = true;
+#pragma unroll 1
+        for (int k = 0; k < KS; ++k) {
+            uint32_t v4[4];
+            ldsm4_t(v4, value_piece(rec, lane, k));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int y = 0; y < D / 64; ++y)
-                ldsm4_t(v + 4 * (k + 4 * y), row + (((2 * k + hi) ^ x) << 4) + 128 * y);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = v4[i] & keep[i >> 1];
+                ok &= (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
+            }
+        }
+        return ok;
+    }
+
+    // Address of the row that a lane gives for m-tile k of the values.
+    __device__ static uint32_t value_piece(uint32_t rec, int lane, int k) {
+        const uint32_t swap = lane & 7, hi = (lane >> 3) & 1;
+        return rec + L::kPart + ((lane >> 4) * 8 + swap) * L::kRow + (((2 * k + hi) ^ swap) << 4);
     }
 
     // New token of column 2t + c of tile n.
@@ -471,25 +493,28 @@ struct Tile {
     // some tokens see and others do not: 0 * inf would reach the rows that do
     // not see it, so each token's rows get a product of their own over the
     // keys that they see.
-    __device__ __forceinline__ void tokens_apart(const AttnArgs &a, const uint32_t (&v)[VREGS],
-                                              int j0, int len, int row0, int rows,
-                                              const uint32_t (&p)[NT][2]) {
+    __device__ __forceinline__ void tokens_apart(const AttnArgs &a, uint32_t rec, int j0, int len,
+                                                 int row0, int rows, const uint32_t (&p)[NT][2]) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
         for (int i = 0; i < a.tokens; ++i) {
             const int last = len - a.tokens + i;
             uint32_t keep[2];
             kept_keys(j0, a.window > 0 ? last - a.window : -1, last, keep);
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k) {
+                uint32_t v[4];
+                ldsm4_t(v, value_piece(rec, lane, k));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float d[4] = {o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]};
-                    mma_bf16_16816(d, v[4 * k] & keep[0], v[4 * k + 1] & keep[0],
-                                   v[4 * k + 2] & keep[1], v[4 * k + 3] & keep[1], p[n][0],
-                                   p[n][1]);
+                    mma_bf16_16816(d, v[0] & keep[0], v[1] & keep[0], v[2] & keep[1],
+                                   v[3] & keep[1], p[n][0], p[n][1]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (token_of(a, n, c & 1, row0, rows) == i) o[n][k][c] = d[c];
                 }
+            }
         }
     }
 
@@ -521,12 +546,15 @@ __device__ __forceinline__ float *slot_of(const AttnArgs &a, int block, bool sta
            (size_t)(2 * block + (starts ? 1 : 0)) * kRowsMax * (D + 2);
 }
 
-__device__ void store_row(const AttnArgs &a, int b, int h, int row, int d, float4 o, float m,
-                          float l) {
+// Four values of a row, l and m its sum and reference.  dry: nothing is stored.
+__device__ __forceinline__ void store_row(const AttnArgs &a, int b, int h, int row, int d,
+                                          float4 o, float m, float l, bool dry) {
     const int i = row / a.group, hq = h * a.group + row - i * a.group;
     const long long t = (long long)b * a.tokens + i;
     const float f = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;    // NaN stays NaN
     const long long at = t * a.out.token_stride + (long long)hq * a.out.head_stride + d;
+    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (dry) return;
     if (a.f32_out) {
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out.data) + at) =
             make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
@@ -535,7 +563,7 @@ __device__ void store_row(const AttnArgs &a, int b, int h, int row, int d, float
             make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
     }
     if (a.lse && d == 0)
-        a.lse[t * a.q_heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        a.lse[t * a.q_heads + hq] = lse;
 }
 
 __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) {
@@ -543,24 +571,21 @@ __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) 
     o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
 }
 
-// Start of stretch c of `work` records over `blocks` blocks.
-__device__ __forceinline__ int stretch(int work, int blocks, int c) {
-    const int q = work / blocks;
-    return q * c + (int)((unsigned)(work - q * blocks) * (unsigned)c / (unsigned)blocks);
-}
-
 // A place in the list of records (the host refuses lists of 2^31).
 struct Cut {
     int b, item, u;        // sequence, head (x row tile) of it, record of that
 };
 
-// The list, as a warp sees it: lane i holds sequences [b0, b1), their items'
-// records are [before, before + mine) * per_seq.
+// The list, as a warp sees it: lane i holds sequences [b0, b1), whose items
+// have the records [before, before + mine) * per_seq.
 struct List {
     int b0, b1, before, mine, per_seq, work;
+    int blocks, least;     // blocks that have a stretch, records that are not cut off
+    int q, rest;           // work / blocks and its remainder
+    unsigned magic;        // 2^32 / blocks, rounded up
 
-    __device__ __forceinline__ List(const AttnArgs &a, int row_tiles) {
-        const int lane = threadIdx.x & 31, each = (a.pool.seqs + 31) / 32;
+    __device__ __forceinline__ List(const AttnArgs &a, int row_tiles, int KG) {
+        const int lane = threadIdx.x & 31, each = (a.pool.seqs + 31) >> 5;
         per_seq = a.pool.kv_heads * row_tiles;
         b0 = min(lane * each, a.pool.seqs), b1 = min(b0 + each, a.pool.seqs);
         mine = 0;
@@ -576,35 +601,56 @@ struct List {
         }
         before = upto - mine;
         work = __shfl_sync(0xFFFFFFFFu, upto, a.pool.seqs > 1 ? 31 : 0) * per_seq;
+        // as many blocks as heads, or that many times the parts of at least 4
+        // records a group that the mean head has (so heads of one length are
+        // cut alike), while there are blocks
+        const int heads = a.pool.seqs * per_seq;
+        blocks = min(min((int)gridDim.x, work), heads * max(1, work / (heads * 4 * KG)));
+        q = work / blocks, rest = work - q * blocks;
+        magic = 0xFFFFFFFFu / (unsigned)blocks + 1;
+        least = min(4 * KG, max(KG, q >> 3));
+    }
+
+    // Start of block c's stretch.  rest * c < 2^16, so the product with magic
+    // gives rest * c / blocks exactly (blocks = 1: rest is 0).
+    __device__ __forceinline__ int start(int c) const {
+        return q * c + (int)__umulhi((unsigned)(rest * c), magic);
     }
 
     // Place of record u of the list, moved to its head's border where fewer
     // than `least` records would be cut off.
-    __device__ __forceinline__ Cut cut(const AttnArgs &a, int u, int least) const {
+    __device__ __forceinline__ Cut cut(const AttnArgs &a, int u) const {
         const bool here = u >= before * per_seq && u < (before + mine) * per_seq;
-        int b = b0, n = 1, in = u - before * per_seq;
-        if (here)
-            for (;; ++b) {
-                n = max(sequence(a, b).records, 1);
-                if (in < n * per_seq) break;
-                in -= n * per_seq;
-            }
+        int b = b0, n = mine, in = u - before * per_seq;
+        if (a.pool.seqs > 1) {
+            if (here)
+                for (;; ++b) {
+                    n = max(sequence(a, b).records, 1);
+                    if (in < n * per_seq) break;
+                    in -= n * per_seq;
+                }
+        }
         const unsigned found = __ballot_sync(0xFFFFFFFFu, here);
         const int src = found ? __ffs(found) - 1 : 0;
         Cut c;
         c.b = __shfl_sync(0xFFFFFFFFu, b, src);
         n = __shfl_sync(0xFFFFFFFFu, n, src);
         in = __shfl_sync(0xFFFFFFFFu, in, src);
-        if (!found) {                                         // the list's end
-            c.b = a.pool.seqs, c.item = 0, c.u = 0;
-            return c;
-        }
-        c.item = in / n;
-        c.u = in - c.item * n;
-        if (c.u < least || n - c.u < least) {
+        c.item = found ? in / n : 0;
+        c.u = found ? in - c.item * n : 0;
+        if (!found) c.b = a.pool.seqs;                        // the list's end
+        if (found && (c.u < least || n - c.u < least)) {
             if (2 * c.u > n && ++c.item == per_seq) c.item = 0, ++c.b;
             c.u = 0;
         }
+        return c;
+    }
+
+    // First block c with start(c) >= u (u > 0).
+    __device__ __forceinline__ int block_from(int u) const {
+        int c = min((int)((float)u * ((float)blocks / (float)work)), blocks);
+        while (c > 0 && start(c) >= u) --c;
+        while (start(c) < u) ++c;
         return c;
     }
 };
@@ -615,72 +661,73 @@ __device__ __forceinline__ void warps_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
+// A running join: o, l relative to m take in 8 values of another piece.
+struct Joined {
+    float4 o0, o1;
+    float m, l;
+
+    __device__ __forceinline__ void take(const float4 &v0, const float4 &v1, float vm, float vl) {
+        const float now = fmaxf(m, vm), f = exp2_fast(m - now), g = exp2_fast(vm - now);
+        o0 = make_float4(o0.x * f, o0.y * f, o0.z * f, o0.w * f);
+        o1 = make_float4(o1.x * f, o1.y * f, o1.z * f, o1.w * f);
+        add_scaled(o0, g, v0);
+        add_scaled(o1, g, v1);
+        l = fmaf(l, f, vl * g);
+        m = now;
+    }
+};
+
 // The block that finished a head last joins its n pieces, those of blocks c0 ..
-// c0 + n - 1, in that order.
+// c0 + n - 1, in an order that depends on their number only.  One pass: a
+// piece's values, reference and sum are asked for together, because a trip to
+// L2 costs more than the arithmetic.
 template <int D, int WARPS>
 __device__ __forceinline__ void join_pieces(const AttnArgs &a, int c0, int n, int b, int h,
-                                         int tile0, int there, float *buf) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // a thread takes 4 values; its first loads are under way while the factors
-    // are worked out
-    constexpr int THREADS = 32 * WARPS, AHEAD = 20;
-    float *fac = buf, *mx = buf + n * there, *sum = mx + kRowsMax;
-    const int values = there * (D / 4);
-    const auto piece = [&](int e, int c) {
-        return __ldcg(reinterpret_cast<const float4 *>(
-            &slot_of<D>(a, c0 + c, c == 0)[e / (D / 4) * D + e % (D / 4) * 4]));
-    };
-    float4 early[AHEAD];
-#pragma unroll
-    for (int x = 0; x < AHEAD; ++x)
-        early[x] = tid < values && x < n ? piece(tid, x) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = warp; r < there; r += WARPS) {               // a warp per row: factors
-        float m = kNone, l = 0.f, m1 = kNone, l1 = 0.f;       // the first 64 stay in registers
-        const float *s = slot_of<D>(a, c0 + lane, lane == 0) + kRowsMax * D + r;
-        const float *s1 = slot_of<D>(a, c0 + lane + 32, false) + kRowsMax * D + r;
-        if (lane < n) m = __ldcg(s), l = __ldcg(s + kRowsMax);
-        if (lane + 32 < n) m1 = __ldcg(s1), l1 = __ldcg(s1 + kRowsMax);
-        float top = fmaxf(m, m1);
-        for (int c = lane + 64; c < n; c += 32)
-            top = fmaxf(top, __ldcg(slot_of<D>(a, c0 + c, false) + kRowsMax * D + r));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-        const float f = exp2_fast(m - top), f1 = exp2_fast(m1 - top);
-        float total = fmaf(f, l, f1 * l1);
-        if (lane < n) fac[lane * there + r] = f;
-        if (lane + 32 < n) fac[(lane + 32) * there + r] = f1;
-        for (int c = lane + 64; c < n; c += 32) {
-            const float *s2 = slot_of<D>(a, c0 + c, false) + kRowsMax * D + r;
-            const float f2 = exp2_fast(__ldcg(s2) - top);
-            fac[c * there + r] = f2;
-            total = fmaf(f2, __ldcg(s2 + kRowsMax), total);
+                                            int tile0, int there, float *buf, bool dry) {
+    constexpr int THREADS = 32 * WARPS, UNITS = D / 8;        // 8 values a thread
+    const int tid = dry ? threadIdx.x & 31 : threadIdx.x;
+    const int values = there * UNITS, sides = max(1, THREADS / values);
+    float4 *part = reinterpret_cast<float4 *>(buf);
+    // `sides` threads per 8 values take every sides-th piece each
+    for (int e0 = 0; e0 < values; e0 += dry ? 1 << 20 : THREADS) {
+        const int side = sides > 1 ? tid / values : 0, e = e0 + tid - side * values;
+        const int r = e / UNITS, d = e % UNITS * 8;
+        const bool has = side < sides && e < values;
+        Joined j = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f), kNone, 0.f};
+        if (has) {
+#pragma unroll 7
+            for (int c = side; c < n; c += sides) {
+                const float *s = slot_of<D>(a, c0 + c, c == 0);
+                const float4 *v = reinterpret_cast<const float4 *>(s + r * D + d);
+                j.take(__ldcg(v), __ldcg(v + 1), __ldcg(s + kRowsMax * D + r),
+                       __ldcg(s + kRowsMax * D + kRowsMax + r));
+            }
         }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
-        if (lane == 0) mx[r] = top, sum[r] = total;
-    }
-    warps_sync<WARPS>();
-    for (int e = tid; e < values; e += THREADS) {
-        const int r = e / (D / 4);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e >= THREADS) {
-#pragma unroll
-            for (int x = 0; x < AHEAD; ++x)
-                if (x < n) early[x] = piece(e, x);
+        if (sides > 1) {
+            if (has && side > 0 && !dry) {
+                part[3 * tid] = j.o0, part[3 * tid + 1] = j.o1;
+                part[3 * tid + 2] = make_float4(j.m, j.l, 0.f, 0.f);
+            }
+            if (!dry) warps_sync<WARPS>();
+#pragma unroll 1
+            for (int x = 1; x < sides && side == 0; ++x) {
+                const float4 *v = part + 3 * (tid + x * values);
+                j.take(v[0], v[1], v[2].x, v[2].y);
+            }
         }
-#pragma unroll
-        for (int x = 0; x < AHEAD; ++x)
-            if (x < n) add_scaled(o, fac[x * there + r], early[x]);
-#pragma unroll 16
-        for (int c = AHEAD; c < n; ++c) add_scaled(o, fac[c * there + r], piece(e, c));
-        store_row(a, b, h, tile0 + r, e % (D / 4) * 4, o, mx[r], sum[r]);
+        if (has && side == 0) {
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x)
+                store_row(a, b, h, tile0 + r, d + 4 * x, x ? j.o1 : j.o0, j.m, j.l, dry);
+        }
     }
 }
 
-// Warps that compute: with the one that copies 16 of 128 registers, or 12 of 168.
+// Warps that compute: with the two that copy 16 of 128 registers, or 12 of 168.
+constexpr int kCopyWarps = 2;
 template <int NT>
 __host__ __device__ constexpr int compute_warps() {
-    return NT == 1 ? 15 : 11;
+    return NT == 1 ? 14 : 10;
 }
 
 // How a launch divides a block (host).
@@ -702,7 +749,8 @@ struct Piece {
     int c0, pieces;    // cut: the head's first block, and how many pieces it has
 };
 
-// The copying warp: lane kg fills the ring of group kg.
+// The copying warps: lane i of warp w fills the ring of group 2 i + w.  Two of
+// them, because a copy costs its warp about 100 cycles.
 template <int FMT, int D, int WARPS>
 __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan, int block_rows,
                                              unsigned char *smem, uint64_t *full, uint64_t *empty,
@@ -710,25 +758,21 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
                                              uint64_t *piece_empty) {
     using L = KvLayout<FMT, D>;
     const int lane = threadIdx.x & 31, KG = plan.KG, stages = plan.stages;
-    const List list(a, plan.row_tiles);
+    const int copier = (threadIdx.x >> 5) - WARPS, kg = kCopyWarps * lane + copier;
+    const List list(a, plan.row_tiles, KG);
     const int per_seq = list.per_seq;
-    // every head a block of its own while there are blocks, else parts of at
-    // least 4 records a group
-    const int blocks = min(min((int)gridDim.x, list.work),
-                           max(a.pool.seqs * per_seq, list.work / (4 * KG)));
-    const int least = min(4 * KG, max(KG, list.work / blocks / 8));
     Cut c, to;
     c.b = 0, c.item = 0, c.u = 0;
     to = c;
-    if ((int)blockIdx.x < blocks) {
-        c = list.cut(a, stretch(list.work, blocks, blockIdx.x), least);
-        to = list.cut(a, stretch(list.work, blocks, blockIdx.x + 1), least);
+    if ((int)blockIdx.x < list.blocks) {
+        c = list.cut(a, list.start(blockIdx.x));
+        to = list.cut(a, list.start(blockIdx.x + 1));
     }
     int put = 0, used = 0, told = 0;
     uint32_t phase = 1;
     bool ok = true;
-    uint64_t *my_full = full + lane * stages, *my_empty = empty + lane * stages;
-    unsigned char *ring = smem + lane * stages * L::kBytes;
+    uint64_t *my_full = full + kg * stages, *my_empty = empty + kg * stages;
+    unsigned char *ring = smem + kg * stages * L::kBytes;
     while (true) {
         const bool more = c.b < to.b || c.item < to.item || c.u < to.u;
         const Seq seq = sequence(a, more ? c.b : 0);
@@ -736,13 +780,29 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
         const bool last = c.b == to.b && c.item == to.item;
         const int u1 = last ? to.u : n_seq, stop = min(u1, seq.records);
         const int h = c.item / plan.row_tiles;
-        Piece p;
-        p.b = more ? c.b : -1;
-        p.h = h, p.tile0 = (c.item - h * plan.row_tiles) * block_rows;
-        p.u0 = c.u, p.stop = stop, p.len = seq.len;
-        p.whole = c.u == 0 && u1 == n_seq, p.starts = c.u == 0;
-        p.c0 = p.pieces = 0;
-        if (more && !p.whole) {
+        const int32_t *pages = a.pool.table + (more ? c.b : 0) * a.pool.stride;
+        constexpr int AHEAD = 4;
+        int page[AHEAD];
+        const auto fetch = [&](int x, int u) {
+            page[x] = u < stop && kg < KG ? pages[page_slot(a.pool, seq.first + u)] : 0;
+        };
+        if (more) {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) fetch(x, c.u + kg + x * KG);
+        }
+        // tell the others, two pieces ahead at most (while the pages' numbers
+        // are on their way)
+        const int slot = told & 1;
+        const bool tells = copier == 0 && lane == 0;
+        if (copier == 0 && told >= 2) mbar_wait(&piece_empty[slot], (told >> 1) + 1 & 1);
+        Piece &p = piece[slot];
+        if (tells) {
+            p.b = more ? c.b : -1;
+            p.h = h, p.tile0 = (c.item - h * plan.row_tiles) * block_rows;
+            p.u0 = c.u, p.stop = stop, p.len = seq.len;
+            p.whole = c.u == 0 && u1 == n_seq, p.starts = c.u == 0;
+        }
+        if (copier == 0 && more && !(c.u == 0 && u1 == n_seq)) {
             // the cuts inside this head, at least `least` records from its borders
             const bool mine = c.b >= list.b0 && c.b < list.b1;
             int head = list.before * per_seq + c.item * n_seq;
@@ -750,61 +810,45 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
                 for (int x = list.b0; x < c.b; ++x)
                     head += max(sequence(a, x).records, 1) * per_seq;
             head = __shfl_sync(0xFFFFFFFFu, head, __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1);
-            const int lo = head + least, hi = head + n_seq - least;
-            int c_lo = (int)((long long)lo * blocks / list.work);
-            while (c_lo > 0 && stretch(list.work, blocks, c_lo) >= lo) --c_lo;
-            while (stretch(list.work, blocks, c_lo) < lo) ++c_lo;
-            int c_hi = (int)((long long)hi * blocks / list.work) + 1;
-            while (stretch(list.work, blocks, c_hi) > hi) --c_hi;
-            p.c0 = c_lo - 1, p.pieces = c_hi - c_lo + 2;
+            const int c_lo = list.block_from(head + list.least);
+            const int c_hi = list.block_from(head + n_seq - list.least + 1) - 1;
+            if (tells) p.c0 = c_lo - 1, p.pieces = c_hi - c_lo + 2;
         }
-        // tell the others, two pieces ahead at most
-        const int slot = told & 1;
-        if (told >= 2) mbar_wait(&piece_empty[slot], (told >> 1) + 1 & 1);
-        if (lane == 0) {
-            piece[slot] = p;
-            mbar_arrive(&piece_full[slot]);
-        }
+        if (tells) mbar_arrive(&piece_full[slot]);
         ++told;
         if (!more) break;
 
-        const int32_t *pages = a.pool.table + c.b * a.pool.stride;
-        constexpr int AHEAD = 4;
-        int page[AHEAD];
-        const auto fetch = [&](int x, int u) {
-            page[x] = u < stop && lane < KG ? pages[page_slot(a.pool, seq.first + u)] : 0;
-        };
-#pragma unroll
-        for (int x = 0; x < AHEAD; ++x) fetch(x, c.u + lane + x * KG);
         for (int u0 = c.u; u0 < stop; u0 += AHEAD * KG)
 #pragma unroll
             for (int x = 0; x < AHEAD; ++x) {
-                const int u = u0 + lane + x * KG, r = seq.first + u, pg = page[x];
+                const int u = u0 + kg + x * KG, r = seq.first + u, pg = page[x];
                 fetch(x, u + AHEAD * KG);
-                if (lane >= KG || u >= stop || !ok) continue;
-                if (used >= stages) {
-                    ok = mbar_wait(&my_empty[put], phase);
-                    if (!ok) {                                // never in normal operation
-                        if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
-                        continue;
-                    }
+                const bool mine = kg < KG && u < stop && ok;
+                // the lanes leave the wait one by one: without the barrier
+                // each would go through the rest by itself
+                if (mine && used >= stages) ok = mbar_wait(&my_empty[put], phase);
+                __syncwarp();
+                if (mine && ok) {
                     fence_proxy_async();
+                    const bool valid = pg >= 0 && pg < a.pool.pages;
+                    first_key[kg * stages + put] = valid ? r * kRecTokens : kAbsent;
+                    if (valid) {
+                        const char *src =
+                            a.pool.records +
+                            (((long long)pg * a.pool.kv_heads + h) * a.pool.page_records + r -
+                             page_slot(a.pool, r) * a.pool.page_records) * L::kBytes;
+                        mbar_expect_tx(&my_full[put], L::kBytes);
+                        bulk_g2s(ring + put * L::kBytes, src, L::kBytes, &my_full[put]);
+                    } else {
+                        if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_PAGE);
+                        mbar_arrive(&my_full[put]);
+                    }
+                    used = min(used + 1, stages);
+                    if (++put == stages) put = 0, phase ^= 1;
+                } else if (mine && a.pool.error) {
+                    atomicOr(a.pool.error, W4_KV_ERR_WAIT);   // never in normal operation
                 }
-                const bool valid = pg >= 0 && pg < a.pool.pages;
-                first_key[lane * stages + put] = valid ? r * kRecTokens : -1;
-                if (valid) {
-                    const char *src =
-                        a.pool.records +
-                        (((long long)pg * a.pool.kv_heads + h) * a.pool.page_records + r -
-                         page_slot(a.pool, r) * a.pool.page_records) * L::kBytes;
-                    mbar_expect_tx(&my_full[put], L::kBytes);
-                    bulk_g2s(ring + put * L::kBytes, src, L::kBytes, &my_full[put]);
-                } else {
-                    if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_PAGE);
-                    mbar_arrive(&my_full[put]);
-                }
-                used = min(used + 1, stages);
-                if (++put == stages) put = 0, phase ^= 1;
+                __syncwarp();
             }
         __syncwarp();
         if (last) {
@@ -823,7 +867,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(32 * (compute_warps<NT>() + 1), 1)
+__global__ void __launch_bounds__(32 * (compute_warps<NT>() + kCopyWarps), 1)
 attn_kernel(const AttnArgs a, const Plan plan) {
     extern __shared__ __align__(128) unsigned char smem[];
     using L = KvLayout<FMT, D>;
@@ -831,14 +875,14 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     constexpr int OROW = D + 4;                               // floats; + 4: no bank conflicts
     __shared__ uint64_t full[kMaxWarps * kMaxStages], empty[kMaxWarps * kMaxStages];
     __shared__ uint64_t piece_full[2], piece_empty[2];
-    __shared__ int first_key[kMaxWarps * kMaxStages];         // of a stage's record; -1: no page
+    __shared__ int first_key[kMaxWarps * kMaxStages];         // of a stage's record, or kAbsent
     __shared__ float join_m[kMaxWarps * 8 * NT], join_l[kMaxWarps * 8 * NT];
     __shared__ Piece piece[2];
     __shared__ int is_last;
     const int block_rows = 8 * NT * plan.QG;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < plan.KG * plan.stages; i += 32 * (WARPS + 1)) {
+    for (int i = tid; i < plan.KG * plan.stages; i += 32 * (WARPS + kCopyWarps)) {
         mbar_init(&full[i], 1);
         mbar_init(&empty[i], plan.QG);
     }
@@ -849,14 +893,17 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     begin_after_previous();
-    if (warp == WARPS) {
+    // A copying warp that is done goes once through the joins, without barriers
+    // and without storing anything: they are run by few blocks and late, so
+    // their instructions would come from DRAM, line after line (5 us of 34 for
+    // one sequence of 64 k tokens).
+    const bool dry = warp >= WARPS;
+    if (dry)
         copy_records<FMT, D, WARPS>(a, plan, block_rows, smem, full, empty, first_key, piece,
                                     piece_full, piece_empty);
-        return;
-    }
 
     const int kg = warp / plan.QG, qg = warp - kg * plan.QG;
-    const bool works = kg < plan.KG;                          // QG may not divide WARPS
+    const bool works = kg < plan.KG && !dry;                  // QG may not divide WARPS
     const uint32_t ring = smem_addr(smem) + kg * plan.stages * L::kBytes;
     int get = 0;
     uint32_t phase = 0;
@@ -864,12 +911,14 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     Tile<FMT, D, NT> w;
     for (int told = 0;; ++told) {
         const Piece &p = piece[told & 1];
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&piece_full[told & 1], (told >> 1) & 1))) {
-            if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
-            return;                                           // every warp does
+        if (!dry) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&piece_full[told & 1], (told >> 1) & 1))) {
+                if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
+                return;                                       // every warp does
+            }
+            if (p.b < 0) return;
         }
-        if (p.b < 0) return;
-        if (works) {
+        if (works && !failed) {
             const int rows = a.tokens * a.group, row0 = p.tile0 + qg * 8 * NT;
             w.load_q(a, p.b, p.h, row0, rows);
             w.clear();
@@ -877,16 +926,16 @@ attn_kernel(const AttnArgs a, const Plan plan) {
             const int len = p.len, seen1 = len - a.tokens + 1;
             const int seen0 = a.window > 0 ? len - a.window : 0;
             uint64_t *my_full = full + kg * plan.stages, *my_empty = empty + kg * plan.stages;
-            for (int u = p.u0 + kg; u < p.stop && !failed; u += plan.KG) {
+            const int *keys = first_key + kg * plan.stages;
+            for (int u = p.u0 + kg; u < p.stop; u += plan.KG) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&my_full[get], phase))) {
-                    failed = true;                            // never in normal operation
                     if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
+                    failed = true;                            // never in normal operation
                     break;
                 }
-                const int j0 = first_key[kg * plan.stages + get];
-                if (j0 >= 0)
-                    w.record(a, ring + get * L::kBytes, j0, j0 + kRecTokens > seen1 || j0 < seen0,
-                             len, row0, rows);
+                const int j0 = keys[get];
+                w.record(a, ring + get * L::kBytes, j0, j0 + kRecTokens > seen1 || j0 < seen0, len,
+                         row0, rows);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&my_empty[get]);
                 if (++get == plan.stages) get = 0, phase ^= 1;
@@ -914,46 +963,48 @@ attn_kernel(const AttnArgs a, const Plan plan) {
                         join_o[(r + (x & 1)) * OROW + 16 * k + g + (x & 2) * 4] = w.o[n][k][x];
             }
         }
-        warps_sync<WARPS>();
-        const int there = min(block_rows, a.tokens * a.group - p.tile0);
+        if (!dry) warps_sync<WARPS>();
+        const bool whole = !dry && p.whole;
+        const int there = dry ? block_rows : min(block_rows, a.tokens * a.group - p.tile0);
         float *slot = slot_of<D>(a, blockIdx.x, p.starts);
-        for (int e = tid; e < there * (D / 4); e += 32 * WARPS) {
+        for (int e = dry ? lane : tid; e < there * (D / 4); e += dry ? 1 << 20 : 32 * WARPS) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = kNone, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float mk[WARPS];
-#pragma unroll
-            for (int k = 0; k < WARPS; ++k) {
-                mk[k] = k < plan.KG ? join_m[k * block_rows + r] : kNone;
-                m = fmaxf(m, mk[k]);
+#pragma unroll 5
+            for (int k = 0; k < plan.KG; ++k) m = fmaxf(m, join_m[k * block_rows + r]);
+#pragma unroll 5
+            for (int k = 0; k < plan.KG; ++k) {
+                const int at = k * block_rows + r;
+                const float f = exp2_fast(join_m[at] - m);
+                l = fmaf(f, join_l[at], l);
+                add_scaled(o, f, *reinterpret_cast<const float4 *>(&join_o[at * OROW + d]));
             }
-#pragma unroll
-            for (int k = 0; k < WARPS; ++k)
-                if (k < plan.KG) {
-                    const int at = k * block_rows + r;
-                    const float f = exp2_fast(mk[k] - m);
-                    l = fmaf(f, join_l[at], l);
-                    add_scaled(o, f, *reinterpret_cast<const float4 *>(&join_o[at * OROW + d]));
-                }
-            if (p.whole) {
-                store_row(a, p.b, p.h, p.tile0 + r, d, o, m, l);
-            } else {
+            if (whole) {
+                store_row(a, p.b, p.h, p.tile0 + r, d, o, m, l, false);
+            } else if (!dry) {
                 *reinterpret_cast<float4 *>(&slot[r * D + d]) = o;
                 if (d == 0) slot[kRowsMax * D + r] = m, slot[kRowsMax * D + kRowsMax + r] = l;
             }
         }
-        if (!p.whole) {
-            uint32_t *counter = static_cast<uint32_t *>(a.workspace) + p.c0;
-            __threadfence();
-            warps_sync<WARPS>();
-            if (tid == 0) is_last = atomicAdd(counter, 1u) == (uint32_t)(p.pieces - 1);
-            warps_sync<WARPS>();
-            if (is_last) {
+        if (!whole) {
+            if (!dry) {
+                uint32_t *counter = static_cast<uint32_t *>(a.workspace) + p.c0;
                 __threadfence();
-                if (tid == 0) *counter = 0u;
-                join_pieces<D, WARPS>(a, p.c0, p.pieces, p.b, p.h, p.tile0, there, join_o);
+                warps_sync<WARPS>();
+                if (tid == 0) {
+                    is_last = atomicAdd(counter, 1u) == (uint32_t)(p.pieces - 1);
+                    if (is_last) *counter = 0u;
+                }
+                warps_sync<WARPS>();
+            }
+            if (dry || is_last) {
+                if (!dry) __threadfence();
+                join_pieces<D, WARPS>(a, dry ? blockIdx.x : p.c0, dry ? 1 : p.pieces, p.b, p.h,
+                                      p.tile0, there, join_o, dry);
             }
         }
+        if (dry) return;
         warps_sync<WARPS>();                                  // the join's memory is free again
         if (lane == 0) mbar_arrive(&piece_empty[told & 1]);
     }
@@ -976,16 +1027,15 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     Plan p;
     p.row_tiles = (tiles + most - 1) / most;
     p.QG = (tiles + p.row_tiles - 1) / p.row_tiles;
-    // groups: as many as the warps allow with two records in a ring, three of
-    // the 8 KB of bf16 ones (with two, HBM was 9 % slower)
-    const int join_row = 8 * NT * p.QG * (D + 4) * 4, deep = bytes > 4224 ? 3 : 2;
+    // groups: as many as the warps allow with three records in a ring
+    const int join_row = 8 * NT * p.QG * (D + 4) * 4;
     p.KG = WARPS / p.QG;
-    while (p.KG > 1 && p.KG * (join_row + deep * bytes) > kSharedBytes) --p.KG;
+    while (p.KG > 1 && p.KG * (join_row + 3 * bytes) > kSharedBytes) --p.KG;
     p.stages = (kSharedBytes - p.KG * join_row) / (p.KG * bytes);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.ring_bytes = p.KG * p.stages * bytes;
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    return launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + 1)),
+    return launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
                              kSharedBytes, stream, a, p);
 }
 
