@@ -75,12 +75,12 @@ struct Rotation {
 };
 
 // Tokens of w4_kv_append and w4_kv_read: token t is at positions[t] of
-// sequence seq_ids[t], or of t / per_seq without seq_ids.
+// sequence seq_ids[t], or of t / run without seq_ids.
 struct TokenList {
     const int32_t *positions;
     const int32_t *seq_ids;
     int tokens;
-    int per_seq;
+    int run;                   // tokens of one sequence in a row (with seq_ids: all)
 };
 
 cudaError_t launch_rope_table(const unsigned long long *turns, int pairs, double amplitude,
@@ -90,11 +90,9 @@ cudaError_t launch_rope(const Heads &x, const Heads &y, int tokens, int heads, i
                         bool wide, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const Heads &k,
                              const Heads &v, const Heads &q, const Heads &q_out, int q_heads,
-                             const TokenList &list, const Rotation &rot, int num_sms,
-                             cudaStream_t stream);
+                             const TokenList &list, const Rotation &rot, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,
-                           const Heads &v, const TokenList &list, int num_sms,
-                           cudaStream_t stream);
+                           const Heads &v, const TokenList &list, cudaStream_t stream);
 
 struct AttnArgs {
     KvPool pool;
@@ -138,6 +136,41 @@ __device__ __forceinline__ void begin_after_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A pair turned by cs = (cos, sin): every operation rounded once, so that the
+// result is that of any other evaluation of the formula bit for bit.
+__device__ __forceinline__ float2 turn_pair(float a, float b, float2 cs) {
+    return make_float2(__fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y)),
+                       __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y)));
+}
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) {
+    return __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// 8 bfloat16 values and their 8 partners.
+__device__ __forceinline__ void turn_halves(uint4 &a, uint4 &b, const float2 (&cs)[8]) {
+    uint32_t *wa = &a.x, *wb = &b.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 r0 = turn_pair(bf16_low(wa[i]), bf16_low(wb[i]), cs[2 * i]);
+        const float2 r1 = turn_pair(bf16_high(wa[i]), bf16_high(wb[i]), cs[2 * i + 1]);
+        wa[i] = bf16_pair(r0.x, r1.x);
+        wb[i] = bf16_pair(r0.y, r1.y);
+    }
+}
+// 4 pairs of neighbours.
+__device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 (&cs)[8]) {
+    uint32_t *w = &a.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 r = turn_pair(bf16_low(w[i]), bf16_high(w[i]), cs[i]);
+        w[i] = bf16_pair(r.x, r.y);
+    }
+}
+
 // Where token t of a list is kept: the first record of its page for head 0,
 // and the token's place; false (and a bit of the error word) if it is
 // nowhere, false without one for padding.
@@ -151,7 +184,7 @@ __device__ __forceinline__ bool kv_place(const KvPool &pool, const TokenList &li
                                          int rotation_rows, TokenPlace *at) {
     const int pos = list.positions[t];
     if (pos < 0) return false;
-    const int seq = list.seq_ids ? list.seq_ids[t] : t / list.per_seq;
+    const int seq = list.seq_ids ? list.seq_ids[t] : t / list.run;
     uint32_t bad = 0;
     int page = 0;
     const int slot = pos / pool.page_tokens;

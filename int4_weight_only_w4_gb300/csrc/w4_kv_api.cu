@@ -240,15 +240,14 @@ w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_hea
     if (q_heads > 0 && (!q->data || !q_out->data || !rows_aligned(q, 2) ||
                         !rows_aligned(q_out, 2)))
         return W4_ERR_INVALID_ARG;
-    const int sms = device_sms();
-    if (sms <= 0) return W4_ERR_CUDA;
     w4::Rotation rot = {nullptr, 0, 0, 0};
     if (rotation)
         rot = {rotation->table, rotation->rows, rotation->rotary_dim / 2, rotation->layout};
-    const w4::TokenList list = {positions, seq_ids, tokens, tokens / table->seqs};
+    const w4::TokenList list = {positions, seq_ids, tokens,
+                                seq_ids ? tokens : tokens / table->seqs};
     return cuda_status(w4::launch_kv_append(
         pool_of(cache, table), cache->format, cache->head_dim, heads_of(k), heads_of(v),
-        heads_of(q), heads_of(q_out), q_heads, list, rot, sms,
+        heads_of(q), heads_of(q_out), q_heads, list, rot,
         reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -262,11 +261,10 @@ w4_status w4_kv_read(const w4_kv_cache *cache, const w4_heads *k_out, const w4_h
     if (tokens == 0) return W4_OK;
     for (const w4_heads *h : {k_out, v_out})
         if (h && (!h->data || !rows_aligned(h, 2))) return W4_ERR_INVALID_ARG;
-    const int sms = device_sms();
-    if (sms <= 0) return W4_ERR_CUDA;
-    const w4::TokenList list = {positions, seq_ids, tokens, tokens / table->seqs};
+    const w4::TokenList list = {positions, seq_ids, tokens,
+                                seq_ids ? tokens : tokens / table->seqs};
     return cuda_status(w4::launch_kv_read(pool_of(cache, table), cache->format, cache->head_dim,
-                                          heads_of(k_out), heads_of(v_out), list, sms,
+                                          heads_of(k_out), heads_of(v_out), list,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 

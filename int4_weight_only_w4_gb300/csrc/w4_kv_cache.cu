@@ -1,105 +1,184 @@
 // The paged key-value cache: writing tokens (w4_kv_append: rotation of q and
-// k, quantisation, scatter into records) and reading them back (w4_kv_read).
+// k, quantisation, the record layout) and reading them back (w4_kv_read).
 //
 // Mathematics of a (token, head) group: w4_quantize's asymmetric rule with
-// Q = 255 or 15 (include/w4.h), every operation rounded to nearest in fp32, so
-// the codes are those of any other evaluation of the rule bit for bit.
+// Q = 255 or 15 levels (include/w4.h), every operation rounded to nearest in
+// fp32, so the codes are those of any other evaluation of the rule bit for bit.
+//
+// A block takes a tile of up to 16 listed tokens and one key/value head, cut so
+// that the tokens of a sequence in order fall into whole records.  Such a
+// record is put together (or taken apart) in shared memory and moved with
+// 16-byte accesses; the values' layout scatters a token over 64 sectors, so
+// moving it byte by byte would cost up to 16 times the traffic.  Tiles that are
+// no whole record (decode steps, the ends of a prompt, tokens in another
+// order) go byte by byte, straight to the cache.
 #include "w4_kv.cuh"
 
 namespace w4 {
 namespace {
 
-constexpr int kKvThreads = 256;
+constexpr int kKvThreads = 128, kKvWarps = kKvThreads / 32;
+
+// The tile's tokens: list indexes i0 .. i0 + 15 of which [lo, hi) are there.
+struct Tile16 {
+    long long page_record[kRecTokens];
+    int in_page[kRecTokens];
+    int position[kRecTokens];
+    int valid[kRecTokens];
+};
+
+// Fills the tile of this block; returns the list index of its token 0, or a
+// negative number's worth of nothing: `count` is 0 when no token is there.
+// whole: the tokens are one record.  All threads call.
+__device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &list, int tiles,
+                                         int rotation_rows, Tile16 *tile, int *first, int *count,
+                                         bool *whole) {
+    const int b = blockIdx.x / tiles, j = blockIdx.x - b * tiles;
+    const int base = b * list.run;
+    const int shift = list.positions[base] & (kRecTokens - 1);
+    const int i0 = j * kRecTokens - shift;
+    *first = max(0, -i0);
+    *count = min(kRecTokens, list.run - i0) - *first;
+    if (*count <= 0) return 0;
+    const int r = threadIdx.x;
+    if (r < kRecTokens) {
+        TokenPlace at = {};
+        const bool there = r >= *first && r < *first + *count;
+        // (one block of a tile's heads records what is out of range)
+        const bool ok = there && kv_place(pool, list, base + i0 + r, rotation_rows, &at);
+        tile->valid[r] = ok;
+        tile->in_page[r] = at.in_page;
+        tile->position[r] = at.position;
+        tile->page_record[r] = at.page_record;
+    }
+    __syncthreads();
+    bool same = true;
+    if (r < kRecTokens)
+        same = tile->valid[r] && tile->page_record[r] == tile->page_record[0] &&
+               tile->in_page[r] == tile->in_page[0] + r && tile->in_page[0] % kRecTokens == 0;
+    *whole = __syncthreads_and(same);
+    return base + i0;
+}
 
 __device__ __forceinline__ float clampf(float v, float a, float b) {
     return fminf(fmaxf(v, a), b);
 }
 
-__device__ __forceinline__ float2 load_pair(const Heads &x, int t, int h, int d) {
-    const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(x.data) +
-                             t * x.token_stride + h * x.head_stride + d;
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+// rint(w / s) for the correctly rounded quotient (NaN: 0), with r = rcp_rn(s)
+// and tol = T * 2^-21, T >= |w r|: w r is within 2^-22.4 of the quotient's
+// magnitude, so the two round alike unless w r lies that close to a half; there
+// the division decides.
+__device__ __forceinline__ float rint_quotient(float w, float s, float r, float tol) {
+    const float t = __fmul_rn(w, r), n = rintf(t);
+    if (0.5f - fabsf(__fsub_rn(t, n)) > tol) return n;
+    const float q = rintf(__fdiv_rn(w, s));
+    return q == q ? q : 0.f;
 }
 
-__device__ __forceinline__ void store_pair(const Heads &x, int t, int h, int d, float2 v) {
-    __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(x.data) + t * x.token_stride +
-                       h * x.head_stride + d;
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
-}
-
-// Values d, d + 1 (d even) of a head, rotated by row pos.
-__device__ __forceinline__ float2 load_turned(const Heads &x, int t, int h, int d,
-                                              const Rotation &rot, int pos) {
-    const float2 own = load_pair(x, t, h, d);
-    if (!rot.table || d >= 2 * rot.pairs) return own;
-    const float *row = rot.table + 2LL * pos * rot.pairs;
-    if (rot.layout == W4_ROPE_INTERLEAVED) {
-        const float2 cs = *reinterpret_cast<const float2 *>(row + d);
-        return make_float2(__fsub_rn(__fmul_rn(own.x, cs.x), __fmul_rn(own.y, cs.y)),
-                           __fadd_rn(__fmul_rn(own.y, cs.x), __fmul_rn(own.x, cs.y)));
-    }
-    const bool first = d < rot.pairs;
-    const int i = first ? d : d - rot.pairs;
-    const float2 other = load_pair(x, t, h, first ? d + rot.pairs : i);
-    const float4 cs = *reinterpret_cast<const float4 *>(row + 2 * i);
-    if (first)
-        return make_float2(__fsub_rn(__fmul_rn(own.x, cs.x), __fmul_rn(other.x, cs.y)),
-                           __fsub_rn(__fmul_rn(own.y, cs.z), __fmul_rn(other.y, cs.w)));
-    return make_float2(__fadd_rn(__fmul_rn(own.x, cs.x), __fmul_rn(other.x, cs.y)),
-                       __fadd_rn(__fmul_rn(own.y, cs.z), __fmul_rn(other.y, cs.w)));
-}
-
-// One warp per (token, head of k, v or q).
+// D / 8 lanes take a row (a head of a token), 8 values a lane; a warp 256 / D
+// rows at a time, of one token: v, k, then the q heads of this block.
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvThreads)
 append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, TokenList list,
-              Rotation rot) {
+              Rotation rot, int tiles) {
     using L = KvLayout<FMT, D>;
+    constexpr int LANES = D / 8, ROWS = 32 / LANES;
+    __shared__ Tile16 tile;
+    __shared__ __align__(16) unsigned char staged[L::kBytes];
     begin_after_previous();
-    const int lane = threadIdx.x & 31;
-    const int heads = 2 * pool.kv_heads + q_heads;
-    const long long n = (long long)list.tokens * heads;
-    for (long long w = ((long long)blockIdx.x * kKvThreads + threadIdx.x) >> 5; w < n;
-         w += (long long)gridDim.x * (kKvThreads / 32)) {
-        const int t = (int)(w / heads), row = (int)(w % heads);
-        TokenPlace at;
-        if (!kv_place(pool, list, t, rot.table ? rot.rows : 0x7FFFFFFF, &at)) continue;
-        float2 x[D / 64];
-        if (row >= 2 * pool.kv_heads) {
-            const int h = row - 2 * pool.kv_heads;
+    int first, count;
+    bool whole;
+    const int i0 = load_tile(pool, list, tiles, rot.table ? rot.rows : 0x7FFFFFFF, &tile, &first,
+                             &count, &whole);
+    if (count <= 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
+    const int h = blockIdx.y;
+    const int my_q = q_heads > h ? (q_heads - h + pool.kv_heads - 1) / pool.kv_heads : 0;
+    const int steps = (2 + my_q + ROWS - 1) / ROWS;           // of a token
+    for (int it = warp; it < count * steps; it += kKvWarps) {
+        const int n = it / steps, r = first + n;
+        const int row = (it - n * steps) * ROWS + lane / LANES;
+        const bool valid = tile.valid[r] && row < 2 + my_q;
+        const int t = i0 + r, pos = tile.position[r];
+        const bool is_v = row == 0, is_q = row >= 2;
+        const int head = is_q ? h + (row - 2) * pool.kv_heads : h;
+        const Heads &src = is_q ? q : is_v ? v : k;
+        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+        if (valid)
+            raw = *reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const __nv_bfloat16 *>(src.data) + t * src.token_stride +
+                head * src.head_stride + 8 * c);
+        float x[8];
+        const uint32_t *w = &raw.x;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j)
-                x[j] = load_turned(q, t, h, 64 * j + 2 * lane, rot, at.position);
-            __syncwarp();                  // q_out may be q: all loads before any store
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16_low(w[i]), x[2 * i + 1] = bf16_high(w[i]);
+        if (rot.table) {
+            const bool turns = valid && !is_v && 8 * c < 2 * rot.pairs;
+            const float *row_of = rot.table + 2LL * (valid ? pos : 0) * rot.pairs;
+            if (rot.layout == W4_ROPE_INTERLEAVED) {
+                if (turns) {
+                    const float4 *tab = reinterpret_cast<const float4 *>(row_of + 8 * c);
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) store_pair(q_out, t, h, 64 * j + 2 * lane, x[j]);
-            continue;
-        }
-        const bool is_v = row >= pool.kv_heads;
-        const int h = is_v ? row - pool.kv_heads : row;
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 cs = tab[i];
+                        const float2 y0 = turn_pair(x[4 * i], x[4 * i + 1], make_float2(cs.x, cs.y));
+                        const float2 y1 =
+                            turn_pair(x[4 * i + 2], x[4 * i + 3], make_float2(cs.z, cs.w));
+                        x[4 * i] = y0.x, x[4 * i + 1] = y0.y;
+                        x[4 * i + 2] = y1.x, x[4 * i + 3] = y1.y;
+                    }
+                }
+            } else {
+                // the partners are another lane's values
+                const int half = rot.pairs / 8;
+                const bool upper = c >= half;
+                const int from = lane - c + (upper ? c - half : c + half);
+                uint32_t p[4];
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-            x[j] = is_v ? load_pair(v, t, h, 64 * j + 2 * lane)
-                        : load_turned(k, t, h, 64 * j + 2 * lane, rot, at.position);
-        const int r = at.in_page % kRecTokens;
-        char *rec = pool.records + (at.page_record + (long long)h * pool.page_records +
-                                    at.in_page / kRecTokens) * L::kBytes;
-        if constexpr (FMT == W4_KV_BF16) {
+                for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xFFFFFFFFu, w[i], from & 31);
+                if (turns) {
+                    const float4 *tab = reinterpret_cast<const float4 *>(
+                        row_of + 16 * (upper ? c - half : c));
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const int d = 64 * j + 2 * lane;
-                *reinterpret_cast<__nv_bfloat162 *>(rec + (is_v ? L::value(r, d) : L::key(r, d))) =
-                    __floats2bfloat162_rn(x[j].x, x[j].y);
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 cs = tab[i];
+                        const float p0 = bf16_low(p[i]), p1 = bf16_high(p[i]);
+                        const float2 y0 = upper ? turn_pair(p0, x[2 * i], make_float2(cs.x, cs.y))
+                                                : turn_pair(x[2 * i], p0, make_float2(cs.x, cs.y));
+                        const float2 y1 =
+                            upper ? turn_pair(p1, x[2 * i + 1], make_float2(cs.z, cs.w))
+                                  : turn_pair(x[2 * i + 1], p1, make_float2(cs.z, cs.w));
+                        x[2 * i] = upper ? y0.y : y0.x;
+                        x[2 * i + 1] = upper ? y1.y : y1.x;
+                    }
+                }
             }
+        }
+        const uint4 packed = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
+                                        bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+        if (valid && is_q)
+            *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(q_out.data) +
+                                       t * q_out.token_stride + head * q_out.head_stride + 8 * c) =
+                packed;
+        // warps that only turn q are done here (row 0 and 1 are in one step)
+        if ((it - n * steps) > 0) continue;
+        const bool keeps = valid && !is_q;
+        const int in = tile.in_page[r], rr = in % kRecTokens;
+        unsigned char *rec =
+            whole ? staged
+                  : reinterpret_cast<unsigned char *>(pool.records) +
+                        (tile.page_record[r] + (long long)h * pool.page_records +
+                         in / kRecTokens) * L::kBytes;
+        if constexpr (FMT == W4_KV_BF16) {
+            if (keeps)
+                *reinterpret_cast<uint4 *>(rec + (is_v ? L::value(rr, 8 * c) : L::key(rr, 8 * c))) =
+                    packed;
         } else {
             float lo = 0.f, hi = 0.f;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                lo = fminf(lo, fminf(x[j].x, x[j].y));
-                hi = fmaxf(hi, fmaxf(x[j].x, x[j].y));
-            }
+            for (int i = 0; i < 8; ++i) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
+            for (int o = LANES / 2; o > 0; o >>= 1) {
                 lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
                 hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
             }
@@ -108,134 +187,182 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
                 __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), top), 65504.f));
             const float s = __half2float(sh);
             const float z = s == 0.f ? 0.f : clampf(rintf(__fdiv_rn(-lo, s)), 0.f, top);
-            const auto code = [&](float w) {
-                if (s == 0.f) return 0;
-                // NaN: rintf gives NaN, and clampf's fmaxf takes 0 for it after z
-                return (int)clampf((w == w ? rintf(__fdiv_rn(w, s)) : 0.f) + z, 0.f, top);
-            };
+            const float rcp = s == 0.f ? 0.f : __frcp_rn(s);
+            const float tol = __fmul_rn(__fmul_rn(fmaxf(-lo, hi), rcp), 0x1p-21f);
+            uint32_t code[2] = {0u, 0u};                      // 8 codes, a byte each
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const int d = 64 * j + 2 * lane;
-                const int c0 = code(x[j].x), c1 = code(x[j].y);
-                if constexpr (FMT == W4_KV_INT8) {
-                    if (is_v) {
-                        rec[L::value(r, d)] = (char)c0;
-                        rec[L::value(r, d + 1)] = (char)c1;
-                    } else {
-                        *reinterpret_cast<uint16_t *>(rec + L::key(r, d)) =
-                            (uint16_t)(c0 | c1 << 8);
+            for (int i = 0; i < 8; ++i) {
+                const float f =
+                    s == 0.f ? 0.f : clampf(rint_quotient(x[i], s, rcp, tol) + z, 0.f, top);
+                code[i / 4] |= (uint32_t)f << (8 * (i % 4));
+            }
+            if constexpr (FMT == W4_KV_INT8) {
+                if (keeps && !is_v)
+                    *reinterpret_cast<uint2 *>(rec + L::key(rr, 8 * c)) =
+                        make_uint2(code[0], code[1]);
+                if (keeps && is_v) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        rec[L::value(rr, 8 * c + i)] = (unsigned char)(code[i / 4] >> 8 * (i % 4));
+                }
+            } else {
+                // the other nibble of a value's byte is 8 values on: the next
+                // lane's (each of the two writes half of the bytes)
+                const uint32_t other0 = __shfl_xor_sync(0xFFFFFFFFu, code[0], 1);
+                const uint32_t other1 = __shfl_xor_sync(0xFFFFFFFFu, code[1], 1);
+                if (keeps && !is_v) {
+                    uint32_t bytes = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t two = code[i / 2] >> (16 * (i % 2));
+                        bytes |= ((two & 15u) | (two >> 4 & 0xF0u)) << (8 * i);
                     }
-                } else {
-                    const int up0 = __shfl_down_sync(0xFFFFFFFFu, c0, 4);
-                    const int up1 = __shfl_down_sync(0xFFFFFFFFu, c1, 4);
-                    if (!is_v) {
-                        rec[L::key(r, d)] = (char)(c0 | c1 << 4);
-                    } else if (!(d & 8)) {
-                        rec[L::value(r, d)] = (char)(c0 | up0 << 4);
-                        rec[L::value(r, d + 1)] = (char)(c1 | up1 << 4);
-                    }
+                    *reinterpret_cast<uint32_t *>(rec + L::key(rr, 8 * c)) = bytes;
+                }
+                if (keeps && is_v) {
+                    const bool odd = c & 1;
+                    const uint32_t both = odd ? other1 | code[1] << 4 : code[0] | other0 << 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        rec[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i)] =
+                            (unsigned char)(both >> 8 * i);
                 }
             }
-            if (lane == 0)
-                *reinterpret_cast<uint32_t *>(rec + (is_v ? L::kMetaV : L::kMeta) + 4 * r) =
+            if (keeps && c == 0)
+                *reinterpret_cast<uint32_t *>(rec + (is_v ? L::kMetaV : L::kMeta) + 4 * rr) =
                     (uint32_t)__half_as_ushort(sh) | (uint32_t)z << 16;
         }
     }
+    if (!whole) return;
+    __syncthreads();
+    uint4 *out = reinterpret_cast<uint4 *>(
+        pool.records + (tile.page_record[0] + (long long)h * pool.page_records +
+                        tile.in_page[0] / kRecTokens) * L::kBytes);
+    for (int i = threadIdx.x; i < L::kBytes / 16; i += kKvThreads)
+        out[i] = reinterpret_cast<const uint4 *>(staged)[i];
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvThreads)
-read_kernel(KvPool pool, Heads k, Heads v, TokenList list) {
+read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles) {
     using L = KvLayout<FMT, D>;
+    constexpr int LANES = D / 8, TOKENS = 16 / LANES;         // tokens a warp takes at a time
+    __shared__ Tile16 tile;
+    __shared__ __align__(16) unsigned char staged[L::kBytes];
     begin_after_previous();
-    const int lane = threadIdx.x & 31;
-    const int heads = 2 * pool.kv_heads;
-    const long long n = (long long)list.tokens * heads;
-    for (long long w = ((long long)blockIdx.x * kKvThreads + threadIdx.x) >> 5; w < n;
-         w += (long long)gridDim.x * (kKvThreads / 32)) {
-        const int t = (int)(w / heads), row = (int)(w % heads);
-        const bool is_v = row >= pool.kv_heads;
-        const int h = is_v ? row - pool.kv_heads : row;
-        if (!(is_v ? v : k).data) continue;
-        TokenPlace at;
-        if (!kv_place(pool, list, t, 0x7FFFFFFF, &at)) continue;
-        const int r = at.in_page % kRecTokens;
-        const char *rec = pool.records + (at.page_record + (long long)h * pool.page_records +
-                                          at.in_page / kRecTokens) * L::kBytes;
-        float s = 0.f;
-        int z = 0;
-        if constexpr (FMT != W4_KV_BF16) {
-            const uint32_t m = *reinterpret_cast<const uint32_t *>(
-                rec + (is_v ? L::kMetaV : L::kMeta) + 4 * r);
-            s = __half2float(__ushort_as_half((unsigned short)(m & 0xFFFFu)));
-            z = (int)(m >> 16);
-        }
+    int first, count;
+    bool whole;
+    const int i0 = load_tile(pool, list, tiles, 0x7FFFFFFF, &tile, &first, &count, &whole);
+    if (count <= 0) return;
+    const int h = blockIdx.y;
+    if (whole) {
+        const uint4 *in = reinterpret_cast<const uint4 *>(
+            pool.records + (tile.page_record[0] + (long long)h * pool.page_records +
+                            tile.in_page[0] / kRecTokens) * L::kBytes);
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            const int d = 64 * j + 2 * lane;
-            const int at0 = is_v ? L::value(r, d) : L::key(r, d);
-            const int at1 = is_v ? L::value(r, d + 1) : L::key(r, d + 1);
-            float2 x;
-            if constexpr (FMT == W4_KV_BF16) {
-                x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(rec + at0));
-            } else {
-                int c0 = (uint8_t)rec[at0], c1 = (uint8_t)rec[at1];
-                if constexpr (FMT == W4_KV_INT4) {
-                    c0 = is_v ? (d & 8 ? c0 >> 4 : c0 & 15) : c0 & 15;
-                    c1 = is_v ? (d & 8 ? c1 >> 4 : c1 & 15) : c1 >> 4;
-                }
-                x = make_float2(__fmul_rn((float)(c0 - z), s), __fmul_rn((float)(c1 - z), s));
-            }
-            store_pair(is_v ? v : k, t, h, d, x);
+        for (int i = 0; i < (L::kBytes / 16 + kKvThreads - 1) / kKvThreads; ++i) {
+            const int at = i * kKvThreads + threadIdx.x;
+            if (at < L::kBytes / 16) reinterpret_cast<uint4 *>(staged)[at] = in[at];
         }
+        __syncthreads();
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
+    // 2 LANES lanes take a token: its key, then its value
+    for (int n = warp * TOKENS + lane / (2 * LANES); n < count; n += kKvWarps * TOKENS) {
+        const int r = first + n;
+        const bool is_v = lane / LANES & 1;
+        const Heads &dst = is_v ? v : k;
+        if (!tile.valid[r] || !dst.data) continue;
+        const int in = tile.in_page[r], rr = in % kRecTokens;
+        const unsigned char *rec =
+            whole ? staged
+                  : reinterpret_cast<const unsigned char *>(pool.records) +
+                        (tile.page_record[r] + (long long)h * pool.page_records +
+                         in / kRecTokens) * L::kBytes;
+        uint4 packed;
+        if constexpr (FMT == W4_KV_BF16) {
+            packed = *reinterpret_cast<const uint4 *>(
+                rec + (is_v ? L::value(rr, 8 * c) : L::key(rr, 8 * c)));
+        } else {
+            const uint32_t m = *reinterpret_cast<const uint32_t *>(
+                rec + (is_v ? L::kMetaV : L::kMeta) + 4 * rr);
+            const float s = __half2float(__ushort_as_half((unsigned short)(m & 0xFFFFu)));
+            const int z = (int)(m >> 16);
+            uint32_t code[2] = {0u, 0u};
+            if constexpr (FMT == W4_KV_INT8) {
+                if (!is_v) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(rec + L::key(rr, 8 * c));
+                    code[0] = w.x, code[1] = w.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        code[i / 4] |= (uint32_t)rec[L::value(rr, 8 * c + i)] << (8 * (i % 4));
+                }
+            } else if (!is_v) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + L::key(rr, 8 * c));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    code[i / 4] |= (w >> (4 * i) & 15u) << (8 * (i % 4));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    code[i / 4] |= ((uint32_t)rec[L::value(rr, 8 * c + i)] >> (4 * (c & 1)) & 15u)
+                                   << (8 * (i % 4));
+            }
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = __fmul_rn((float)((int)(code[i / 4] >> (8 * (i % 4)) & 255u) - z), s);
+            packed = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
+                                bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+        }
+        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(dst.data) +
+                                   (i0 + r) * dst.token_stride + h * dst.head_stride + 8 * c) =
+            packed;
     }
 }
 
-int grid_for(long long warps, int num_sms) {
-    const long long blocks = (warps + kKvThreads / 32 - 1) / (kKvThreads / 32);
-    const long long cap = 8LL * num_sms;
-    return (int)(blocks < cap ? blocks : cap);
-}
+// Tiles that a run of `run` tokens can touch, wherever in a record it starts.
+int tiles_of(int run) { return (run + 2 * (kRecTokens - 1)) / kRecTokens; }
 
 template <int D>
 cudaError_t append_dim(const KvPool &pool, int format, const Heads &k, const Heads &v,
                        const Heads &q, const Heads &q_out, int q_heads, const TokenList &list,
-                       const Rotation &rot, int num_sms, cudaStream_t stream) {
-    const dim3 grid(grid_for((long long)list.tokens * (2 * pool.kv_heads + q_heads), num_sms));
+                       const Rotation &rot, cudaStream_t stream) {
+    const int tiles = tiles_of(list.run);
+    const dim3 grid((unsigned)(list.tokens / list.run * tiles), (unsigned)pool.kv_heads);
     const auto kernel = format == W4_KV_BF16   ? append_kernel<W4_KV_BF16, D>
                         : format == W4_KV_INT8 ? append_kernel<W4_KV_INT8, D>
                                                : append_kernel<W4_KV_INT4, D>;
     return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, q, q_out,
-                             q_heads, list, rot);
+                             q_heads, list, rot, tiles);
 }
 
 template <int D>
 cudaError_t read_dim(const KvPool &pool, int format, const Heads &k, const Heads &v,
-                     const TokenList &list, int num_sms, cudaStream_t stream) {
-    const dim3 grid(grid_for((long long)list.tokens * 2 * pool.kv_heads, num_sms));
+                     const TokenList &list, cudaStream_t stream) {
+    const int tiles = tiles_of(list.run);
+    const dim3 grid((unsigned)(list.tokens / list.run * tiles), (unsigned)pool.kv_heads);
     const auto kernel = format == W4_KV_BF16   ? read_kernel<W4_KV_BF16, D>
                         : format == W4_KV_INT8 ? read_kernel<W4_KV_INT8, D>
                                                : read_kernel<W4_KV_INT4, D>;
-    return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, list);
+    return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, list, tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const Heads &k,
                              const Heads &v, const Heads &q, const Heads &q_out, int q_heads,
-                             const TokenList &list, const Rotation &rot, int num_sms,
-                             cudaStream_t stream) {
-    return head_dim == 64 ? append_dim<64>(pool, format, k, v, q, q_out, q_heads, list, rot,
-                                           num_sms, stream)
-                          : append_dim<128>(pool, format, k, v, q, q_out, q_heads, list, rot,
-                                            num_sms, stream);
+                             const TokenList &list, const Rotation &rot, cudaStream_t stream) {
+    return head_dim == 64
+               ? append_dim<64>(pool, format, k, v, q, q_out, q_heads, list, rot, stream)
+               : append_dim<128>(pool, format, k, v, q, q_out, q_heads, list, rot, stream);
 }
 
 cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,
-                           const Heads &v, const TokenList &list, int num_sms,
-                           cudaStream_t stream) {
-    return head_dim == 64 ? read_dim<64>(pool, format, k, v, list, num_sms, stream)
-                          : read_dim<128>(pool, format, k, v, list, num_sms, stream);
+                           const Heads &v, const TokenList &list, cudaStream_t stream) {
+    return head_dim == 64 ? read_dim<64>(pool, format, k, v, list, stream)
+                          : read_dim<128>(pool, format, k, v, list, stream);
 }
 
 }  // namespace w4

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -419,12 +420,11 @@ RECORD_TOKENS = 16        # tokens of a cache record; page sizes are multiples o
 _I64 = ctypes.c_int64
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64)]
-
-
-class _Rotation(ctypes.Structure):
-    _fields_ = [("table", _P), ("rows", _I), ("rotary_dim", _I), ("layout", _I)]
+# w4_heads, w4_rotation and w4_block_table as bytes: these calls are a few
+# microseconds long, and ctypes structures would cost a good part of that.
+_pack_heads = struct.Struct("=Qqq").pack
+_pack_rotation = struct.Struct("=Qiii4x").pack
+_pack_table = struct.Struct("=Qiiq").pack
 
 
 class _RopeSpec(ctypes.Structure):
@@ -439,10 +439,6 @@ class _KvCache(ctypes.Structure):
                 ("page_tokens", _I), ("pages", _I), ("error", _P)]
 
 
-class _BlockTable(ctypes.Structure):
-    _fields_ = [("pages", _P), ("seqs", _I), ("width", _I), ("stride", _I64)]
-
-
 _rope_table = _decl("w4_rope_table", _ST, _P, _I, _P, _P)
 _rope = _decl("w4_rope", _ST, _P, _P, _I, _I, _I, _P, _P, _P, _P)
 _kv_pool_bytes = _decl("w4_kv_pool_bytes", _ST, _P, ctypes.POINTER(ctypes.c_size_t))
@@ -455,36 +451,38 @@ _paged_attn = _decl("w4_paged_attn", _ST, *_ATTN_ARGS)
 _paged_attn_f32 = _decl("w4_paged_attn_f32", _ST, *_ATTN_ARGS)
 
 
-def _heads(t, dtype=torch.bfloat16) -> _Heads | None:
+def _heads(t, dtype=torch.bfloat16) -> bytes | None:
     """[tokens, heads, head_dim] with a contiguous last dimension, as w4_heads."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 3:
-        raise ValueError(f"expected a {dtype} tensor [tokens, heads, head_dim]")
+    if t.dtype is not dtype or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"expected a {dtype} CUDA tensor [tokens, heads, head_dim]")
     st, sh, sd = t.stride()
     if sd != 1 and t.shape[2] > 1:
         raise ValueError("the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), st, sh)
+    return _pack_heads(t.data_ptr(), st, sh)
 
 
 def _int32(t, n: int, what: str) -> int | None:
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() != n:
-        raise ValueError(f"{what}: expected {n} int32 values")
-    return _ptr(t)
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous int32 values on the device")
+    return t.data_ptr()
 
 
-def _block_table(t) -> _BlockTable:
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
+def _block_table(t) -> bytes:
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.stride(1) != 1 or not t.is_cuda:
         raise ValueError("block table: expected a CUDA int32 tensor [seqs, pages]")
-    return _BlockTable(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]))
+    seqs, width = t.shape
+    return _pack_table(t.data_ptr(), seqs, width, max(t.stride(0), width))
 
 
-def _ref(struct):
-    return None if struct is None else ctypes.byref(struct)
+def _raw_stream(stream, like) -> int:
+    """As _stream, without making a Stream object for the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def rope_table(spec: dict, rows: int, table, stream=None) -> None:
@@ -507,9 +505,8 @@ def rope(x, y, positions, rotation: "RopeTable", error=None, stream=None) -> Non
     T, H, D = x.shape
     if y.shape != x.shape:
         raise ValueError("y: expected the shape of x")
-    _ok(_rope(ctypes.byref(_heads(x)), ctypes.byref(_heads(y)), T, H, D,
-              _int32(positions, T, "positions"), ctypes.byref(rotation.struct), _ptr(error),
-              _stream(stream, x)), "w4_rope")
+    _ok(_rope(_heads(x), _heads(y), T, H, D, _int32(positions, T, "positions"), rotation.packed,
+              _ptr(error), _raw_stream(stream, x)), "w4_rope")
 
 
 def kv_pool_bytes(fmt: int, kv_heads: int, head_dim: int, page_tokens: int, pages: int) -> int:
@@ -529,11 +526,10 @@ def kv_append(cache: "PagedCache", k, v, positions, table, seq_ids=None, q=None,
     if q is not None and (q.shape[0] != T or q.shape[2] != cache.head_dim or q_out is None
                           or q_out.shape != q.shape):
         raise ValueError("q, q_out: expected [tokens, q_heads, head_dim]")
-    _ok(_kv_append(cache.ref, _ref(_heads(k)), _ref(_heads(v)), _ref(_heads(q)),
-                   _ref(_heads(q_out)), 0 if q is None else q.shape[1], T,
-                   _int32(positions, T, "positions"), _int32(seq_ids, T, "seq_ids"),
-                   _ref(_block_table(table)), _ref(rotation and rotation.struct),
-                   _stream(stream, k)), "w4_kv_append")
+    _ok(_kv_append(cache.ref, _heads(k), _heads(v), _heads(q), _heads(q_out),
+                   0 if q is None else q.shape[1], T, _int32(positions, T, "positions"),
+                   _int32(seq_ids, T, "seq_ids"), _block_table(table),
+                   rotation and rotation.packed, _raw_stream(stream, k)), "w4_kv_append")
 
 
 def kv_read(cache: "PagedCache", k_out, v_out, positions, table, seq_ids=None,
@@ -543,9 +539,9 @@ def kv_read(cache: "PagedCache", k_out, v_out, positions, table, seq_ids=None,
     for x in (k_out, v_out):
         if x is not None and x.shape != (T, cache.kv_heads, cache.head_dim):
             raise ValueError("k_out, v_out: expected [tokens, kv_heads, head_dim]")
-    _ok(_kv_read(cache.ref, _ref(_heads(k_out)), _ref(_heads(v_out)), T,
+    _ok(_kv_read(cache.ref, _heads(k_out), _heads(v_out), T,
                  _int32(positions, T, "positions"), _int32(seq_ids, T, "seq_ids"),
-                 _ref(_block_table(table)), _stream(stream, positions)), "w4_kv_read")
+                 _block_table(table), _raw_stream(stream, positions)), "w4_kv_read")
 
 
 def paged_attn_workspace_bytes(cache: "PagedCache") -> int:
@@ -562,10 +558,10 @@ def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, work
         raise ValueError("q, out: expected [seqs * tokens, q_heads, head_dim]")
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != T * H):
         raise ValueError("lse: expected float32 [seqs * tokens, q_heads]")
-    _ok(fn(cache.ref, ctypes.byref(_heads(q)), ctypes.byref(_heads(out, dtype)), H, T // B,
-           _int32(lens, B, "lens"), ctypes.byref(_block_table(table)),
-           D ** -0.5 if scale is None else scale, window, _ptr(lse), _ptr(workspace),
-           workspace.numel() * workspace.element_size(), _stream(stream, q)), where)
+    _ok(fn(cache.ref, _heads(q), _heads(out, dtype), H, T // B, _int32(lens, B, "lens"),
+           _block_table(table), D ** -0.5 if scale is None else scale, window, _ptr(lse),
+           _ptr(workspace), workspace.numel() * workspace.element_size(),
+           _raw_stream(stream, q)), where)
 
 
 def paged_attn(cache: "PagedCache", q, out, lens, table, workspace, scale=None, window: int = 0,
@@ -591,7 +587,7 @@ class RopeTable:
         if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32:
             raise ValueError("table: expected float32 [rows, rotary_dim/2, 2]")
         self.table, self.layout = table, layout
-        self.struct = _Rotation(_ptr(table), table.shape[0], 2 * table.shape[1], layout)
+        self.packed = _pack_rotation(_ptr(table), table.shape[0], 2 * table.shape[1], layout)
 
     @classmethod
     def make(cls, rows: int, rotary_dim: int, base: float, layout: int = ROPE_HALF, device=None,
