@@ -591,8 +591,8 @@ w4_status w4_kv_pool_bytes(const w4_kv_cache *cache, size_t *bytes);
  *   rotation  : NULL for none; rotary_dim a multiple of 16, at most head_dim
  * A token that is out of range (position, sequence, page) is left out whole,
  * its q too, and recorded in cache->error.
- * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim, tokens * heads
- * >= 2^31), W4_ERR_CUDA.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim; 2^27 or more
+ * tokens x heads of k, v and q), W4_ERR_CUDA.
  */
 w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_heads *v,
                        const w4_heads *q, const w4_heads *q_out, int q_heads, int tokens,

@@ -90,7 +90,8 @@ cudaError_t launch_rope(const Heads &x, const Heads &y, int tokens, int heads, i
                         bool wide, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const Heads &k,
                              const Heads &v, const Heads &q, const Heads &q_out, int q_heads,
-                             const TokenList &list, const Rotation &rot, cudaStream_t stream);
+                             const TokenList &list, const Rotation &rot, int num_sms,
+                             cudaStream_t stream);
 cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,
                            const Heads &v, const TokenList &list, cudaStream_t stream);
 
@@ -128,6 +129,14 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// Units of a head that turn_unit takes (in place nothing is copied).
+inline int turn_units(const Heads &x, const Heads &y, int head_dim, const Rotation &rot) {
+    const bool in_place = x.data == y.data && x.token_stride == y.token_stride &&
+                          x.head_stride == y.head_stride;
+    return (rot.layout == W4_ROPE_HALF ? rot.pairs / 8 : rot.pairs / 4) +
+           (in_place ? 0 : (head_dim - 2 * rot.pairs) / 8);
 }
 
 #ifdef __CUDACC__
@@ -168,6 +177,57 @@ __device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 (&cs)[8])
     for (int i = 0; i < 4; ++i) {
         const float2 r = turn_pair(bf16_low(w[i]), bf16_high(w[i]), cs[i]);
         w[i] = bf16_pair(r.x, r.y);
+    }
+}
+
+// What one thread turns with 16-byte accesses: unit u of the heads h0, h0 +
+// groups, ... of a token, HEADS of them at most, all their loads under way
+// together and the unit's (cos, sin) in registers.  A unit is 8 values and their
+// 8 partners (half), 4 pairs (interleaved), or past the rotated part 8 values
+// to copy.  row: the table's; back: the transposed rotation.
+template <int LAYOUT, int HEADS>
+__device__ __forceinline__ void turn_unit(const Heads &x, const Heads &y, long long t, int u,
+                                          int h0, int groups, int heads, const Rotation &rot,
+                                          unsigned row, bool back) {
+    const int turned = LAYOUT == W4_ROPE_HALF ? rot.pairs / 8 : rot.pairs / 4;
+    const bool turns = u < turned;
+    const int d = LAYOUT == W4_ROPE_HALF && !turns ? 8 * (u + turned) : 8 * u;
+    float2 cs[8];
+    if (turns) {
+        const float4 *tab = reinterpret_cast<const float4 *>(
+            rot.table + 2 * ((long long)row * rot.pairs + (LAYOUT == W4_ROPE_HALF ? d : d / 2)));
+#pragma unroll
+        for (int i = 0; i < (LAYOUT == W4_ROPE_HALF ? 4 : 2); ++i) {
+            const float4 v = tab[i];
+            cs[2 * i] = make_float2(v.x, back ? -v.y : v.y);
+            cs[2 * i + 1] = make_float2(v.z, back ? -v.w : v.w);
+        }
+    }
+    const __nv_bfloat16 *in =
+        reinterpret_cast<const __nv_bfloat16 *>(x.data) + t * x.token_stride + d;
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(y.data) + t * y.token_stride + d;
+    uint4 a[HEADS], b[HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i * groups;
+        if (h >= heads) continue;
+        a[i] = *reinterpret_cast<const uint4 *>(in + h * x.head_stride);
+        if (LAYOUT == W4_ROPE_HALF && turns)
+            b[i] = *reinterpret_cast<const uint4 *>(in + h * x.head_stride + rot.pairs);
+    }
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i * groups;
+        if (h >= heads) continue;
+        if (turns) {
+            if constexpr (LAYOUT == W4_ROPE_HALF)
+                turn_halves(a[i], b[i], cs);
+            else
+                turn_neighbours(a[i], cs);
+        }
+        *reinterpret_cast<uint4 *>(out + h * y.head_stride) = a[i];
+        if (LAYOUT == W4_ROPE_HALF && turns)
+            *reinterpret_cast<uint4 *>(out + h * y.head_stride + rot.pairs) = b[i];
     }
 }
 

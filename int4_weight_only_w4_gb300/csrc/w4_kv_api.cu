@@ -91,7 +91,8 @@ w4_status list_ok(const w4_kv_cache *cache, const w4_block_table *table, int tok
     if (tokens > 0 && (!positions || !aligned(positions, 4) || !aligned(seq_ids, 4)))
         return W4_ERR_INVALID_ARG;
     if (!seq_ids && tokens % table->seqs) return W4_ERR_INVALID_ARG;
-    if ((long long)tokens * heads >= (1LL << 31)) return W4_ERR_UNSUPPORTED;
+    // (query units, 16 a head at most, are counted in 32 bits)
+    if ((long long)tokens * heads >= (1LL << 27)) return W4_ERR_UNSUPPORTED;
     return W4_OK;
 }
 
@@ -240,6 +241,8 @@ w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_hea
     if (q_heads > 0 && (!q->data || !q_out->data || !rows_aligned(q, 2) ||
                         !rows_aligned(q_out, 2)))
         return W4_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0) return W4_ERR_CUDA;
     w4::Rotation rot = {nullptr, 0, 0, 0};
     if (rotation)
         rot = {rotation->table, rotation->rows, rotation->rotary_dim / 2, rotation->layout};
@@ -247,7 +250,7 @@ w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_hea
                                 seq_ids ? tokens : tokens / table->seqs};
     return cuda_status(w4::launch_kv_append(
         pool_of(cache, table), cache->format, cache->head_dim, heads_of(k), heads_of(v),
-        heads_of(q), heads_of(q_out), q_heads, list, rot,
+        heads_of(q), heads_of(q_out), q_heads, list, rot, sms,
         reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -30,10 +30,10 @@ struct Tile16 {
 // Fills the tile of this block; returns the list index of its token 0, or a
 // negative number's worth of nothing: `count` is 0 when no token is there.
 // whole: the tokens are one record.  All threads call.
-__device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &list, int tiles,
-                                         int rotation_rows, Tile16 *tile, int *first, int *count,
+__device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &list, int tile_no,
+                                         int tiles, int rotation_rows, Tile16 *tile, int *first, int *count,
                                          bool *whole) {
-    const int b = blockIdx.x / tiles, j = blockIdx.x - b * tiles;
+    const int b = tile_no / tiles, j = tile_no - b * tiles;
     const int base = b * list.run;
     const int shift = list.positions[base] & (kRecTokens - 1);
     const int i0 = j * kRecTokens - shift;
@@ -75,39 +75,59 @@ __device__ __forceinline__ float rint_quotient(float w, float s, float r, float 
     return q == q ? q : 0.f;
 }
 
-// D / 8 lanes take a row (a head of a token), 8 values a lane; a warp 256 / D
-// rows at a time, of one token: v, k, then the q heads of this block.
-template <int FMT, int D>
+// The queries of a launch of append_kernel, turned as by w4_rope in blocks of
+// their own (in the rows' loop below every lane would turn its partner too:
+// 16 k tokens of 28 query heads 146 us against 84).
+struct Queries {
+    Heads q, out;
+    int heads;
+    unsigned groups, units;    // see turn_unit
+    unsigned all;              // tokens * groups * units
+    unsigned first_block;      // blocks from here on turn queries
+};
+
+// Keys and values: D / 8 lanes take a row (a head of a token), 8 values a lane;
+// a warp takes the key and value of 128 / D tokens at a time.
+template <int FMT, int D, int HEADS>
 __global__ void __launch_bounds__(kKvThreads)
-append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, TokenList list,
-              Rotation rot, int tiles) {
+append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation rot, int tiles) {
     using L = KvLayout<FMT, D>;
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;
+    constexpr int LANES = D / 8, TOKENS = 16 / LANES;
     __shared__ Tile16 tile;
     __shared__ __align__(16) unsigned char staged[L::kBytes];
     begin_after_previous();
+    if (blockIdx.x >= q.first_block) {
+        const unsigned e = (blockIdx.x - q.first_block) * kKvThreads + threadIdx.x;
+        if (e >= q.all) return;
+        const unsigned tg = e / q.units, u = e - tg * q.units, t = tg / q.groups;
+        TokenPlace at;
+        if (!kv_place(pool, list, t, rot.rows, &at)) return;
+        if (rot.layout == W4_ROPE_HALF)
+            turn_unit<W4_ROPE_HALF, HEADS>(q.q, q.out, t, u, tg - t * q.groups, q.groups, q.heads,
+                                           rot, at.position, false);
+        else
+            turn_unit<W4_ROPE_INTERLEAVED, HEADS>(q.q, q.out, t, u, tg - t * q.groups, q.groups,
+                                                  q.heads, rot, at.position, false);
+        return;
+    }
+    const int tile_no = blockIdx.x / pool.kv_heads, h = blockIdx.x - tile_no * pool.kv_heads;
     int first, count;
     bool whole;
-    const int i0 = load_tile(pool, list, tiles, rot.table ? rot.rows : 0x7FFFFFFF, &tile, &first,
+    const int i0 = load_tile(pool, list, tile_no, tiles, rot.table ? rot.rows : 0x7FFFFFFF, &tile, &first,
                              &count, &whole);
     if (count <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
-    const int h = blockIdx.y;
-    const int my_q = q_heads > h ? (q_heads - h + pool.kv_heads - 1) / pool.kv_heads : 0;
-    const int steps = (2 + my_q + ROWS - 1) / ROWS;           // of a token
-    for (int it = warp; it < count * steps; it += kKvWarps) {
-        const int n = it / steps, r = first + n;
-        const int row = (it - n * steps) * ROWS + lane / LANES;
-        const bool valid = tile.valid[r] && row < 2 + my_q;
+    for (int n0 = warp * TOKENS; n0 < count; n0 += kKvWarps * TOKENS) {
+        const int r = min(first + n0 + lane / (2 * LANES), kRecTokens - 1);
+        const bool valid = n0 + lane / (2 * LANES) < count && tile.valid[r];
         const int t = i0 + r, pos = tile.position[r];
-        const bool is_v = row == 0, is_q = row >= 2;
-        const int head = is_q ? h + (row - 2) * pool.kv_heads : h;
-        const Heads &src = is_q ? q : is_v ? v : k;
+        const bool is_v = lane / LANES & 1;
+        const Heads &src = is_v ? v : k;
         uint4 raw = make_uint4(0u, 0u, 0u, 0u);
         if (valid)
             raw = *reinterpret_cast<const uint4 *>(
                 reinterpret_cast<const __nv_bfloat16 *>(src.data) + t * src.token_stride +
-                head * src.head_stride + 8 * c);
+                h * src.head_stride + 8 * c);
         float x[8];
         const uint32_t *w = &raw.x;
 #pragma unroll
@@ -156,13 +176,6 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
         }
         const uint4 packed = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
                                         bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
-        if (valid && is_q)
-            *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(q_out.data) +
-                                       t * q_out.token_stride + head * q_out.head_stride + 8 * c) =
-                packed;
-        // warps that only turn q are done here (row 0 and 1 are in one step)
-        if ((it - n * steps) > 0) continue;
-        const bool keeps = valid && !is_q;
         const int in = tile.in_page[r], rr = in % kRecTokens;
         unsigned char *rec =
             whole ? staged
@@ -170,7 +183,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
                         (tile.page_record[r] + (long long)h * pool.page_records +
                          in / kRecTokens) * L::kBytes;
         if constexpr (FMT == W4_KV_BF16) {
-            if (keeps)
+            if (valid)
                 *reinterpret_cast<uint4 *>(rec + (is_v ? L::value(rr, 8 * c) : L::key(rr, 8 * c))) =
                     packed;
         } else {
@@ -197,10 +210,10 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
                 code[i / 4] |= (uint32_t)f << (8 * (i % 4));
             }
             if constexpr (FMT == W4_KV_INT8) {
-                if (keeps && !is_v)
+                if (valid && !is_v)
                     *reinterpret_cast<uint2 *>(rec + L::key(rr, 8 * c)) =
                         make_uint2(code[0], code[1]);
-                if (keeps && is_v) {
+                if (valid && is_v) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         rec[L::value(rr, 8 * c + i)] = (unsigned char)(code[i / 4] >> 8 * (i % 4));
@@ -210,7 +223,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
                 // lane's (each of the two writes half of the bytes)
                 const uint32_t other0 = __shfl_xor_sync(0xFFFFFFFFu, code[0], 1);
                 const uint32_t other1 = __shfl_xor_sync(0xFFFFFFFFu, code[1], 1);
-                if (keeps && !is_v) {
+                if (valid && !is_v) {
                     uint32_t bytes = 0u;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -219,7 +232,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
                     }
                     *reinterpret_cast<uint32_t *>(rec + L::key(rr, 8 * c)) = bytes;
                 }
-                if (keeps && is_v) {
+                if (valid && is_v) {
                     const bool odd = c & 1;
                     const uint32_t both = odd ? other1 | code[1] << 4 : code[0] | other0 << 4;
 #pragma unroll
@@ -228,7 +241,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Heads q, Heads q_out, int q_heads, 
                             (unsigned char)(both >> 8 * i);
                 }
             }
-            if (keeps && c == 0)
+            if (valid && c == 0)
                 *reinterpret_cast<uint32_t *>(rec + (is_v ? L::kMetaV : L::kMeta) + 4 * rr) =
                     (uint32_t)__half_as_ushort(sh) | (uint32_t)z << 16;
         }
@@ -252,7 +265,7 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles) {
     begin_after_previous();
     int first, count;
     bool whole;
-    const int i0 = load_tile(pool, list, tiles, 0x7FFFFFFF, &tile, &first, &count, &whole);
+    const int i0 = load_tile(pool, list, blockIdx.x, tiles, 0x7FFFFFFF, &tile, &first, &count, &whole);
     if (count <= 0) return;
     const int h = blockIdx.y;
     if (whole) {
@@ -325,17 +338,17 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles) {
 // Tiles that a run of `run` tokens can touch, wherever in a record it starts.
 int tiles_of(int run) { return (run + 2 * (kRecTokens - 1)) / kRecTokens; }
 
-template <int D>
-cudaError_t append_dim(const KvPool &pool, int format, const Heads &k, const Heads &v,
-                       const Heads &q, const Heads &q_out, int q_heads, const TokenList &list,
-                       const Rotation &rot, cudaStream_t stream) {
+template <int D, int HEADS>
+cudaError_t append_dim(const KvPool &pool, int format, const Heads &k, const Heads &v, Queries q,
+                       const TokenList &list, const Rotation &rot, cudaStream_t stream) {
     const int tiles = tiles_of(list.run);
-    const dim3 grid((unsigned)(list.tokens / list.run * tiles), (unsigned)pool.kv_heads);
-    const auto kernel = format == W4_KV_BF16   ? append_kernel<W4_KV_BF16, D>
-                        : format == W4_KV_INT8 ? append_kernel<W4_KV_INT8, D>
-                                               : append_kernel<W4_KV_INT4, D>;
-    return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, q, q_out,
-                             q_heads, list, rot, tiles);
+    q.first_block = (unsigned)(list.tokens / list.run * tiles) * pool.kv_heads;
+    const dim3 grid(q.first_block + (q.all + kKvThreads - 1) / kKvThreads);
+    const auto kernel = format == W4_KV_BF16   ? append_kernel<W4_KV_BF16, D, HEADS>
+                        : format == W4_KV_INT8 ? append_kernel<W4_KV_INT8, D, HEADS>
+                                               : append_kernel<W4_KV_INT4, D, HEADS>;
+    return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, q, list, rot,
+                             tiles);
 }
 
 template <int D>
@@ -353,10 +366,23 @@ cudaError_t read_dim(const KvPool &pool, int format, const Heads &k, const Heads
 
 cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const Heads &k,
                              const Heads &v, const Heads &q, const Heads &q_out, int q_heads,
-                             const TokenList &list, const Rotation &rot, cudaStream_t stream) {
-    return head_dim == 64
-               ? append_dim<64>(pool, format, k, v, q, q_out, q_heads, list, rot, stream)
-               : append_dim<128>(pool, format, k, v, q, q_out, q_heads, list, rot, stream);
+                             const TokenList &list, const Rotation &rot, int num_sms,
+                             cudaStream_t stream) {
+    Queries qs = {q, q_out, q_heads, 1, 1, 0, 0};
+    bool four = false;
+    if (q_heads > 0) {
+        // four heads a thread once that still gives every SM two blocks
+        qs.units = turn_units(q, q_out, head_dim, rot);
+        const long long by_four = (long long)list.tokens * ((q_heads + 3) / 4) * qs.units;
+        four = by_four >= 2LL * num_sms * kKvThreads;
+        qs.groups = four ? (q_heads + 3) / 4 : q_heads;
+        qs.all = (unsigned)((long long)list.tokens * qs.groups * qs.units);
+    }
+    if (head_dim == 64)
+        return four ? append_dim<64, 4>(pool, format, k, v, qs, list, rot, stream)
+                    : append_dim<64, 1>(pool, format, k, v, qs, list, rot, stream);
+    return four ? append_dim<128, 4>(pool, format, k, v, qs, list, rot, stream)
+                : append_dim<128, 1>(pool, format, k, v, qs, list, rot, stream);
 }
 
 cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,

@@ -75,12 +75,10 @@ rope_kernel(Heads x, Heads y, int tokens, int heads, int head_dim,
     }
 }
 
-// Rows on 16-byte boundaries.  A unit is what one thread turns with 16-byte
-// accesses: 8 values and their 8 partners (half) or 4 pairs (interleaved), or 8
-// values to copy.  A thread keeps its unit's (cos, sin) in registers over HEADS
-// heads, whose loads are all under way together.  Bound by HBM: 8192 tokens of
-// 32 heads of 128 in 23.6 us = 5780 GB/s, 85 % of the measured copy; the pair
-// kernel above took 112 us, with its 2-byte accesses.
+// Rows on 16-byte boundaries: a thread per unit of HEADS heads (turn_unit).
+// Bound by HBM: 8192 tokens of 32 heads of 128 in 23.4 us = 5830 GB/s, 86 % of
+// the measured copy; the pair kernel above takes 112 us, with its 2-byte
+// accesses.
 template <int LAYOUT, int HEADS>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_wide_kernel(Heads x, Heads y, unsigned units_all, int heads, unsigned groups, unsigned units,
@@ -95,47 +93,7 @@ rope_wide_kernel(Heads x, Heads y, unsigned units_all, int heads, unsigned group
         if (error && u == 0 && h0 == 0) atomicOr(error, W4_KV_ERR_POSITION);
         return;
     }
-    // first value of the unit, its partners' distance (0: none), pairs
-    const int turned = LAYOUT == W4_ROPE_HALF ? rot.pairs / 8 : rot.pairs / 4;
-    const bool turns = (int)u < turned;
-    const int d = LAYOUT == W4_ROPE_HALF && !turns ? 8 * (u + turned) : 8 * u;
-    float2 cs[8];
-    if (turns) {
-        const float4 *tab = reinterpret_cast<const float4 *>(
-            rot.table + 2 * ((long long)row * rot.pairs + (LAYOUT == W4_ROPE_HALF ? d : d / 2)));
-#pragma unroll
-        for (int i = 0; i < (LAYOUT == W4_ROPE_HALF ? 4 : 2); ++i) {
-            const float4 v = tab[i];
-            cs[2 * i] = make_float2(v.x, pos < 0 ? -v.y : v.y);
-            cs[2 * i + 1] = make_float2(v.z, pos < 0 ? -v.w : v.w);
-        }
-    }
-    const __nv_bfloat16 *in = reinterpret_cast<const __nv_bfloat16 *>(x.data) +
-                              t * x.token_stride + d;
-    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(y.data) + t * y.token_stride + d;
-    uint4 a[HEADS], b[HEADS];
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-        const int h = h0 + i * groups;
-        if (h >= heads) continue;
-        a[i] = *reinterpret_cast<const uint4 *>(in + h * x.head_stride);
-        if (LAYOUT == W4_ROPE_HALF && turns)
-            b[i] = *reinterpret_cast<const uint4 *>(in + h * x.head_stride + rot.pairs);
-    }
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-        const int h = h0 + i * groups;
-        if (h >= heads) continue;
-        if (turns) {
-            if constexpr (LAYOUT == W4_ROPE_HALF)
-                turn_halves(a[i], b[i], cs);
-            else
-                turn_neighbours(a[i], cs);
-        }
-        *reinterpret_cast<uint4 *>(out + h * y.head_stride) = a[i];
-        if (LAYOUT == W4_ROPE_HALF && turns)
-            *reinterpret_cast<uint4 *>(out + h * y.head_stride + rot.pairs) = b[i];
-    }
+    turn_unit<LAYOUT, HEADS>(x, y, t, u, h0, groups, heads, rot, row, pos < 0);
 }
 
 int grid_for(long long units, int num_sms) {
@@ -171,11 +129,7 @@ cudaError_t launch_rope(const Heads &x, const Heads &y, int tokens, int heads, i
                         const int32_t *positions, const Rotation &rot, uint32_t *error,
                         bool wide, int num_sms, cudaStream_t stream) {
     if (wide) {
-        // in place nothing is copied
-        const bool in_place = x.data == y.data && x.token_stride == y.token_stride &&
-                              x.head_stride == y.head_stride;
-        const int turned = rot.layout == W4_ROPE_HALF ? rot.pairs / 8 : rot.pairs / 4;
-        const int units = turned + (in_place ? 0 : (head_dim - 2 * rot.pairs) / 8);
+        const int units = turn_units(x, y, head_dim, rot);
         // four heads a thread once that still gives every SM two blocks
         const long long by_head = (long long)tokens * heads * units;
         const long long by_four = (long long)tokens * ((heads + 3) / 4) * units;
