@@ -93,7 +93,8 @@ cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const
                              const TokenList &list, const Rotation &rot, int num_sms,
                              cudaStream_t stream);
 cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,
-                           const Heads &v, const TokenList &list, cudaStream_t stream);
+                           const Heads &v, const TokenList &list, int num_sms,
+                           cudaStream_t stream);
 
 struct AttnArgs {
     KvPool pool;

@@ -264,10 +264,12 @@ w4_status w4_kv_read(const w4_kv_cache *cache, const w4_heads *k_out, const w4_h
     if (tokens == 0) return W4_OK;
     for (const w4_heads *h : {k_out, v_out})
         if (h && (!h->data || !rows_aligned(h, 2))) return W4_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0) return W4_ERR_CUDA;
     const w4::TokenList list = {positions, seq_ids, tokens,
                                 seq_ids ? tokens : tokens / table->seqs};
     return cuda_status(w4::launch_kv_read(pool_of(cache, table), cache->format, cache->head_dim,
-                                          heads_of(k_out), heads_of(v_out), list,
+                                          heads_of(k_out), heads_of(v_out), list, sms,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 

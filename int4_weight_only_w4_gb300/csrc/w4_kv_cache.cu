@@ -5,13 +5,13 @@
 // Q = 255 or 15 levels (include/w4.h), every operation rounded to nearest in
 // fp32, so the codes are those of any other evaluation of the rule bit for bit.
 //
-// A block takes a tile of up to 16 listed tokens and one key/value head, cut so
-// that the tokens of a sequence in order fall into whole records.  Such a
-// record is put together (or taken apart) in shared memory and moved with
-// 16-byte accesses; the values' layout scatters a token over 64 sectors, so
-// moving it byte by byte would cost up to 16 times the traffic.  Tiles that are
-// no whole record (decode steps, the ends of a prompt, tokens in another
-// order) go byte by byte, straight to the cache.
+// A tile is up to 16 listed tokens, cut so that the tokens of a sequence in
+// order fall into whole records.  A warp takes the keys, or the values, of a
+// tile and head; all its loads are under way together.  A whole record's
+// quantised values are put together (or taken apart) in shared memory and
+// moved with 16-byte accesses: their layout scatters a token over 64 sectors.
+// Tiles that are no whole record (decode steps, the ends of a prompt, tokens
+// in another order) go byte by byte.
 #include "w4_kv.cuh"
 
 namespace w4 {
@@ -21,18 +21,16 @@ constexpr int kKvThreads = 128, kKvWarps = kKvThreads / 32;
 
 // The tile's tokens: list indexes i0 .. i0 + 15 of which [lo, hi) are there.
 struct Tile16 {
-    long long page_record[kRecTokens];
-    int in_page[kRecTokens];
+    unsigned char *record[kRecTokens];    // of head 0; NULL: the token is left out
+    int in_record[kRecTokens];
     int position[kRecTokens];
-    int valid[kRecTokens];
 };
 
-// Fills the tile of this block; returns the list index of its token 0, or a
-// negative number's worth of nothing: `count` is 0 when no token is there.
-// whole: the tokens are one record.  All threads call.
+// Fills the tile of this block; returns the list index of its token 0; tokens
+// first .. first + count - 1 are there (count <= 0: none).  whole: the tokens are one record.  All threads call.
 __device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &list, int tile_no,
-                                         int tiles, int rotation_rows, Tile16 *tile, int *first, int *count,
-                                         bool *whole) {
+                                         int tiles, int rotation_rows, int record_bytes,
+                                         Tile16 *tile, int *first, int *count, bool *whole) {
     const int b = tile_no / tiles, j = tile_no - b * tiles;
     const int base = b * list.run;
     const int shift = list.positions[base] & (kRecTokens - 1);
@@ -46,33 +44,103 @@ __device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &li
         const bool there = r >= *first && r < *first + *count;
         // (one block of a tile's heads records what is out of range)
         const bool ok = there && kv_place(pool, list, base + i0 + r, rotation_rows, &at);
-        tile->valid[r] = ok;
-        tile->in_page[r] = at.in_page;
+        tile->record[r] = ok ? reinterpret_cast<unsigned char *>(pool.records) +
+                                   (at.page_record + at.in_page / kRecTokens) * record_bytes
+                             : nullptr;
+        tile->in_record[r] = at.in_page % kRecTokens;
         tile->position[r] = at.position;
-        tile->page_record[r] = at.page_record;
     }
     __syncthreads();
     bool same = true;
     if (r < kRecTokens)
-        same = tile->valid[r] && tile->page_record[r] == tile->page_record[0] &&
-               tile->in_page[r] == tile->in_page[0] + r && tile->in_page[0] % kRecTokens == 0;
+        same = tile->record[r] && tile->record[r] == tile->record[0] && tile->in_record[r] == r;
     *whole = __syncthreads_and(same);
     return base + i0;
 }
 
-__device__ __forceinline__ float clampf(float v, float a, float b) {
-    return fminf(fmaxf(v, a), b);
+// Two fp32 operations in one instruction, each rounded to nearest.
+union Two {
+    unsigned long long both;
+    float2 f;
+    int2 i;
+};
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.both) : "l"(a.both), "l"(b.both));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.both) : "l"(a.both), "l"(b.both));
+    return r;
+}
+__device__ __forceinline__ Two twice(float v) {
+    Two r;
+    r.f = make_float2(v, v);
+    return r;
 }
 
-// rint(w / s) for the correctly rounded quotient (NaN: 0), with r = rcp_rn(s)
-// and tol = T * 2^-21, T >= |w r|: w r is within 2^-22.4 of the quotient's
-// magnitude, so the two round alike unless w r lies that close to a half; there
-// the division decides.
-__device__ __forceinline__ float rint_quotient(float w, float s, float r, float tol) {
-    const float t = __fmul_rn(w, r), n = rintf(t);
-    if (0.5f - fabsf(__fsub_rn(t, n)) > tol) return n;
+__device__ __forceinline__ int rint_quotient(float w, float s) {
     const float q = rintf(__fdiv_rn(w, s));
-    return q == q ? q : 0.f;
+    return q == q ? (int)fminf(fmaxf(q, -512.f), 512.f) : 0;
+}
+
+// Zero point and codes of 8 of a row's values, of range [lo, hi]; s > 0.  The
+// rule wants rint(w / s), w / s the correctly rounded quotient.  With r within an
+// ulp of 1 / s, t = w r is within 2^-22.4 of the quotient's magnitude; adding and
+// subtracting 1.5 * 2^23 rounds t to the nearest integer (ties to even), and
+// where t is further than T * 2^-21 (T >= every |t| of the row) from a half,
+// that integer is the rule's.  In the rare other case the division decides.
+template <int BITS>
+__device__ __forceinline__ void codes_of(const float (&w)[8], float lo, float hi, float s,
+                                         int *zero, int (&n)[8]) {
+    constexpr float kMagic = 12582912.f;                      // 1.5 * 2^23
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const float tol = __fmul_rn(__fmul_rn(fmaxf(-lo, hi), r), 0x1p-21f);
+    const float tz = __fmul_rn(-lo, r), yz = __fadd_rn(tz, kMagic);
+    float far = fabsf(__fsub_rn(tz, __fsub_rn(yz, kMagic)));   // from an integer
+    int z = __float_as_int(yz) - __float_as_int(kMagic);
+    z = min(max(z, 0), (1 << BITS) - 1);
+    const int shift = z - __float_as_int(kMagic);
+    const Two up = twice(kMagic), down = twice(-kMagic), rr = twice(r), minus = twice(-1.f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        Two x;
+        x.f = make_float2(w[i], w[i + 1]);
+        const Two q = mul2(x, rr), y = add2(q, up);
+        const Two d = add2(mul2(add2(y, down), minus), q);    // exact
+        far = fmaxf(far, fmaxf(fabsf(d.f.x), fabsf(d.f.y)));
+        n[i] = y.i.x + shift, n[i + 1] = y.i.y + shift;
+    }
+    if (!(0.5f - far > tol)) {
+        z = min(max(rint_quotient(-lo, s), 0), (1 << BITS) - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = rint_quotient(w[i], s) + z;
+    }
+    *zero = z;
+}
+
+// Four codes clamped (by saturation) to bytes; eight to nibbles.
+__device__ __forceinline__ uint32_t to_bytes(int n0, int n1, int n2, int n3) {
+    uint32_t w;
+    asm("cvt.pack.sat.u8.s32.b32 %0, %1, %2, 0;" : "=r"(w) : "r"(n3), "r"(n2));
+    asm("cvt.pack.sat.u8.s32.b32 %0, %1, %2, %3;" : "=r"(w) : "r"(n1), "r"(n0), "r"(w));
+    return w;
+}
+__device__ __forceinline__ uint32_t to_nibbles(const int (&n)[8]) {
+    uint32_t w = 0u;
+#pragma unroll
+    for (int i = 6; i >= 0; i -= 2)
+        asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %3;"
+            : "=r"(w)
+            : "r"(n[i + 1]), "r"(n[i]), "r"(w));
+    return w;
+}
+
+// The float of byte i of w, less z = 2^23 + the zero point: exact.
+__device__ __forceinline__ float byte_less(uint32_t w, int i, float z) {
+    return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i)), z);
 }
 
 // The queries of a launch of append_kernel, turned as by w4_rope in blocks of
@@ -83,21 +151,25 @@ struct Queries {
     int heads;
     unsigned groups, units;    // see turn_unit
     unsigned all;              // tokens * groups * units
-    unsigned first_block;      // blocks from here on turn queries
-};
+    unsigned rows_blocks;      // blocks that take keys and values: every period-th,
+    unsigned period;           // from the first on, so that their arithmetic
+};                             // and the others' traffic overlap
 
-// Keys and values: D / 8 lanes take a row (a head of a token), 8 values a lane;
-// a warp takes the key and value of 128 / D tokens at a time.
+// Keys and values: D / 8 lanes take a row (a head of a token), 8 values a lane.
 template <int FMT, int D, int HEADS>
 __global__ void __launch_bounds__(kKvThreads)
-append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation rot, int tiles) {
+append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation rot, int tiles,
+              int split) {
     using L = KvLayout<FMT, D>;
-    constexpr int LANES = D / 8, TOKENS = 16 / LANES;
+    constexpr int LANES = D / 8, TOKENS = 32 / LANES;
     __shared__ Tile16 tile;
-    __shared__ __align__(16) unsigned char staged[L::kBytes];
+    __shared__ uint4 rows[kKvWarps][kRecTokens * LANES];
+    __shared__ __align__(16) unsigned char staged[kKvWarps][FMT == W4_KV_BF16 ? 16 : L::kPart];
     begin_after_previous();
-    if (blockIdx.x >= q.first_block) {
-        const unsigned e = (blockIdx.x - q.first_block) * kKvThreads + threadIdx.x;
+    const unsigned turn = blockIdx.x / q.period;
+    if (blockIdx.x != turn * q.period || turn >= q.rows_blocks) {
+        const unsigned e =
+            (blockIdx.x - min(turn + 1, q.rows_blocks)) * kKvThreads + threadIdx.x;
         if (e >= q.all) return;
         const unsigned tg = e / q.units, u = e - tg * q.units, t = tg / q.groups;
         TokenPlace at;
@@ -110,30 +182,50 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                                                   q.heads, rot, at.position, false);
         return;
     }
-    const int tile_no = blockIdx.x / pool.kv_heads, h = blockIdx.x - tile_no * pool.kv_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
+    const int parts = (2 * pool.kv_heads * split + kKvWarps - 1) / kKvWarps;    // blocks of a tile
+    const int tile_no = turn / parts;
+    int task = (turn - tile_no * parts) * kKvWarps + warp;
+    const int part = task % split;
+    task /= split;
     int first, count;
     bool whole;
-    const int i0 = load_tile(pool, list, tile_no, tiles, rot.table ? rot.rows : 0x7FFFFFFF, &tile, &first,
-                             &count, &whole);
-    if (count <= 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
-    for (int n0 = warp * TOKENS; n0 < count; n0 += kKvWarps * TOKENS) {
-        const int r = min(first + n0 + lane / (2 * LANES), kRecTokens - 1);
-        const bool valid = n0 + lane / (2 * LANES) < count && tile.valid[r];
-        const int t = i0 + r, pos = tile.position[r];
-        const bool is_v = lane / LANES & 1;
-        const Heads &src = is_v ? v : k;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (valid)
-            raw = *reinterpret_cast<const uint4 *>(
-                reinterpret_cast<const __nv_bfloat16 *>(src.data) + t * src.token_stride +
-                h * src.head_stride + 8 * c);
+    const int i0 = load_tile(pool, list, tile_no, tiles, rot.table ? rot.rows : 0x7FFFFFFF,
+                             L::kBytes, &tile, &first, &count, &whole);
+    if (count <= 0 || task >= 2 * pool.kv_heads) return;
+    whole = whole && split == 1;                              // staged by one warp
+    const bool is_v = task & 1;
+    const int h = task >> 1;
+    const long long head_bytes = (long long)h * pool.page_records * L::kBytes;
+    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>((is_v ? v : k).data) +
+                               h * (is_v ? v : k).head_stride + 8 * c;
+    const long long stride = (is_v ? v : k).token_stride;
+    // all rows are asked for at once, into shared memory: held in registers
+    // they would need an unrolled loop, which its instructions' fetching slows
+    for (int x = part; x * TOKENS < count; x += split) {
+        const int n = x * TOKENS + lane / LANES;
+        if (n < count && tile.record[first + n])
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             (uint32_t)__cvta_generic_to_shared(&rows[warp][32 * x + lane])),
+                         "l"(src + (i0 + first + n) * stride)
+                         : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll 1
+    for (int x0 = part; x0 * TOKENS < count; x0 += split) {
+        const int n = x0 * TOKENS + lane / LANES, r = min(first + n, kRecTokens - 1);
+        unsigned char *rec = n < count ? tile.record[r] : nullptr;
+        const bool valid = rec != nullptr;
+        rec += head_bytes;
+        const int pos = tile.position[r];
         float x[8];
-        const uint32_t *w = &raw.x;
+        const uint4 raw = valid ? rows[warp][32 * x0 + lane] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[2 * i] = bf16_low(w[i]), x[2 * i + 1] = bf16_high(w[i]);
-        if (rot.table) {
-            const bool turns = valid && !is_v && 8 * c < 2 * rot.pairs;
+        if (rot.table && !is_v) {
+            const bool turns = valid && 8 * c < 2 * rot.pairs;
             const float *row_of = rot.table + 2LL * (valid ? pos : 0) * rot.pairs;
             if (rot.layout == W4_ROPE_INTERLEAVED) {
                 if (turns) {
@@ -149,10 +241,12 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                     }
                 }
             } else {
-                // the partners are another lane's values
+                // the partners are another lane's values; a lane works out its
+                // own half of each pair: x c + p s, with -s in the lower half
                 const int half = rot.pairs / 8;
                 const bool upper = c >= half;
                 const int from = lane - c + (upper ? c - half : c + half);
+                const uint32_t flip = upper ? 0u : 0x80000000u;
                 uint32_t p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xFFFFFFFFu, w[i], from & 31);
@@ -162,30 +256,22 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 cs = tab[i];
-                        const float p0 = bf16_low(p[i]), p1 = bf16_high(p[i]);
-                        const float2 y0 = upper ? turn_pair(p0, x[2 * i], make_float2(cs.x, cs.y))
-                                                : turn_pair(x[2 * i], p0, make_float2(cs.x, cs.y));
-                        const float2 y1 =
-                            upper ? turn_pair(p1, x[2 * i + 1], make_float2(cs.z, cs.w))
-                                  : turn_pair(x[2 * i + 1], p1, make_float2(cs.z, cs.w));
-                        x[2 * i] = upper ? y0.y : y0.x;
-                        x[2 * i + 1] = upper ? y1.y : y1.x;
+                        const float s0 = __uint_as_float(__float_as_uint(cs.y) ^ flip);
+                        const float s1 = __uint_as_float(__float_as_uint(cs.w) ^ flip);
+                        x[2 * i] = __fadd_rn(__fmul_rn(x[2 * i], cs.x),
+                                             __fmul_rn(bf16_low(p[i]), s0));
+                        x[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], cs.z),
+                                                 __fmul_rn(bf16_high(p[i]), s1));
                     }
                 }
             }
         }
-        const uint4 packed = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
-                                        bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
-        const int in = tile.in_page[r], rr = in % kRecTokens;
-        unsigned char *rec =
-            whole ? staged
-                  : reinterpret_cast<unsigned char *>(pool.records) +
-                        (tile.page_record[r] + (long long)h * pool.page_records +
-                         in / kRecTokens) * L::kBytes;
+        const int rr = tile.in_record[r];
         if constexpr (FMT == W4_KV_BF16) {
             if (valid)
                 *reinterpret_cast<uint4 *>(rec + (is_v ? L::value(rr, 8 * c) : L::key(rr, 8 * c))) =
-                    packed;
+                    make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]),
+                               bf16_pair(x[6], x[7]));
         } else {
             float lo = 0.f, hi = 0.f;
 #pragma unroll
@@ -199,46 +285,40 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
             const __half sh =
                 __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), top), 65504.f));
             const float s = __half2float(sh);
-            const float z = s == 0.f ? 0.f : clampf(rintf(__fdiv_rn(-lo, s)), 0.f, top);
-            const float rcp = s == 0.f ? 0.f : __frcp_rn(s);
-            const float tol = __fmul_rn(__fmul_rn(fmaxf(-lo, hi), rcp), 0x1p-21f);
-            uint32_t code[2] = {0u, 0u};                      // 8 codes, a byte each
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f =
-                    s == 0.f ? 0.f : clampf(rint_quotient(x[i], s, rcp, tol) + z, 0.f, top);
-                code[i / 4] |= (uint32_t)f << (8 * (i % 4));
-            }
+            int z = 0, n8[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (s > 0.f) codes_of<L::kBits>(x, lo, hi, s, &z, n8);
+            // values: the bytes of a whole record go to shared memory first
+            unsigned char *to = whole ? staged[warp] - L::kPart : rec;
             if constexpr (FMT == W4_KV_INT8) {
+                const uint32_t b0 = to_bytes(n8[0], n8[1], n8[2], n8[3]);
+                const uint32_t b1 = to_bytes(n8[4], n8[5], n8[6], n8[7]);
                 if (valid && !is_v)
-                    *reinterpret_cast<uint2 *>(rec + L::key(rr, 8 * c)) =
-                        make_uint2(code[0], code[1]);
+                    *reinterpret_cast<uint2 *>(rec + L::key(rr, 8 * c)) = make_uint2(b0, b1);
                 if (valid && is_v) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        rec[L::value(rr, 8 * c + i)] = (unsigned char)(code[i / 4] >> 8 * (i % 4));
+                        to[L::value(rr, 8 * c + i)] = (unsigned char)((i < 4 ? b0 : b1) >> 8 * (i & 3));
                 }
+            } else if (!is_v) {
+                if (valid) *reinterpret_cast<uint32_t *>(rec + L::key(rr, 8 * c)) = to_nibbles(n8);
             } else {
-                // the other nibble of a value's byte is 8 values on: the next
-                // lane's (each of the two writes half of the bytes)
-                const uint32_t other0 = __shfl_xor_sync(0xFFFFFFFFu, code[0], 1);
-                const uint32_t other1 = __shfl_xor_sync(0xFFFFFFFFu, code[1], 1);
-                if (valid && !is_v) {
-                    uint32_t bytes = 0u;
+                // the high nibble of a value's byte is 8 values on, in the next
+                // lane: the even lane writes the first four bytes of the two,
+                // the odd one the others (15 is the largest code: the bytes
+                // are saturated at 4 bits first)
+                uint32_t b[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t two = code[i / 2] >> (16 * (i % 2));
-                        bytes |= ((two & 15u) | (two >> 4 & 0xF0u)) << (8 * i);
-                    }
-                    *reinterpret_cast<uint32_t *>(rec + L::key(rr, 8 * c)) = bytes;
-                }
-                if (valid && is_v) {
-                    const bool odd = c & 1;
-                    const uint32_t both = odd ? other1 | code[1] << 4 : code[0] | other0 << 4;
+                for (int i = 0; i < 2; ++i)
+                    b[i] = to_bytes(min(n8[4 * i], 15), min(n8[4 * i + 1], 15),
+                                    min(n8[4 * i + 2], 15), min(n8[4 * i + 3], 15));
+                const bool odd = c & 1;
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? b[0] : b[1], 1);
+                const uint32_t bytes = odd ? got | b[1] << 4 : b[0] | got << 4;
+                if (valid) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        rec[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i)] =
-                            (unsigned char)(both >> 8 * i);
+                        to[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i)] =
+                            (unsigned char)(bytes >> 8 * i);
                 }
             }
             if (valid && c == 0)
@@ -246,52 +326,55 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                     (uint32_t)__half_as_ushort(sh) | (uint32_t)z << 16;
         }
     }
-    if (!whole) return;
-    __syncthreads();
+    if (FMT == W4_KV_BF16 || !whole || !is_v) return;
+    __syncwarp();
     uint4 *out = reinterpret_cast<uint4 *>(
-        pool.records + (tile.page_record[0] + (long long)h * pool.page_records +
-                        tile.in_page[0] / kRecTokens) * L::kBytes);
-    for (int i = threadIdx.x; i < L::kBytes / 16; i += kKvThreads)
-        out[i] = reinterpret_cast<const uint4 *>(staged)[i];
+        tile.record[0] + head_bytes + L::kPart);
+#pragma unroll
+    for (int i = 0; i < L::kPart / 512; ++i)
+        out[32 * i + lane] = reinterpret_cast<const uint4 *>(staged[warp])[32 * i + lane];
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvThreads)
-read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles) {
+read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split) {
     using L = KvLayout<FMT, D>;
-    constexpr int LANES = D / 8, TOKENS = 16 / LANES;         // tokens a warp takes at a time
+    constexpr int LANES = D / 8, TOKENS = 32 / LANES, STEPS = kRecTokens / TOKENS;
     __shared__ Tile16 tile;
-    __shared__ __align__(16) unsigned char staged[L::kBytes];
+    __shared__ __align__(16) unsigned char staged[kKvWarps][FMT == W4_KV_BF16 ? 16 : L::kPart];
     begin_after_previous();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
+    const int parts = (2 * pool.kv_heads * split + kKvWarps - 1) / kKvWarps;    // of a tile
+    const int tile_no = blockIdx.x / parts;
+    int task = (blockIdx.x - tile_no * parts) * kKvWarps + warp;
+    const int part = task % split;
+    task /= split;
     int first, count;
     bool whole;
-    const int i0 = load_tile(pool, list, blockIdx.x, tiles, 0x7FFFFFFF, &tile, &first, &count, &whole);
-    if (count <= 0) return;
-    const int h = blockIdx.y;
-    if (whole) {
+    const int i0 = load_tile(pool, list, tile_no, tiles, 0x7FFFFFFF, L::kBytes, &tile, &first, &count,
+                             &whole);
+    const bool is_v = task & 1;
+    const int h = task >> 1;
+    const long long head_bytes = (long long)h * pool.page_records * L::kBytes;
+    if (count <= 0 || task >= 2 * pool.kv_heads || !(is_v ? v : k).data) return;
+    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>((is_v ? v : k).data) +
+                         h * (is_v ? v : k).head_stride + 8 * c;
+    const long long stride = (is_v ? v : k).token_stride;
+    const bool apart = FMT != W4_KV_BF16 && whole && is_v && split == 1;
+    if (apart) {
         const uint4 *in = reinterpret_cast<const uint4 *>(
-            pool.records + (tile.page_record[0] + (long long)h * pool.page_records +
-                            tile.in_page[0] / kRecTokens) * L::kBytes);
+            tile.record[0] + head_bytes + L::kPart);
 #pragma unroll
-        for (int i = 0; i < (L::kBytes / 16 + kKvThreads - 1) / kKvThreads; ++i) {
-            const int at = i * kKvThreads + threadIdx.x;
-            if (at < L::kBytes / 16) reinterpret_cast<uint4 *>(staged)[at] = in[at];
-        }
-        __syncthreads();
+        for (int i = 0; i < L::kPart / 512; ++i)
+            reinterpret_cast<uint4 *>(staged[warp])[32 * i + lane] = in[32 * i + lane];
+        __syncwarp();
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
-    // 2 LANES lanes take a token: its key, then its value
-    for (int n = warp * TOKENS + lane / (2 * LANES); n < count; n += kKvWarps * TOKENS) {
-        const int r = first + n;
-        const bool is_v = lane / LANES & 1;
-        const Heads &dst = is_v ? v : k;
-        if (!tile.valid[r] || !dst.data) continue;
-        const int in = tile.in_page[r], rr = in % kRecTokens;
-        const unsigned char *rec =
-            whole ? staged
-                  : reinterpret_cast<const unsigned char *>(pool.records) +
-                        (tile.page_record[r] + (long long)h * pool.page_records +
-                         in / kRecTokens) * L::kBytes;
+#pragma unroll 2
+    for (int x0 = part; x0 < STEPS; x0 += split) {
+        const int n = x0 * TOKENS + lane / LANES, r = min(first + n, kRecTokens - 1);
+        if (n >= count || !tile.record[r]) continue;
+        const int rr = tile.in_record[r];
+        const unsigned char *rec = tile.record[r] + head_bytes;
         uint4 packed;
         if constexpr (FMT == W4_KV_BF16) {
             packed = *reinterpret_cast<const uint4 *>(
@@ -300,66 +383,78 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles) {
             const uint32_t m = *reinterpret_cast<const uint32_t *>(
                 rec + (is_v ? L::kMetaV : L::kMeta) + 4 * rr);
             const float s = __half2float(__ushort_as_half((unsigned short)(m & 0xFFFFu)));
-            const int z = (int)(m >> 16);
+            const float z = (float)(8388608 + (m >> 16));
             uint32_t code[2] = {0u, 0u};
-            if constexpr (FMT == W4_KV_INT8) {
-                if (!is_v) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(rec + L::key(rr, 8 * c));
-                    code[0] = w.x, code[1] = w.y;
-                } else {
+            if (is_v) {
+                const unsigned char *from = apart ? staged[warp] - L::kPart : rec;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        code[i / 4] |= (uint32_t)rec[L::value(rr, 8 * c + i)] << (8 * (i % 4));
+                for (int i = 0; i < 8; ++i)
+                    code[i / 4] |= (uint32_t)from[L::value(rr, 8 * c + i)] << (8 * (i % 4));
+                if (FMT == W4_KV_INT4) {
+                    code[0] = code[0] >> (4 * (c & 1)) & 0x0F0F0F0Fu;
+                    code[1] = code[1] >> (4 * (c & 1)) & 0x0F0F0F0Fu;
                 }
-            } else if (!is_v) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + L::key(rr, 8 * c));
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    code[i / 4] |= (w >> (4 * i) & 15u) << (8 * (i % 4));
+            } else if constexpr (FMT == W4_KV_INT8) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(rec + L::key(rr, 8 * c));
+                code[0] = w.x, code[1] = w.y;
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    code[i / 4] |= ((uint32_t)rec[L::value(rr, 8 * c + i)] >> (4 * (c & 1)) & 15u)
-                                   << (8 * (i % 4));
+                // nibbles 0, 2, 4, 6 and 1, 3, 5, 7 to bytes, then in order
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + L::key(rr, 8 * c));
+                const uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
+                code[0] = __byte_perm(lo, hi, 0x5140);
+                code[1] = __byte_perm(lo, hi, 0x7362);
             }
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = __fmul_rn((float)((int)(code[i / 4] >> (8 * (i % 4)) & 255u) - z), s);
+            for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(byte_less(code[i / 4], i % 4, z), s);
             packed = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
                                 bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
         }
-        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(dst.data) +
-                                   (i0 + r) * dst.token_stride + h * dst.head_stride + 8 * c) =
-            packed;
+        *reinterpret_cast<uint4 *>(dst + (i0 + r) * stride) = packed;
     }
 }
 
 // Tiles that a run of `run` tokens can touch, wherever in a record it starts.
 int tiles_of(int run) { return (run + 2 * (kRecTokens - 1)) / kRecTokens; }
 
+// Warps that share a tile's keys (values) of a head: one where the blocks fill
+// the GPU (then it can put a whole record together), four where the time is
+// that of one block, and always in bf16, which has nothing to put together.
+int split_of(const KvPool &pool, int format, int head_dim, const TokenList &list, int tiles,
+             int num_sms) {
+    if (list.run <= 256 / head_dim) return 1;
+    const long long warps = (long long)(list.tokens / list.run) * tiles * 2 * pool.kv_heads;
+    return format == W4_KV_BF16 || warps < 32LL * num_sms ? 4 : 1;
+}
+unsigned blocks_of(const KvPool &pool, const TokenList &list, int tiles, int split) {
+    return (unsigned)(list.tokens / list.run * tiles) *
+           ((2 * (unsigned)pool.kv_heads * split + kKvWarps - 1) / kKvWarps);
+}
+
 template <int D, int HEADS>
 cudaError_t append_dim(const KvPool &pool, int format, const Heads &k, const Heads &v, Queries q,
-                       const TokenList &list, const Rotation &rot, cudaStream_t stream) {
-    const int tiles = tiles_of(list.run);
-    q.first_block = (unsigned)(list.tokens / list.run * tiles) * pool.kv_heads;
-    const dim3 grid(q.first_block + (q.all + kKvThreads - 1) / kKvThreads);
+                       const TokenList &list, const Rotation &rot, int num_sms,
+                       cudaStream_t stream) {
+    const int tiles = tiles_of(list.run), split = split_of(pool, format, D, list, tiles, num_sms);
+    q.rows_blocks = blocks_of(pool, list, tiles, split);
+    const dim3 grid(q.rows_blocks + (q.all + kKvThreads - 1) / kKvThreads);
+    q.period = grid.x / q.rows_blocks;
     const auto kernel = format == W4_KV_BF16   ? append_kernel<W4_KV_BF16, D, HEADS>
                         : format == W4_KV_INT8 ? append_kernel<W4_KV_INT8, D, HEADS>
                                                : append_kernel<W4_KV_INT4, D, HEADS>;
     return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, q, list, rot,
-                             tiles);
+                             tiles, split);
 }
 
 template <int D>
 cudaError_t read_dim(const KvPool &pool, int format, const Heads &k, const Heads &v,
-                     const TokenList &list, cudaStream_t stream) {
-    const int tiles = tiles_of(list.run);
-    const dim3 grid((unsigned)(list.tokens / list.run * tiles), (unsigned)pool.kv_heads);
+                     const TokenList &list, int num_sms, cudaStream_t stream) {
+    const int tiles = tiles_of(list.run), split = split_of(pool, format, D, list, tiles, num_sms);
     const auto kernel = format == W4_KV_BF16   ? read_kernel<W4_KV_BF16, D>
                         : format == W4_KV_INT8 ? read_kernel<W4_KV_INT8, D>
                                                : read_kernel<W4_KV_INT4, D>;
-    return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, list, tiles);
+    return launch_overlapped(kernel, dim3(blocks_of(pool, list, tiles, split)), dim3(kKvThreads),
+                             0, stream, pool, k, v, list, tiles, split);
 }
 
 }  // namespace
@@ -368,7 +463,7 @@ cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const
                              const Heads &v, const Heads &q, const Heads &q_out, int q_heads,
                              const TokenList &list, const Rotation &rot, int num_sms,
                              cudaStream_t stream) {
-    Queries qs = {q, q_out, q_heads, 1, 1, 0, 0};
+    Queries qs = {q, q_out, q_heads, 1, 1, 0, 0, 1};
     bool four = false;
     if (q_heads > 0) {
         // four heads a thread once that still gives every SM two blocks
@@ -379,16 +474,17 @@ cudaError_t launch_kv_append(const KvPool &pool, int format, int head_dim, const
         qs.all = (unsigned)((long long)list.tokens * qs.groups * qs.units);
     }
     if (head_dim == 64)
-        return four ? append_dim<64, 4>(pool, format, k, v, qs, list, rot, stream)
-                    : append_dim<64, 1>(pool, format, k, v, qs, list, rot, stream);
-    return four ? append_dim<128, 4>(pool, format, k, v, qs, list, rot, stream)
-                : append_dim<128, 1>(pool, format, k, v, qs, list, rot, stream);
+        return four ? append_dim<64, 4>(pool, format, k, v, qs, list, rot, num_sms, stream)
+                    : append_dim<64, 1>(pool, format, k, v, qs, list, rot, num_sms, stream);
+    return four ? append_dim<128, 4>(pool, format, k, v, qs, list, rot, num_sms, stream)
+                : append_dim<128, 1>(pool, format, k, v, qs, list, rot, num_sms, stream);
 }
 
 cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const Heads &k,
-                           const Heads &v, const TokenList &list, cudaStream_t stream) {
-    return head_dim == 64 ? read_dim<64>(pool, format, k, v, list, stream)
-                          : read_dim<128>(pool, format, k, v, list, stream);
+                           const Heads &v, const TokenList &list, int num_sms,
+                           cudaStream_t stream) {
+    return head_dim == 64 ? read_dim<64>(pool, format, k, v, list, num_sms, stream)
+                          : read_dim<128>(pool, format, k, v, list, num_sms, stream);
 }
 
 }  // namespace w4
