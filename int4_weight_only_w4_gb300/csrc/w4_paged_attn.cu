@@ -28,11 +28,12 @@
 // evenly among themselves, from the lengths on the device: block c takes the
 // records from cut c to cut c + 1.  A cut that would leave only a few records
 // of a head on one side moves to the head's border, so short heads stay whole.
-// The pieces of a cut head are joined by the block that finishes it last, in
-// block order.  In a block, one warp issues the copies, a record a bulk copy,
-// running ahead over the block's whole stretch; the others form KG groups of
-// QG: a group takes every KG-th record through its own ring, and its QG warps
-// hold 8 NT rows each.
+// The pieces of cut heads are joined by a second kernel that is already
+// resident when the first one ends, a few rows a block: left to the block that
+// finished a head last, the joining of 5 pieces of 56 rows took 7 us.  In a
+// block, two warps issue the copies, a record a bulk copy, running ahead over
+// the block's whole stretch; the others form KG groups of QG: a group takes
+// every KG-th record through its own ring, and its QG warps hold 8 NT rows each.
 #include <atomic>
 
 #include "w4_device.cuh"
@@ -537,24 +538,28 @@ struct Tile {
     }
 };
 
-// The workspace: a counter per block, then the pieces that are joined, two a
-// block: float [64][D], then m [64], l [64].
-constexpr int kCounterBytes = 4 * kMaxGrid;
+// The workspace: of every block, the head that it starts and others go on with
+// (pieces = 0: none), then two pieces of rows: float [64][D], m [64], l [64].
+struct CutHead {
+    int b, h, tile0, pieces;
+};
+constexpr int kHeadBytes = kMaxGrid * sizeof(CutHead);
+__device__ __forceinline__ CutHead *cut_head(const AttnArgs &a, int block) {
+    return static_cast<CutHead *>(a.workspace) + block;
+}
 template <int D>
 __device__ __forceinline__ float *slot_of(const AttnArgs &a, int block, bool starts) {
-    return reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes) +
+    return reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kHeadBytes) +
            (size_t)(2 * block + (starts ? 1 : 0)) * kRowsMax * (D + 2);
 }
 
-// Four values of a row, l and m its sum and reference.  dry: nothing is stored.
+// Four values of a row, l and m its sum and reference.
 __device__ __forceinline__ void store_row(const AttnArgs &a, int b, int h, int row, int d,
-                                          float4 o, float m, float l, bool dry) {
+                                          float4 o, float m, float l) {
     const int i = row / a.group, hq = h * a.group + row - i * a.group;
     const long long t = (long long)b * a.tokens + i;
     const float f = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;    // NaN stays NaN
     const long long at = t * a.out.token_stride + (long long)hq * a.out.head_stride + d;
-    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    if (dry) return;
     if (a.f32_out) {
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out.data) + at) =
             make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
@@ -563,7 +568,7 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, int b, int h, int r
             make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
     }
     if (a.lse && d == 0)
-        a.lse[t * a.q_heads + hq] = lse;
+        a.lse[t * a.q_heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) {
@@ -661,66 +666,51 @@ __device__ __forceinline__ void warps_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
-// A running join: o, l relative to m take in 8 values of another piece.
-struct Joined {
-    float4 o0, o1;
-    float m, l;
-
-    __device__ __forceinline__ void take(const float4 &v0, const float4 &v1, float vm, float vl) {
-        const float now = fmaxf(m, vm), f = exp2_fast(m - now), g = exp2_fast(vm - now);
-        o0 = make_float4(o0.x * f, o0.y * f, o0.z * f, o0.w * f);
-        o1 = make_float4(o1.x * f, o1.y * f, o1.z * f, o1.w * f);
-        add_scaled(o0, g, v0);
-        add_scaled(o1, g, v1);
-        l = fmaf(l, f, vl * g);
-        m = now;
-    }
-};
-
-// The block that finished a head last joins its n pieces, those of blocks c0 ..
-// c0 + n - 1, in an order that depends on their number only.  One pass: a
-// piece's values, reference and sum are asked for together, because a trip to
-// L2 costs more than the arithmetic.
-template <int D, int WARPS>
-__device__ __forceinline__ void join_pieces(const AttnArgs &a, int c0, int n, int b, int h,
-                                            int tile0, int there, float *buf, bool dry) {
-    constexpr int THREADS = 32 * WARPS, UNITS = D / 8;        // 8 values a thread
-    const int tid = dry ? threadIdx.x & 31 : threadIdx.x;
-    const int values = there * UNITS, sides = max(1, THREADS / values);
-    float4 *part = reinterpret_cast<float4 *>(buf);
-    // `sides` threads per 8 values take every sides-th piece each
-    for (int e0 = 0; e0 < values; e0 += dry ? 1 << 20 : THREADS) {
-        const int side = sides > 1 ? tid / values : 0, e = e0 + tid - side * values;
-        const int r = e / UNITS, d = e % UNITS * 8;
-        const bool has = side < sides && e < values;
-        Joined j = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f), kNone, 0.f};
-        if (has) {
-#pragma unroll 7
-            for (int c = side; c < n; c += sides) {
-                const float *s = slot_of<D>(a, c0 + c, c == 0);
-                const float4 *v = reinterpret_cast<const float4 *>(s + r * D + d);
-                j.take(__ldcg(v), __ldcg(v + 1), __ldcg(s + kRowsMax * D + r),
-                       __ldcg(s + kRowsMax * D + kRowsMax + r));
-            }
-        }
-        if (sides > 1) {
-            if (has && side > 0 && !dry) {
-                part[3 * tid] = j.o0, part[3 * tid + 1] = j.o1;
-                part[3 * tid + 2] = make_float4(j.m, j.l, 0.f, 0.f);
-            }
-            if (!dry) warps_sync<WARPS>();
-#pragma unroll 1
-            for (int x = 1; x < sides && side == 0; ++x) {
-                const float4 *v = part + 3 * (tid + x * values);
-                j.take(v[0], v[1], v[2].x, v[2].y);
-            }
-        }
-        if (has && side == 0) {
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x)
-                store_row(a, b, h, tile0 + r, d + 4 * x, x ? j.o1 : j.o0, j.m, j.l, dry);
+// Joins the pieces of the heads that blocks start and others go on with: block
+// (c, y) rows ROWS y .. of block c's head, in the pieces' order.  256 / ROWS
+// threads a row: groups of D / 4 take every other (or fourth) piece of it.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int block_rows) {
+    constexpr int UNITS = D / 4, GROUPS = 256 / ROWS / UNITS;
+    __shared__ float4 part[256];
+    __shared__ float2 part_ml[256];
+    begin_after_previous();
+    const int4 head = __ldcg(reinterpret_cast<const int4 *>(cut_head(a, blockIdx.x)));
+    const int tid = threadIdx.x, row = ROWS * blockIdx.y + tid / (GROUPS * UNITS);
+    const int group = tid / UNITS % GROUPS, d = tid % UNITS * 4;
+    if (head.w == 0) return;
+    const bool there = row < min(block_rows, a.tokens * a.group - head.z);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = kNone, l = 0.f;
+    if (there) {
+#pragma unroll 10
+        for (int c = group; c < head.w; c += GROUPS) {
+            const float *s = slot_of<D>(a, blockIdx.x + c, c == 0);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + row * D + d));
+            const float vm = __ldcg(s + kRowsMax * D + row);
+            const float vl = __ldcg(s + kRowsMax * D + kRowsMax + row);
+            const float now = fmaxf(m, vm), f = exp2_fast(m - now), g = exp2_fast(vm - now);
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            add_scaled(o, g, v);
+            l = fmaf(l, f, vl * g);
+            m = now;
         }
     }
+    if (GROUPS > 1) {
+        part[tid] = o, part_ml[tid] = make_float2(m, l);
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int x = 1; x < GROUPS; ++x) {
+            const float2 ml = part_ml[tid + x * UNITS];
+            const float now = fmaxf(m, ml.x), f = exp2_fast(m - now), g = exp2_fast(ml.x - now);
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            add_scaled(o, g, part[tid + x * UNITS]);
+            l = fmaf(l, f, ml.y * g);
+            m = now;
+        }
+    }
+    if (there) store_row(a, head.x, head.y, head.z + row, d, o, m, l);
 }
 
 // Warps that compute: with the two that copy 16 of 128 registers, or 12 of 168.
@@ -746,7 +736,7 @@ struct Piece {
     int len;
     int whole;         // the head is not cut
     int starts;        // the piece starts the head
-    int c0, pieces;    // cut: the head's first block, and how many pieces it has
+    int pieces;        // of a head that starts here and is cut
 };
 
 // The copying warps: lane i of warp w fills the ring of group 2 i + w.  Two of
@@ -802,7 +792,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
             p.u0 = c.u, p.stop = stop, p.len = seq.len;
             p.whole = c.u == 0 && u1 == n_seq, p.starts = c.u == 0;
         }
-        if (copier == 0 && more && !(c.u == 0 && u1 == n_seq)) {
+        if (copier == 0 && more && c.u == 0 && u1 != n_seq) {
             // the cuts inside this head, at least `least` records from its borders
             const bool mine = c.b >= list.b0 && c.b < list.b1;
             int head = list.before * per_seq + c.item * n_seq;
@@ -812,7 +802,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
             head = __shfl_sync(0xFFFFFFFFu, head, __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1);
             const int c_lo = list.block_from(head + list.least);
             const int c_hi = list.block_from(head + n_seq - list.least + 1) - 1;
-            if (tells) p.c0 = c_lo - 1, p.pieces = c_hi - c_lo + 2;
+            if (tells) p.pieces = c_hi - c_lo + 2;
         }
         if (tells) mbar_arrive(&piece_full[slot]);
         ++told;
@@ -878,7 +868,6 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     __shared__ int first_key[kMaxWarps * kMaxStages];         // of a stage's record, or kAbsent
     __shared__ float join_m[kMaxWarps * 8 * NT], join_l[kMaxWarps * 8 * NT];
     __shared__ Piece piece[2];
-    __shared__ int is_last;
     const int block_rows = 8 * NT * plan.QG;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -893,31 +882,32 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     begin_after_previous();
-    // A copying warp that is done goes once through the joins, without barriers
-    // and without storing anything: they are run by few blocks and late, so
-    // their instructions would come from DRAM, line after line (5 us of 34 for
-    // one sequence of 64 k tokens).
-    const bool dry = warp >= WARPS;
-    if (dry)
+    if (warp >= WARPS) {
         copy_records<FMT, D, WARPS>(a, plan, block_rows, smem, full, empty, first_key, piece,
                                     piece_full, piece_empty);
+        return;
+    }
 
     const int kg = warp / plan.QG, qg = warp - kg * plan.QG;
-    const bool works = kg < plan.KG && !dry;                  // QG may not divide WARPS
+    const bool works = kg < plan.KG;                          // QG may not divide WARPS
     const uint32_t ring = smem_addr(smem) + kg * plan.stages * L::kBytes;
     int get = 0;
     uint32_t phase = 0;
     bool failed = false;
+    CutHead started = {0, 0, 0, 0};
     Tile<FMT, D, NT> w;
     for (int told = 0;; ++told) {
         const Piece &p = piece[told & 1];
-        if (!dry) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&piece_full[told & 1], (told >> 1) & 1))) {
-                if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
-                return;                                       // every warp does
-            }
-            if (p.b < 0) return;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&piece_full[told & 1], (told >> 1) & 1))) {
+            if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);
+            if (tid == 0) *cut_head(a, blockIdx.x) = {0, 0, 0, 0};
+            return;                                           // every warp does
         }
+        if (p.b < 0) {
+            if (tid == 0) *cut_head(a, blockIdx.x) = started;
+            return;
+        }
+        if (p.starts && !p.whole) started = {p.b, p.h, p.tile0, p.pieces};
         if (works && !failed) {
             const int rows = a.tokens * a.group, row0 = p.tile0 + qg * 8 * NT;
             w.load_q(a, p.b, p.h, row0, rows);
@@ -963,11 +953,10 @@ attn_kernel(const AttnArgs a, const Plan plan) {
                         join_o[(r + (x & 1)) * OROW + 16 * k + g + (x & 2) * 4] = w.o[n][k][x];
             }
         }
-        if (!dry) warps_sync<WARPS>();
-        const bool whole = !dry && p.whole;
-        const int there = dry ? block_rows : min(block_rows, a.tokens * a.group - p.tile0);
+        warps_sync<WARPS>();
+        const int there = min(block_rows, a.tokens * a.group - p.tile0);
         float *slot = slot_of<D>(a, blockIdx.x, p.starts);
-        for (int e = dry ? lane : tid; e < there * (D / 4); e += dry ? 1 << 20 : 32 * WARPS) {
+        for (int e = tid; e < there * (D / 4); e += 32 * WARPS) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = kNone, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -980,31 +969,13 @@ attn_kernel(const AttnArgs a, const Plan plan) {
                 l = fmaf(f, join_l[at], l);
                 add_scaled(o, f, *reinterpret_cast<const float4 *>(&join_o[at * OROW + d]));
             }
-            if (whole) {
-                store_row(a, p.b, p.h, p.tile0 + r, d, o, m, l, false);
-            } else if (!dry) {
+            if (p.whole) {
+                store_row(a, p.b, p.h, p.tile0 + r, d, o, m, l);
+            } else {
                 *reinterpret_cast<float4 *>(&slot[r * D + d]) = o;
                 if (d == 0) slot[kRowsMax * D + r] = m, slot[kRowsMax * D + kRowsMax + r] = l;
             }
         }
-        if (!whole) {
-            if (!dry) {
-                uint32_t *counter = static_cast<uint32_t *>(a.workspace) + p.c0;
-                __threadfence();
-                warps_sync<WARPS>();
-                if (tid == 0) {
-                    is_last = atomicAdd(counter, 1u) == (uint32_t)(p.pieces - 1);
-                    if (is_last) *counter = 0u;
-                }
-                warps_sync<WARPS>();
-            }
-            if (dry || is_last) {
-                if (!dry) __threadfence();
-                join_pieces<D, WARPS>(a, dry ? blockIdx.x : p.c0, dry ? 1 : p.pieces, p.b, p.h,
-                                      p.tile0, there, join_o, dry);
-            }
-        }
-        if (dry) return;
         warps_sync<WARPS>();                                  // the join's memory is free again
         if (lane == 0) mbar_arrive(&piece_empty[told & 1]);
     }
@@ -1035,8 +1006,21 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.ring_bytes = p.KG * p.stages * bytes;
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    return launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
-                             kSharedBytes, stream, a, p);
+    e = launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
+                          kSharedBytes, stream, a, p);
+    if (e != cudaSuccess) return e;
+    // one sequence that is too short for a second part of a head: nothing to join
+    const long long longest = (long long)a.pool.width * a.pool.page_records;
+    if (a.pool.seqs == 1 && longest < 8 * p.KG && a.pool.kv_heads * p.row_tiles <= grid)
+        return cudaSuccess;
+    const int block_rows = 8 * NT * p.QG, rows = a.tokens * a.group;
+    constexpr int FEW = 2, MANY = 1024 / D;                   // rows of a joining block
+    if (rows <= 8)
+        return launch_overlapped(join_kernel<D, FEW>, dim3(grid, (rows + FEW - 1) / FEW), dim3(256),
+                                 0, stream, a, block_rows);
+    return launch_overlapped(join_kernel<D, MANY>,
+                             dim3(grid, ((rows < block_rows ? rows : block_rows) + MANY - 1) / MANY),
+                             dim3(256), 0, stream, a, block_rows);
 }
 
 // Two tiles a warp from 9 rows on: the operands of a record serve both.
@@ -1050,7 +1034,7 @@ cudaError_t launch_rows(const AttnArgs &a, int num_sms, cudaStream_t stream) {
 
 size_t attn_workspace_bytes(int head_dim, int num_sms) {
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    return kCounterBytes + (size_t)grid * 2 * kRowsMax * (head_dim + 2) * 4;
+    return kHeadBytes + (size_t)grid * 2 * kRowsMax * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, int num_sms,
