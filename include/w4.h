@@ -634,12 +634,12 @@ w4_status w4_paged_attn_workspace_bytes(const w4_kv_cache *cache, size_t *bytes)
  *   out    : device [seqs * tokens][q_heads][head_dim] bf16, rows 16-byte aligned
  *            (w4_paged_attn_f32: float, rows 16-byte aligned)
  *   lse    : device float [seqs * tokens][q_heads], or NULL
- *   tokens : 1..8;  q_heads : a multiple of kv_heads
+ *   tokens : 1..8;  q_heads : a multiple of kv_heads, at most 4096 times it
  *   lens   : device int32 [table->seqs]; negative counts as 0
  *   scale  : finite; usually head_dim^-0.5
  *   window : 0 for none
- *   workspace : device, 256-byte aligned, zero before its first use; calls that
- *            overlap on the device must not share one (as for w4_gemv_ws)
+ *   workspace : device, 256-byte aligned; calls that overlap on the device must
+ *            not share one; what it holds between calls does not matter
  * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, or a table
  * and heads that allow 2^31 or more visits of records), W4_ERR_CUDA.
  */

@@ -104,6 +104,7 @@ struct AttnArgs {
     const int32_t *lens;
     int q_heads;
     int group;       // query heads per key/value head
+    unsigned group_magic;    // 2^32 / group, rounded up: rows below 2^16 divide by it
     int tokens;      // new tokens per sequence
     float scale;
     int window;      // 0: none

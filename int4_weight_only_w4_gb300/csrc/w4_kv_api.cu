@@ -108,6 +108,7 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     if (tokens < 1 || tokens > W4_MAX_TOKENS) return W4_ERR_UNSUPPORTED;
     if (q_heads < 1 || q_heads % cache->kv_heads || window < 0 || !isfinite(scale))
         return W4_ERR_INVALID_ARG;
+    if (q_heads / cache->kv_heads > 4096) return W4_ERR_UNSUPPORTED;
     if (!rows_aligned(q, 2) || !rows_aligned(out, f32_out ? 4 : 2) || !aligned(lens, 4) ||
         !aligned(lse, 4) || !aligned(workspace, 256))
         return W4_ERR_INVALID_ARG;
@@ -135,6 +136,7 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     a.lens = lens;
     a.q_heads = q_heads;
     a.group = q_heads / cache->kv_heads;
+    a.group_magic = a.group > 1 ? 0xFFFFFFFFu / (unsigned)a.group + 1 : 0;
     a.tokens = tokens;
     a.scale = scale;
     a.window = window;

@@ -103,6 +103,11 @@ __device__ __forceinline__ int page_slot(const KvPool &pool, int r) {
     return pool.page_shift >= 0 ? r >> pool.page_shift : r / pool.page_records;
 }
 
+// New token of a row.
+__device__ __forceinline__ int token_of_row(const AttnArgs &a, int row) {
+    return a.group == 1 ? row : (int)__umulhi((unsigned)row, a.group_magic);
+}
+
 struct Seq {
     int len;           // visible tokens
     int first;         // first record with a visible key
@@ -150,7 +155,7 @@ struct Tile {
         for (int n = 0; n < NT; ++n) {
             const int r = row0 + 8 * n + g;
             const bool there = r < rows;
-            const int i = there ? r / a.group : 0, hq = there ? r - i * a.group : 0;
+            const int i = there ? token_of_row(a, r) : 0, hq = there ? r - i * a.group : 0;
             const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.q.data) +
                                      (long long)(b * a.tokens + i) * a.q.token_stride +
                                      (long long)(h * a.group + hq) * a.q.head_stride;
@@ -476,7 +481,7 @@ struct Tile {
 
     // New token of column 2t + c of tile n.
     __device__ static int token_of(const AttnArgs &a, int n, int c, int row0, int rows) {
-        return min(row0 + 8 * n + 2 * ((int)threadIdx.x & 3) + c, rows - 1) / a.group;
+        return token_of_row(a, min(row0 + 8 * n + 2 * ((int)threadIdx.x & 3) + c, rows - 1));
     }
 
     // Masks of the keys 2t, 2t + 1 and 2t + 8, 2t + 9 of a record that lie in
@@ -553,12 +558,14 @@ __device__ __forceinline__ float *slot_of(const AttnArgs &a, int block, bool sta
            (size_t)(2 * block + (starts ? 1 : 0)) * kRowsMax * (D + 2);
 }
 
-// Four values of a row, l and m its sum and reference.
+// Four values of a row, l and m its sum and reference.  (With the approximate
+// division and logarithm here the kernel's main loop, of all things, compiled
+// to 40 % more time for 4-bit caches.)
 __device__ __forceinline__ void store_row(const AttnArgs &a, int b, int h, int row, int d,
                                           float4 o, float m, float l) {
-    const int i = row / a.group, hq = h * a.group + row - i * a.group;
+    const int i = token_of_row(a, row), hq = h * a.group + row - i * a.group;
     const long long t = (long long)b * a.tokens + i;
-    const float f = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;    // NaN stays NaN
+    const float f = l > 0.f ? 1.f / l : l;                     // 0 and NaN stay
     const long long at = t * a.out.token_stride + (long long)hq * a.out.head_stride + d;
     if (a.f32_out) {
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out.data) + at) =
@@ -683,17 +690,33 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int block_r
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = kNone, l = 0.f;
     if (there) {
-#pragma unroll 10
-        for (int c = group; c < head.w; c += GROUPS) {
-            const float *s = slot_of<D>(a, blockIdx.x + c, c == 0);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + row * D + d));
-            const float vm = __ldcg(s + kRowsMax * D + row);
-            const float vl = __ldcg(s + kRowsMax * D + kRowsMax + row);
-            const float now = fmaxf(m, vm), f = exp2_fast(m - now), g = exp2_fast(vm - now);
-            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-            add_scaled(o, g, v);
-            l = fmaf(l, f, vl * g);
-            m = now;
+        // AHEAD pieces are asked for together, however many there are: the
+        // remainder of an unrolled loop would take a trip to L2 for each
+        constexpr int AHEAD = 3;
+        for (int c0 = group; c0 < head.w; c0 += GROUPS * AHEAD) {
+            float4 v[AHEAD];
+            float vm[AHEAD], vl[AHEAD];
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                const int c = c0 + x * GROUPS;
+                const float *s = slot_of<D>(a, blockIdx.x + c, c == 0);
+                v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                vm[x] = kNone, vl[x] = 0.f;
+                if (c < head.w) {
+                    v[x] = __ldcg(reinterpret_cast<const float4 *>(s + row * D + d));
+                    vm[x] = __ldcg(s + kRowsMax * D + row);
+                    vl[x] = __ldcg(s + kRowsMax * D + kRowsMax + row);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                const float now = fmaxf(m, vm[x]), f = exp2_fast(m - now);
+                const float g = exp2_fast(vm[x] - now);
+                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                add_scaled(o, g, v[x]);
+                l = fmaf(l, f, vl[x] * g);
+                m = now;
+            }
         }
     }
     if (GROUPS > 1) {
@@ -935,23 +958,22 @@ attn_kernel(const AttnArgs a, const Plan plan) {
         // ---- join the groups of warps through shared memory
         float *join_o = reinterpret_cast<float *>(smem + plan.ring_bytes);
         if (works) {
-            const int g = lane >> 2, t = lane & 3;
+            const int g = lane >> 2, t = lane & 3, own = kg * block_rows + qg * 8 * NT + 2 * t;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int r = kg * block_rows + qg * 8 * NT + 8 * n + 2 * t;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float l = w.l[n][x];
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
-                    if (g == 0) join_m[r + x] = w.m[n][x], join_l[r + x] = l;
+                    const int r = own + 8 * n + x;
+                    if (g == 0) join_m[r] = w.m[n][x], join_l[r] = l;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            join_o[r * OROW + 16 * k + 8 * y + g] = w.o[n][k][2 * y + x];
                 }
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        join_o[(r + (x & 1)) * OROW + 16 * k + g + (x & 2) * 4] = w.o[n][k][x];
-            }
         }
         warps_sync<WARPS>();
         const int there = min(block_rows, a.tokens * a.group - p.tile0);
@@ -960,9 +982,9 @@ attn_kernel(const AttnArgs a, const Plan plan) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = kNone, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 5
+#pragma unroll 2
             for (int k = 0; k < plan.KG; ++k) m = fmaxf(m, join_m[k * block_rows + r]);
-#pragma unroll 5
+#pragma unroll 2
             for (int k = 0; k < plan.KG; ++k) {
                 const int at = k * block_rows + r;
                 const float f = exp2_fast(join_m[at] - m);
@@ -1023,11 +1045,14 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
                              dim3(256), 0, stream, a, block_rows);
 }
 
-// Two tiles a warp from 9 rows on: the operands of a record serve both.
+// Two tiles a warp where that makes half as many groups again: the operands of
+// a record serve both tiles, but fewer warps are there to wait.
 template <int FMT, int D>
 cudaError_t launch_rows(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    return a.tokens * a.group <= 8 ? launch<FMT, D, 1>(a, num_sms, stream)
-                                   : launch<FMT, D, 2>(a, num_sms, stream);
+    const int tiles = (a.tokens * a.group < kRowsMax ? a.tokens * a.group + 7 : kRowsMax) / 8;
+    const int one = compute_warps<1>() / tiles, two = compute_warps<2>() / ((tiles + 1) / 2);
+    return tiles > 1 && 2 * two >= 3 * one ? launch<FMT, D, 2>(a, num_sms, stream)
+                                           : launch<FMT, D, 1>(a, num_sms, stream);
 }
 
 }  // namespace

@@ -654,8 +654,8 @@ class PagedCache:
         return k, v
 
     def new_workspace(self) -> torch.Tensor:
-        """A zero-filled workspace for attend()."""
-        return torch.zeros(paged_attn_workspace_bytes(self), dtype=torch.uint8,
+        """A workspace for attend()."""
+        return torch.empty(paged_attn_workspace_bytes(self), dtype=torch.uint8,
                            device=self.pool.device)
 
     def attend(self, q, lens, table, scale=None, window: int = 0, out=None, lse=None,
