@@ -1036,7 +1036,7 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     if (a.pool.seqs == 1 && longest < 8 * p.KG && a.pool.kv_heads * p.row_tiles <= grid)
         return cudaSuccess;
     const int block_rows = 8 * NT * p.QG, rows = a.tokens * a.group;
-    constexpr int FEW = 2, MANY = 1024 / D;                   // rows of a joining block
+    constexpr int FEW = 2, MANY = 512 / D;                    // rows of a joining block
     if (rows <= 8)
         return launch_overlapped(join_kernel<D, FEW>, dim3(grid, (rows + FEW - 1) / FEW), dim3(256),
                                  0, stream, a, block_rows);
