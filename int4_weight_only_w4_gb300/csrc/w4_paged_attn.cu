@@ -43,7 +43,6 @@ namespace w4 {
 namespace {
 
 constexpr int kRowsMax = 64;           // rows of a block
-constexpr int kMaxWarps = 16;          // warps that compute
 constexpr int kMaxStages = 16;         // of one group's ring
 constexpr int kMaxGrid = 256;
 constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not there: past any length
@@ -736,11 +735,12 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int block_r
     if (there) store_row(a, head.x, head.y, head.z + row, d, o, m, l);
 }
 
-// Warps that compute: with the two that copy 16 of 128 registers, or 12 of 168.
+// Warps that compute; with the two that copy 20 of 96 registers, 16 of 128 or 12
+// of 168, by the values that a warp holds.
 constexpr int kCopyWarps = 2;
-template <int NT>
+template <int D, int NT>
 __host__ __device__ constexpr int compute_warps() {
-    return NT == 1 ? 14 : 10;
+    return D * NT == 64 ? 18 : D * NT == 128 ? 14 : 10;
 }
 
 // How a launch divides a block (host).
@@ -880,16 +880,16 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(32 * (compute_warps<NT>() + kCopyWarps), 1)
+__global__ void __launch_bounds__(32 * (compute_warps<D, NT>() + kCopyWarps), 1)
 attn_kernel(const AttnArgs a, const Plan plan) {
     extern __shared__ __align__(128) unsigned char smem[];
     using L = KvLayout<FMT, D>;
-    constexpr int WARPS = compute_warps<NT>();
+    constexpr int WARPS = compute_warps<D, NT>();
     constexpr int OROW = D + 4;                               // floats; + 4: no bank conflicts
-    __shared__ uint64_t full[kMaxWarps * kMaxStages], empty[kMaxWarps * kMaxStages];
+    __shared__ uint64_t full[WARPS * kMaxStages], empty[WARPS * kMaxStages];
     __shared__ uint64_t piece_full[2], piece_empty[2];
-    __shared__ int first_key[kMaxWarps * kMaxStages];         // of a stage's record, or kAbsent
-    __shared__ float join_m[kMaxWarps * 8 * NT], join_l[kMaxWarps * 8 * NT];
+    __shared__ int first_key[WARPS * kMaxStages];             // of a stage's record, or kAbsent
+    __shared__ float join_m[WARPS * 8 * NT], join_l[WARPS * 8 * NT];
     __shared__ Piece piece[2];
     const int block_rows = 8 * NT * plan.QG;
 
@@ -1005,7 +1005,7 @@ attn_kernel(const AttnArgs a, const Plan plan) {
 
 template <int FMT, int D, int NT>
 cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    constexpr int bytes = KvLayout<FMT, D>::kBytes, WARPS = compute_warps<NT>();
+    constexpr int bytes = KvLayout<FMT, D>::kBytes, WARPS = compute_warps<D, NT>();
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1045,13 +1045,17 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
                              dim3(256), 0, stream, a, block_rows);
 }
 
-// Two tiles a warp where that makes half as many groups again: the operands of
-// a record serve both tiles, but fewer warps are there to wait.
+// Two tiles a warp where that makes a third as many groups again: the operands
+// of a record serve both tiles, but fewer warps are there to wait.  Measured at
+// 48 x 4 k tokens of 64 bf16 values: 3 tiles 26.7 us with one, 27.9 with two;
+// 4 tiles 32.6, 28.3; 5 tiles 39.5, 34.8; 7 tiles 50.7, 42.9; at 8 x 8 k of 128:
+// 2 tiles 31.5, 33.2; 3 tiles 34.5, 37.1; 5 tiles 43.9, 41.7; 6 tiles 48.1, 43.2;
+// 7 tiles 50.0, 54.2.
 template <int FMT, int D>
 cudaError_t launch_rows(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     const int tiles = (a.tokens * a.group < kRowsMax ? a.tokens * a.group + 7 : kRowsMax) / 8;
-    const int one = compute_warps<1>() / tiles, two = compute_warps<2>() / ((tiles + 1) / 2);
-    return tiles > 1 && 2 * two >= 3 * one ? launch<FMT, D, 2>(a, num_sms, stream)
+    const int one = compute_warps<D, 1>() / tiles, two = compute_warps<D, 2>() / ((tiles + 1) / 2);
+    return tiles > 2 && 3 * two >= 4 * one ? launch<FMT, D, 2>(a, num_sms, stream)
                                            : launch<FMT, D, 1>(a, num_sms, stream);
 }
 

@@ -556,12 +556,13 @@ def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, work
     B = table.shape[0]
     if T % B or D != cache.head_dim or out.shape != q.shape:
         raise ValueError("q, out: expected [seqs * tokens, q_heads, head_dim]")
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != T * H):
-        raise ValueError("lse: expected float32 [seqs * tokens, q_heads]")
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.numel() != T * H:
+            raise ValueError("lse: expected float32 [seqs * tokens, q_heads]")
+        lse = _ptr(lse)
     _ok(fn(cache.ref, _heads(q), _heads(out, dtype), H, T // B, _int32(lens, B, "lens"),
-           _block_table(table), D ** -0.5 if scale is None else scale, window, _ptr(lse),
-           _ptr(workspace), workspace.numel() * workspace.element_size(),
-           _raw_stream(stream, q)), where)
+           _block_table(table), D ** -0.5 if scale is None else scale, window, lse,
+           _ptr(workspace), workspace.nbytes, _raw_stream(stream, q)), where)
 
 
 def paged_attn(cache: "PagedCache", q, out, lens, table, workspace, scale=None, window: int = 0,
