@@ -807,7 +807,11 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
         // are on their way)
         const int slot = told & 1;
         const bool tells = copier == 0 && lane == 0;
-        if (copier == 0 && told >= 2) mbar_wait(&piece_empty[slot], (told >> 1) + 1 & 1);
+        if (copier == 0 && told >= 2 &&
+            !__all_sync(0xFFFFFFFFu, mbar_wait(&piece_empty[slot], ((told >> 1) + 1) & 1))) {
+            if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_WAIT);   // never in normal operation
+            break;
+        }
         Piece &p = piece[slot];
         if (tells) {
             p.b = more ? c.b : -1;
