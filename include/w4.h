@@ -544,10 +544,10 @@ w4_status w4_rope(const w4_heads *x, const w4_heads *y, int tokens, int heads, i
  *   int8, int4: then 16 key and 16 value descriptors, uint32: binary16 scale
  *           s | zero point z << 16
  * for 64 D bytes (bf16), 32 D + 128 (int8) or 16 D + 128 (int4) in all.
- * A token's key (value) of a head is one group, quantised as by
- * W4_QUANT_ASYMMETRIC with Q = 255 or 15 levels, in fp32, each operation
- * rounded to nearest even: lo = min(0, min x), hi = max(0, max x),
- * s = binary16((hi - lo) / Q) (at most 65504), z = clamp(rint(-lo / s), 0, Q),
+ * A token's key (value) of a head is one group, quantised with a zero point to
+ * Q = 255 or 15 levels, in fp32, each operation rounded to nearest even:
+ * lo = min(0, min x), hi = max(0, max x), s = binary16((hi - lo) * r) with r the
+ * fp32 value of 1 / Q (s at most 65504), z = clamp(rint(-lo / s), 0, Q),
  * q = clamp(rint(x / s) + z, 0, Q), read back as (q - z) * s; s = 0 stores
  * z = q = 0.  An infinite value is held as the largest that the scale reaches,
  * NaN as 0; bf16 caches keep both.

@@ -1,9 +1,11 @@
 // The paged key-value cache: writing tokens (w4_kv_append: rotation of q and
 // k, quantisation, the record layout) and reading them back (w4_kv_read).
 //
-// Mathematics of a (token, head) group: w4_quantize's asymmetric rule with
-// Q = 255 or 15 levels (include/w4.h), every operation rounded to nearest in
-// fp32, so the codes are those of any other evaluation of the rule bit for bit.
+// Mathematics of a (token, head) group: the rule of include/w4.h, w4_quantize's
+// asymmetric one with Q = 255 or 15 levels but for the scale, which is a
+// product with 1 / Q instead of a quotient; every operation rounded to nearest
+// in fp32, so the codes are those of any other evaluation of the rule bit for
+// bit.
 //
 // A tile is up to 16 listed tokens, cut so that the tokens of a sequence in
 // order fall into whole records.  A warp takes the keys, or the values, of a
@@ -281,9 +283,9 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                 lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
                 hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
             }
-            constexpr float top = (float)L::kLevels;
+            constexpr float level = 1.f / L::kLevels;
             const __half sh =
-                __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), top), 65504.f));
+                __float2half_rn(fminf(__fmul_rn(__fsub_rn(hi, lo), level), 65504.f));
             const float s = __half2float(sh);
             int z = 0, n8[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (s > 0.f) codes_of<L::kBits>(x, lo, hi, s, &z, n8);

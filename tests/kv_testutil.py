@@ -85,7 +85,7 @@ def quantise(x: np.ndarray, fmt: str):
     top = np.float32(LEVELS[fmt])
     lo = np.minimum(x.min(-1), np.float32(0))
     hi = np.maximum(x.max(-1), np.float32(0))
-    s16 = np.minimum((hi - lo) / top, np.float32(65504)).astype(np.float16)
+    s16 = np.minimum((hi - lo) * (np.float32(1) / top), np.float32(65504)).astype(np.float16)
     s = s16.astype(np.float32)
     safe = np.where(s == 0, np.float32(1), s)
     z = np.where(s == 0, np.float32(0), np.clip(np.rint(-lo / safe), 0, top))

@@ -238,3 +238,24 @@ def test_refusals(w4):
         w4.PagedCache.make(2, w4.KV_INT4, 2, 96)
     with pytest.raises(w4.W4Error):
         w4.PagedCache.make(2, w4.KV_INT4, 2, 64, page_tokens=24)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("layout", [None, 0, 1])
+def test_codes_of_many_values(w4, fmt, layout):
+    """Every code of 4096 tokens: the scales that round the other way and the
+    quotients next to a half, which small cases hardly meet."""
+    rng = np.random.default_rng(7)
+    T, H, D = 4096, 4, 128
+    x, pos = rows(rng, T, H, D), np.arange(T, dtype=np.int32)
+    table = torch.arange(T // 16, dtype=torch.int32, device="cuda").view(1, -1)
+    rope, xr = None, x
+    if layout is not None:
+        angle = pos[:, None] * 1e6 ** (-np.arange(0, D, 2) / D)
+        tab = np.stack([np.cos(angle), np.sin(angle)], -1).astype(np.float32)
+        rope, xr = w4.RopeTable(torch.from_numpy(tab).cuda(), layout), kv.rotate(x, pos, tab, layout)
+    cache = w4.PagedCache.make(T // 16, kv.FMT[fmt], H, D)
+    cache.append(to_gpu(x), to_gpu(x), i32(pos), table, rope=rope)
+    k, v = cache.read(i32(pos), table)
+    assert np.array_equal(bits(k), kv.bf16_bits(kv.held(xr, fmt)))
+    assert np.array_equal(bits(v), kv.bf16_bits(kv.held(x, fmt)))
