@@ -115,10 +115,11 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     if ((long long)table->width * cache->page_tokens >= (1LL << 31) ||
         (long long)table->seqs * q_heads * tokens >= (1LL << 31))
         return W4_ERR_UNSUPPORTED;
-    // records that the call could visit, counted in 32 bits
+    // records that the call could visit, counted in 32 bits (a head costs up to
+    // 128 records more)
     const long long row_tiles = ((long long)tokens * (q_heads / cache->kv_heads) + 63) / 64;
     const long long longest =
-        (long long)table->width * (cache->page_tokens / w4::kRecTokens) + 1;
+        (long long)table->width * (cache->page_tokens / w4::kRecTokens) + 128;
     if (longest * table->seqs >= (1LL << 31) ||
         longest * table->seqs * cache->kv_heads >= (1LL << 31) ||
         longest * table->seqs * cache->kv_heads * row_tiles >= (1LL << 31))

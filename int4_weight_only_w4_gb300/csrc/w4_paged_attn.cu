@@ -26,8 +26,11 @@
 //
 // Schedule.  The blocks, one per SM, divide the list (sequence, head, record)
 // evenly among themselves, from the lengths on the device: block c takes the
-// records from cut c to cut c + 1.  A cut that would leave only a few records
-// of a head on one side moves to the head's border, so short heads stay whole.
+// records from cut c to cut c + 1.  A head counts for some records more than it
+// has, what it costs to start and to finish one: without that, blocks with many
+// short heads came last, and 64 ragged sequences of up to 8192 tokens in 8 bits
+// took 64 us instead of 50.  A cut that would leave only a few records of a head
+// on one side moves to the head's border.
 // The pieces of cut heads are joined by a second kernel that is already
 // resident when the first one ends, a few rows a block: left to the block that
 // finished a head last, the joining of 5 pieces of 56 rows took 7 us.  In a
@@ -43,6 +46,11 @@ namespace w4 {
 namespace {
 
 constexpr int kRowsMax = 64;           // rows of a block
+// What a head's start and end cost, in records of one tile of rows.  Ragged
+// batches: 64 x 8k int8 64 us at 0, 50.8 at 28, 49.7 at 40, 50.5 at 56; 8 new
+// tokens over 8 x 8k bf16 44.1, 33.8, 30.4, 30.7; 64 x 8k int4 57.6, 43.6, 41.4,
+// 40.2; even ones lose a little (8 x 2k bf16 12.0, 13.5, 12.6, 12.7).
+constexpr int kHeadRecords = 40;
 constexpr int kMaxStages = 16;         // of one group's ring
 constexpr int kMaxGrid = 256;
 constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not there: past any length
@@ -582,26 +590,40 @@ __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) 
     o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
 }
 
+// How a launch divides a block (host).
+struct Plan {
+    int row_tiles;     // blocks of rows per key/value head
+    int QG, KG;        // warps on a record, groups of them
+    int stages;        // records of a group's ring
+    int ring_bytes;    // of all rings
+    int extra;         // see List
+};
+
 // A place in the list of records (the host refuses lists of 2^31).
 struct Cut {
     int b, item, u;        // sequence, head (x row tile) of it, record of that
 };
 
 // The list, as a warp sees it: lane i holds sequences [b0, b1), whose items
-// have the records [before, before + mine) * per_seq.
+// cost [before, before + mine) * per_seq.
 struct List {
     int b0, b1, before, mine, per_seq, work;
+    int extra;             // what a head costs beside its records
     int blocks, least;     // blocks that have a stretch, records that are not cut off
     int q, rest;           // work / blocks and its remainder
     unsigned magic;        // 2^32 / blocks, rounded up
 
-    __device__ __forceinline__ List(const AttnArgs &a, int row_tiles, int KG) {
+    __device__ __forceinline__ int cost(const AttnArgs &a, int b) const {
+        return sequence(a, b).records + extra;
+    }
+
+    __device__ __forceinline__ List(const AttnArgs &a, const Plan &plan) : extra(plan.extra) {
         const int lane = threadIdx.x & 31, each = (a.pool.seqs + 31) >> 5;
-        per_seq = a.pool.kv_heads * row_tiles;
+        per_seq = a.pool.kv_heads * plan.row_tiles;
         b0 = min(lane * each, a.pool.seqs), b1 = min(b0 + each, a.pool.seqs);
         mine = 0;
 #pragma unroll 4
-        for (int b = b0; b < b1; ++b) mine += max(sequence(a, b).records, 1);
+        for (int b = b0; b < b1; ++b) mine += cost(a, b);
         int upto = mine;
         if (a.pool.seqs > 1) {
 #pragma unroll
@@ -616,10 +638,10 @@ struct List {
         // records a group that the mean head has (so heads of one length are
         // cut alike), while there are blocks
         const int heads = a.pool.seqs * per_seq;
-        blocks = min(min((int)gridDim.x, work), heads * max(1, work / (heads * 4 * KG)));
+        blocks = min((int)gridDim.x, heads * max(1, (work / heads - extra) / (4 * plan.KG)));
         q = work / blocks, rest = work - q * blocks;
         magic = 0xFFFFFFFFu / (unsigned)blocks + 1;
-        least = min(4 * KG, max(KG, q >> 3));
+        least = max(plan.KG, extra / 2);
     }
 
     // Start of block c's stretch.  rest * c < 2^16, so the product with magic
@@ -628,7 +650,7 @@ struct List {
         return q * c + (int)__umulhi((unsigned)(rest * c), magic);
     }
 
-    // Place of record u of the list, moved to its head's border where fewer
+    // The record at cost u of the list, moved to its head's border where fewer
     // than `least` records would be cut off.
     __device__ __forceinline__ Cut cut(const AttnArgs &a, int u) const {
         const bool here = u >= before * per_seq && u < (before + mine) * per_seq;
@@ -636,7 +658,7 @@ struct List {
         if (a.pool.seqs > 1) {
             if (here)
                 for (;; ++b) {
-                    n = max(sequence(a, b).records, 1);
+                    n = cost(a, b);
                     if (in < n * per_seq) break;
                     in -= n * per_seq;
                 }
@@ -648,10 +670,10 @@ struct List {
         n = __shfl_sync(0xFFFFFFFFu, n, src);
         in = __shfl_sync(0xFFFFFFFFu, in, src);
         c.item = found ? in / n : 0;
-        c.u = found ? in - c.item * n : 0;
+        c.u = found ? in - c.item * n - extra : 0;
         if (!found) c.b = a.pool.seqs;                        // the list's end
-        if (found && (c.u < least || n - c.u < least)) {
-            if (2 * c.u > n && ++c.item == per_seq) c.item = 0, ++c.b;
+        if (found && (c.u < least || n - extra - c.u < least)) {
+            if (2 * (c.u + extra) > n && ++c.item == per_seq) c.item = 0, ++c.b;
             c.u = 0;
         }
         return c;
@@ -743,14 +765,6 @@ __host__ __device__ constexpr int compute_warps() {
     return D * NT == 64 ? 18 : D * NT == 128 ? 14 : 10;
 }
 
-// How a launch divides a block (host).
-struct Plan {
-    int row_tiles;     // blocks of rows per key/value head
-    int QG, KG;        // warps on a record, groups of them
-    int stages;        // records of a group's ring
-    int ring_bytes;    // of all rings
-};
-
 // A stretch's part of one head, as the copying warp tells the others.
 struct Piece {
     int b;             // sequence; -1: no more pieces
@@ -772,7 +786,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     using L = KvLayout<FMT, D>;
     const int lane = threadIdx.x & 31, KG = plan.KG, stages = plan.stages;
     const int copier = (threadIdx.x >> 5) - WARPS, kg = kCopyWarps * lane + copier;
-    const List list(a, plan.row_tiles, KG);
+    const List list(a, plan);
     const int per_seq = list.per_seq;
     Cut c, to;
     c.b = 0, c.item = 0, c.u = 0;
@@ -789,9 +803,8 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     while (true) {
         const bool more = c.b < to.b || c.item < to.item || c.u < to.u;
         const Seq seq = sequence(a, more ? c.b : 0);
-        const int n_seq = max(seq.records, 1);
         const bool last = c.b == to.b && c.item == to.item;
-        const int u1 = last ? to.u : n_seq, stop = min(u1, seq.records);
+        const int stop = last ? to.u : seq.records;
         const int h = c.item / plan.row_tiles;
         const int32_t *pages = a.pool.table + (more ? c.b : 0) * a.pool.stride;
         constexpr int AHEAD = 4;
@@ -817,18 +830,18 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
             p.b = more ? c.b : -1;
             p.h = h, p.tile0 = (c.item - h * plan.row_tiles) * block_rows;
             p.u0 = c.u, p.stop = stop, p.len = seq.len;
-            p.whole = c.u == 0 && u1 == n_seq, p.starts = c.u == 0;
+            p.whole = c.u == 0 && stop == seq.records, p.starts = c.u == 0;
         }
-        if (copier == 0 && more && c.u == 0 && u1 != n_seq) {
+        if (copier == 0 && more && c.u == 0 && stop != seq.records) {
             // the cuts inside this head, at least `least` records from its borders
             const bool mine = c.b >= list.b0 && c.b < list.b1;
-            int head = list.before * per_seq + c.item * n_seq;
+            const int n = seq.records + list.extra;
+            int head = list.before * per_seq + c.item * n;
             if (mine)
-                for (int x = list.b0; x < c.b; ++x)
-                    head += max(sequence(a, x).records, 1) * per_seq;
+                for (int x = list.b0; x < c.b; ++x) head += list.cost(a, x) * per_seq;
             head = __shfl_sync(0xFFFFFFFFu, head, __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1);
-            const int c_lo = list.block_from(head + list.least);
-            const int c_hi = list.block_from(head + n_seq - list.least + 1) - 1;
+            const int c_lo = list.block_from(head + list.extra + list.least);
+            const int c_hi = list.block_from(head + n - list.least + 1) - 1;
             if (tells) p.pieces = c_hi - c_lo + 2;
         }
         if (tells) mbar_arrive(&piece_full[slot]);
@@ -1031,6 +1044,7 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     p.stages = (kSharedBytes - p.KG * join_row) / (p.KG * bytes);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.ring_bytes = p.KG * p.stages * bytes;
+    p.extra = kHeadRecords / ((p.QG * NT + 1) / 2);
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
     e = launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
                           kSharedBytes, stream, a, p);
