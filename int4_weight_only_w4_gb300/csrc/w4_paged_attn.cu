@@ -15,14 +15,17 @@
 // accumulator, packed to 16 bits and transposed by movmatrix, is the second
 // product's column operand: nothing goes through shared memory.
 //
-// Quantised records.  A code becomes the binary16 1024 + u (or 1024 + 16 u for
-// a high nibble) by one logic operation a pair, and u - z, exact, by one
-// addition (fma) a pair.  Leaving the products with 1024 + z to one correction
-// per score would save the addition, but rounds the scores at 1024 times the
-// codes' unit: the 4-bit log-sum-exp was then off by 2e-4.  A key's scale
-// multiplies its scores; a value's scale goes into its probability,
-// p s_v = exp2(y + log2 s_v - m), m taken over that sum, so that p fits
-// binary16 whatever the scales are.
+// Quantised records.  The bits of a code u (or 16 u, a high nibble) are the
+// binary16 number u 2^-24 (16 u 2^-24; the 1/16 goes into q): a key's operand is
+// one logic operation a pair, and its sum of q starts at -z sum q.  A value's
+// code becomes 1024 + u by one operation and u - z, exact, by another: left to
+// one correction of the sum, z would make the sum over a long cache many times
+// larger than what is left of it, and fp32 accumulation loses the difference.
+// (The keys' products are 8 long.  With 1024 + z left in the scores, they were
+// rounded at 1024 times the codes' unit and the 4-bit log-sum-exp was off by
+// 2e-4.)  A key's scale multiplies its scores; a value's scale goes into its
+// probability, p s_v = exp2(y + log2 s_v - m), m taken over that sum, so that p
+// fits binary16 whatever the scales are.
 //
 // Schedule.  The blocks, one per SM, divide the list (sequence, head, record)
 // evenly among themselves, from the lengths on the device: block c takes the
@@ -55,6 +58,7 @@ constexpr int kMaxStages = 16;         // of one group's ring
 constexpr int kMaxGrid = 256;
 constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not there: past any length
 constexpr int kSharedBytes = 224256;   // rings and join: 219 of the 227 KB of a block
+constexpr float kCodeUnit = 0x1p-24f;  // what the bits of a code are in binary16
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen no key
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
@@ -147,6 +151,7 @@ struct Tile {
     float o[NT][KS][4];
     float m[NT][2], l[NT][2];    // columns 2t, 2t + 1 of each tile
     float sc[NT][2];             // score factor of a column
+    float qs[NT][2];             // quantised: -(sum of its q), in the products' unit
 
     // Which value of the head goes with half e of register i of k-step ks.
     __device__ static constexpr int q_index(int ks, int i, int e, int t) {
@@ -200,21 +205,34 @@ struct Tile {
                         top = fmaxf(top, fmaxf(fabsf(value(ks, j, 0)), fabsf(value(ks, j, 1))));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                // a power of two that brings the largest |q| into [2^14, 2^15):
-                // q is exact in binary16 down to 2^-28 of it
+                // a power of two that brings the largest |q| into [2^14, 2^15);
+                // in 4 bits what meets high nibbles (16 u) is 1/16 of that: q is
+                // exact in binary16 down to 2^-27 of the largest
                 int e = 0;
                 if (top > 0.f && top < INFINITY)
                     e = 14 - max(-86, (int)(__float_as_uint(top) >> 23) - 127);
                 const float up = __int_as_float((127 + e) << 23);
+                float sum = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        qf[n][ks][j] = pack_half(value(ks, j, 0) * up, value(ks, j, 1) * up);
-                const float f = a.scale * kLog2e * __int_as_float((127 - e) << 23);
+                    for (int j = 0; j < 2; ++j) {
+                        const float x = value(ks, j, 0) * up, y = value(ks, j, 1) * up;
+                        const float less = FMT == W4_KV_INT4 && j == 1 ? 0.0625f : 1.f;
+                        sum += x + y;
+                        qf[n][ks][j] = pack_half(x * less, y * less);
+                    }
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                sum *= -kCodeUnit;
+                // (finite: a score of 0 stays 0 whatever q is)
+                float f = a.scale * kLog2e * __int_as_float((127 - e) << 23) / kCodeUnit;
+                f = fminf(fmaxf(f, -3.0e38f), 3.0e38f);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
                     sc[n][c] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t + c));
+                    qs[n][c] = __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * t + c));
+                }
             }
         }
     }
@@ -231,11 +249,14 @@ struct Tile {
         }
     }
 
-    // Operands of four codes: bytes 0, 2 of a word of 8-bit codes, or the low
-    // (high) nibbles of bytes 0, 2; minus: -(1024 + z) of their keys (high
-    // nibbles: (1024 + 16 u) / 16 - (64 + z)).
+    // Values' operands of four codes: bytes 0, 2 (1, 3) of a word of 8-bit codes,
+    // or the low (high) nibbles of bytes 0, 2; minus: -(1024 + z) of their keys
+    // (high nibbles: (1024 + 16 u) / 16 - (64 + z)).
     __device__ static uint32_t even(uint32_t w, uint32_t minus) {
         return half2_add(and_or(w, 0x00FF00FFu, 0x64006400u), minus);
+    }
+    __device__ static uint32_t odd(uint32_t w, uint32_t minus) {
+        return half2_add(__byte_perm(w, 0x64646464u, 0x4341), minus);
     }
     __device__ static uint32_t low(uint32_t w, uint32_t minus) {
         return half2_add(and_or(w, 0x000F000Fu, 0x64006400u), minus);
@@ -292,25 +313,27 @@ struct Tile {
                 lds64(w0, r0 + t * 8);
                 lds64(w1, r1 + t * 8);
             }
-            uint32_t zk[2], zk16[2];      // -(1024 + z), -(64 + z) of keys g, g + 8, twice each
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 mk[r] = lds32(rec + L::kMeta + 4 * (g + 8 * r));
                 mv[r] = lds32(rec + L::kMetaV + 4 * (g + 8 * r));
-                zk[r] = __byte_perm(mk[r], 0u, 0x4242) | 0xE400E400u;
-                zk16[r] = half2_add(zk[r], 0x63806380u);  // + 960
+                const float z = __uint_as_float(__byte_perm(mk[r], 0x4B000000u, 0x7332)) - 0x1p23f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) s[n][2 * r + c] = z * qs[n][c];
             }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 uint32_t a0, a1, a2, a3;
                 if constexpr (FMT == W4_KV_INT8) {
-                    a0 = even(w0[ks], zk[0]), a1 = even(w1[ks], zk[1]);
-                    a2 = even(w0[ks] >> 8, zk[0]), a3 = even(w1[ks] >> 8, zk[1]);
+                    a0 = w0[ks] & 0x00FF00FFu, a1 = w1[ks] & 0x00FF00FFu;
+                    a2 = __byte_perm(w0[ks], 0u, 0x4341), a3 = __byte_perm(w1[ks], 0u, 0x4341);
                 } else {
                     const uint32_t x0 = ks & 1 ? w0[ks >> 1] >> 8 : w0[ks >> 1];
                     const uint32_t x1 = ks & 1 ? w1[ks >> 1] >> 8 : w1[ks >> 1];
-                    a0 = low(x0, zk[0]), a1 = low(x1, zk[1]);
-                    a2 = high(x0, zk16[0]), a3 = high(x1, zk16[1]);
+                    a0 = x0 & 0x000F000Fu, a1 = x1 & 0x000F000Fu;
+                    a2 = x0 & 0x00F000F0u, a3 = x1 & 0x00F000F0u;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -347,7 +370,7 @@ struct Tile {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        s[n][2 * r + c] = fmaf(s[n][2 * r + c], sk * sc[n][c], lv);
+                        s[n][2 * r + c] = fmaf(s[n][2 * r + c] * sc[n][c], sk, lv);
             }
         }
         uint32_t keep[2];
@@ -449,7 +472,7 @@ struct Tile {
                 if constexpr (FMT == W4_KV_INT8) {
                     const uint32_t u = vraw[2 * k], v = vraw[2 * k + 1];
                     a0 = even(u, zlo[0]), a1 = even(v, zlo[0]);
-                    a2 = even(u >> 8, zlo[1]), a3 = even(v >> 8, zlo[1]);
+                    a2 = odd(u, zlo[1]), a3 = odd(v, zlo[1]);
                 } else {
                     const uint32_t u = vraw[k], v = vraw[k] >> 8;
                     a0 = low(u, zlo[0]), a1 = high(u, zhi[0]);
