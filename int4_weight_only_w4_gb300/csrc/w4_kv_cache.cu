@@ -140,11 +140,6 @@ __device__ __forceinline__ uint32_t to_nibbles(const int (&n)[8]) {
     return w;
 }
 
-// The float of byte i of w, less z = 2^23 + the zero point: exact.
-__device__ __forceinline__ float byte_less(uint32_t w, int i, float z) {
-    return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i)), z);
-}
-
 // The queries of a launch of append_kernel, turned as by w4_rope in blocks of
 // their own (in the rows' loop below every lane would turn its partner too:
 // 16 k tokens of 28 query heads 146 us against 84).
@@ -290,7 +285,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
             int z = 0, n8[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (s > 0.f) codes_of<L::kBits>(x, lo, hi, s, &z, n8);
             // values: the bytes of a whole record go to shared memory first
-            unsigned char *to = whole ? staged[warp] - L::kPart : rec;
+            unsigned char *to = whole ? staged[warp] : rec + L::kPart;
             if constexpr (FMT == W4_KV_INT8) {
                 const uint32_t b0 = to_bytes(n8[0], n8[1], n8[2], n8[3]);
                 const uint32_t b1 = to_bytes(n8[4], n8[5], n8[6], n8[7]);
@@ -299,7 +294,8 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                 if (valid && is_v) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        to[L::value(rr, 8 * c + i)] = (unsigned char)((i < 4 ? b0 : b1) >> 8 * (i & 3));
+                        to[L::value(rr, 8 * c + i) - L::kPart] =
+                            (unsigned char)((i < 4 ? b0 : b1) >> 8 * (i & 3));
                 }
             } else if (!is_v) {
                 if (valid) *reinterpret_cast<uint32_t *>(rec + L::key(rr, 8 * c)) = to_nibbles(n8);
@@ -319,7 +315,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                 if (valid) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        to[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i)] =
+                        to[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i) - L::kPart] =
                             (unsigned char)(bytes >> 8 * i);
                 }
             }
@@ -337,13 +333,129 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
         out[32 * i + lane] = reinterpret_cast<const uint4 *>(staged[warp])[32 * i + lane];
 }
 
+// Eight values of a row from their codes, (u - z) s each; zm: -(2^23 + z).
+__device__ __forceinline__ uint4 row_values(uint32_t c0, uint32_t c1, Two zm, Two ss) {
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? c0 : c1;
+        Two y;
+        y.i.x = __byte_perm(w, 0x4B000000u, 0x7540 + 2 * (i & 1));
+        y.i.y = __byte_perm(w, 0x4B000000u, 0x7541 + 2 * (i & 1));
+        y = mul2(add2(y, zm), ss);                            // the sum is exact
+        out[i] = bf16_pair(y.f.x, y.f.y);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+__device__ __forceinline__ float less_of(uint32_t meta) { return -(float)(8388608 + (meta >> 16)); }
+__device__ __forceinline__ float scale_of(uint32_t meta) {
+    return __half2float(__ushort_as_half((unsigned short)(meta & 0xFFFFu)));
+}
+// The codes of 8 of a key's values: nibbles 0, 2, 4, 6 and 1, 3, 5, 7 to bytes,
+// then in order.
+__device__ __forceinline__ void key_codes(uint32_t w, uint32_t *code) {
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
+    code[0] = __byte_perm(lo, hi, 0x5140);
+    code[1] = __byte_perm(lo, hi, 0x7362);
+}
+
+// A whole record's keys to 16 rows from `dst` on: every lane's loads at once.
+template <int FMT, int D>
+__device__ __forceinline__ void read_keys(const unsigned char *rec, __nv_bfloat16 *dst,
+                                          long long stride) {
+    using L = KvLayout<FMT, D>;
+    constexpr int LANES = D / 8, TOKENS = 32 / LANES, STEPS = kRecTokens / TOKENS;
+    const int lane = threadIdx.x & 31, c = lane % LANES, r0 = lane / LANES;
+    uint32_t meta[STEPS];
+    uint2 w[STEPS];
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x) {
+        const unsigned char *at = rec + L::key(x * TOKENS + r0, 8 * c);
+        meta[x] = *reinterpret_cast<const uint32_t *>(rec + L::kMeta + 4 * (x * TOKENS + r0));
+        if (FMT == W4_KV_INT8)
+            w[x] = *reinterpret_cast<const uint2 *>(at);
+        else
+            w[x].x = *reinterpret_cast<const uint32_t *>(at);
+    }
+    dst += r0 * stride + 8 * c;
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x) {
+        uint32_t code[2];
+        if (FMT == W4_KV_INT4)
+            key_codes(w[x].x, code);
+        else
+            code[0] = w[x].x, code[1] = w[x].y;
+        *reinterpret_cast<uint4 *>(dst + x * TOKENS * stride) =
+            row_values(code[0], code[1], twice(less_of(meta[x])), twice(scale_of(meta[x])));
+    }
+}
+
+// A whole record's values: a lane's 16 bytes are of two tokens (and two more,
+// 8 on) and one d modulo 8, so the values come out as 8 x 8 matrices d x token,
+// which stmatrix turns on their way to the rows in shared memory.  (Gathered
+// byte by byte from there, reading 16 k tokens of 4 heads took 21 us.)
+template <int FMT, int D>
+__device__ __forceinline__ void read_values(const unsigned char *rec, unsigned char *rows,
+                                            __nv_bfloat16 *dst, long long stride) {
+    using L = KvLayout<FMT, D>;
+    constexpr int LANES = D / 8, TOKENS = 32 / LANES, STEPS = kRecTokens / TOKENS;
+    constexpr int ROW = 2 * D + 16, PIECES = L::kPart / 512;
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    uint4 raw[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+        raw[i] = *reinterpret_cast<const uint4 *>(rec + L::kPart + i * 512 + lane * 16);
+    Two zm[2], ss[2];                                         // of tokens 2t, 2t + 1 (+ 8)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint2 m = *reinterpret_cast<const uint2 *>(rec + L::kMetaV + 4 * (2 * t + 8 * h));
+        zm[h].f = make_float2(less_of(m.x), less_of(m.y));
+        ss[h].f = make_float2(scale_of(m.x), scale_of(m.y));
+    }
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(rows) + (lane & 15) * ROW +
+                        (lane >> 4) * 16;
+    const auto pair = [&](uint32_t v, int h) {
+        Two y;
+        y.i.x = __byte_perm(v, 0x4B000000u, 0x7540 + h);
+        y.i.y = __byte_perm(v, 0x4B000000u, 0x7542 + h);
+        y = mul2(add2(y, zm[h]), ss[h]);                      // the sum is exact
+        return bf16_pair(y.f.x, y.f.y);
+    };
+    const auto put = [&](int x, uint32_t v0, uint32_t v1) {   // d of 8 x .. 8 x + 15
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         at + 16 * x),
+                     "r"(pair(v0, 0)), "r"(pair(v0, 1)), "r"(pair(v1, 0)), "r"(pair(v1, 1))
+                     : "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        if constexpr (FMT == W4_KV_INT8) {
+            put(4 * i, w[0], w[1]);
+            put(4 * i + 2, w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                put(8 * i + 2 * j, w[j] & 0x0F0F0F0Fu, w[j] >> 4 & 0x0F0F0F0Fu);
+        }
+    }
+    __syncwarp();
+    const int c = lane % LANES, r0 = lane / LANES;
+    dst += r0 * stride + 8 * c;
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x)
+        *reinterpret_cast<uint4 *>(dst + x * TOKENS * stride) =
+            *reinterpret_cast<const uint4 *>(rows + (x * TOKENS + r0) * ROW + 16 * c);
+}
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvThreads)
 read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split) {
     using L = KvLayout<FMT, D>;
     constexpr int LANES = D / 8, TOKENS = 32 / LANES, STEPS = kRecTokens / TOKENS;
     __shared__ Tile16 tile;
-    __shared__ __align__(16) unsigned char staged[kKvWarps][FMT == W4_KV_BF16 ? 16 : L::kPart];
+    __shared__ __align__(16) unsigned char
+        turned[kKvWarps][FMT == W4_KV_BF16 ? 16 : kRecTokens * (2 * D + 16)];
     begin_after_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
     const int parts = (2 * pool.kv_heads * split + kKvWarps - 1) / kKvWarps;    // of a tile
@@ -360,17 +472,19 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split)
     const long long head_bytes = (long long)h * pool.page_records * L::kBytes;
     if (count <= 0 || task >= 2 * pool.kv_heads || !(is_v ? v : k).data) return;
     __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>((is_v ? v : k).data) +
-                         h * (is_v ? v : k).head_stride + 8 * c;
+                         h * (is_v ? v : k).head_stride;
     const long long stride = (is_v ? v : k).token_stride;
-    const bool apart = FMT != W4_KV_BF16 && whole && is_v && split == 1;
-    if (apart) {
-        const uint4 *in = reinterpret_cast<const uint4 *>(
-            tile.record[0] + head_bytes + L::kPart);
-#pragma unroll
-        for (int i = 0; i < L::kPart / 512; ++i)
-            reinterpret_cast<uint4 *>(staged[warp])[32 * i + lane] = in[32 * i + lane];
-        __syncwarp();
+    if constexpr (FMT != W4_KV_BF16) {
+        if (whole && split == 1) {
+            const unsigned char *rec = tile.record[0] + head_bytes;
+            if (is_v)
+                read_values<FMT, D>(rec, turned[warp], dst + i0 * stride, stride);
+            else
+                read_keys<FMT, D>(rec, dst + i0 * stride, stride);
+            return;
+        }
     }
+    dst += 8 * c;
 #pragma unroll 2
     for (int x0 = part; x0 < STEPS; x0 += split) {
         const int n = x0 * TOKENS + lane / LANES, r = min(first + n, kRecTokens - 1);
@@ -384,14 +498,11 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split)
         } else {
             const uint32_t m = *reinterpret_cast<const uint32_t *>(
                 rec + (is_v ? L::kMetaV : L::kMeta) + 4 * rr);
-            const float s = __half2float(__ushort_as_half((unsigned short)(m & 0xFFFFu)));
-            const float z = (float)(8388608 + (m >> 16));
             uint32_t code[2] = {0u, 0u};
             if (is_v) {
-                const unsigned char *from = apart ? staged[warp] - L::kPart : rec;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    code[i / 4] |= (uint32_t)from[L::value(rr, 8 * c + i)] << (8 * (i % 4));
+                    code[i / 4] |= (uint32_t)rec[L::value(rr, 8 * c + i)] << (8 * (i % 4));
                 if (FMT == W4_KV_INT4) {
                     code[0] = code[0] >> (4 * (c & 1)) & 0x0F0F0F0Fu;
                     code[1] = code[1] >> (4 * (c & 1)) & 0x0F0F0F0Fu;
@@ -400,17 +511,9 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split)
                 const uint2 w = *reinterpret_cast<const uint2 *>(rec + L::key(rr, 8 * c));
                 code[0] = w.x, code[1] = w.y;
             } else {
-                // nibbles 0, 2, 4, 6 and 1, 3, 5, 7 to bytes, then in order
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + L::key(rr, 8 * c));
-                const uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
-                code[0] = __byte_perm(lo, hi, 0x5140);
-                code[1] = __byte_perm(lo, hi, 0x7362);
+                key_codes(*reinterpret_cast<const uint32_t *>(rec + L::key(rr, 8 * c)), code);
             }
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(byte_less(code[i / 4], i % 4, z), s);
-            packed = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
-                                bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+            packed = row_values(code[0], code[1], twice(less_of(m)), twice(scale_of(m)));
         }
         *reinterpret_cast<uint4 *>(dst + (i0 + r) * stride) = packed;
     }
@@ -451,7 +554,10 @@ cudaError_t append_dim(const KvPool &pool, int format, const Heads &k, const Hea
 template <int D>
 cudaError_t read_dim(const KvPool &pool, int format, const Heads &k, const Heads &v,
                      const TokenList &list, int num_sms, cudaStream_t stream) {
-    const int tiles = tiles_of(list.run), split = split_of(pool, format, D, list, tiles, num_sms);
+    const int tiles = tiles_of(list.run);
+    const int split = format != W4_KV_BF16 && list.run >= kRecTokens
+                          ? 1
+                          : split_of(pool, format, D, list, tiles, num_sms);
     const auto kernel = format == W4_KV_BF16   ? read_kernel<W4_KV_BF16, D>
                         : format == W4_KV_INT8 ? read_kernel<W4_KV_INT8, D>
                                                : read_kernel<W4_KV_INT4, D>;
