@@ -8,12 +8,20 @@
 // bit.
 //
 // A tile is up to 16 listed tokens, cut so that the tokens of a sequence in
-// order fall into whole records.  A warp takes the keys, or the values, of a
-// tile and head; all its loads are under way together.  A whole record's
-// quantised values are put together (or taken apart) in shared memory and
-// moved with 16-byte accesses: their layout scatters a token over 64 sectors.
-// Tiles that are no whole record (decode steps, the ends of a prompt, tokens
-// in another order) go byte by byte.
+// order fall into whole records.  A warp (or four) takes the keys, or the
+// values, of a tile and head; all its loads are under way together.  The layout
+// of quantised values scatters a token over 64 sectors, so those of a whole
+// record are turned, by ldmatrix (by stmatrix on the way back), and moved with
+// 16-byte accesses: byte by byte 16384 tokens of 28 + 4 heads of 128 in 4 bits
+// took 95 us to write and read back, turned they take 64 (5.15 TB/s: 76 % of a
+// copy's rate).  Tiles that are no whole record (decode steps, the ends of a
+// prompt, tokens in another order) go byte by byte.
+//
+// What bounds it: one token of each of 64 sequences 6.0 us, two launches and a
+// chain of four dependent trips to memory (position, page, row, record); 4096
+// tokens in 8 bits 23.7 us, of which the instructions of the quantisation take
+// about half; from 16 k tokens on the traffic of the queries, which pass
+// through (58 % issue slots, 54 % of the DRAM's cycles in the writing kernel).
 #include "w4_kv.cuh"
 
 namespace w4 {
@@ -29,7 +37,9 @@ struct Tile16 {
 };
 
 // Fills the tile of this block; returns the list index of its token 0; tokens
-// first .. first + count - 1 are there (count <= 0: none).  whole: the tokens are one record.  All threads call.
+// first .. first + count - 1 are there (count <= 0: none).  whole (if ASK): the
+// tokens are one record.  All threads call.
+template <bool ASK>
 __device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &list, int tile_no,
                                          int tiles, int rotation_rows, int record_bytes,
                                          Tile16 *tile, int *first, int *count, bool *whole) {
@@ -53,6 +63,8 @@ __device__ __forceinline__ int load_tile(const KvPool &pool, const TokenList &li
         tile->position[r] = at.position;
     }
     __syncthreads();
+    *whole = false;
+    if (!ASK) return base + i0;
     bool same = true;
     if (r < kRecTokens)
         same = tile->record[r] && tile->record[r] == tile->record[0] && tile->in_record[r] == r;
@@ -142,7 +154,7 @@ __device__ __forceinline__ uint32_t to_nibbles(const int (&n)[8]) {
 
 // The queries of a launch of append_kernel, turned as by w4_rope in blocks of
 // their own (in the rows' loop below every lane would turn its partner too:
-// 16 k tokens of 28 query heads 146 us against 84).
+// 16 k tokens of 28 query heads, written and read back, 148 us against 95).
 struct Queries {
     Heads q, out;
     int heads;
@@ -153,7 +165,9 @@ struct Queries {
 };                             // and the others' traffic overlap
 
 // Keys and values: D / 8 lanes take a row (a head of a token), 8 values a lane.
-template <int FMT, int D, int HEADS>
+// WHOLE: some tiles may be whole records; without that code, which short runs
+// do not need, one token of 64 sequences is written 1.3 us faster.
+template <int FMT, int D, int HEADS, bool WHOLE>
 __global__ void __launch_bounds__(kKvThreads)
 append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation rot, int tiles,
               int split) {
@@ -161,7 +175,6 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
     constexpr int LANES = D / 8, TOKENS = 32 / LANES;
     __shared__ Tile16 tile;
     __shared__ uint4 rows[kKvWarps][kRecTokens * LANES];
-    __shared__ __align__(16) unsigned char staged[kKvWarps][FMT == W4_KV_BF16 ? 16 : L::kPart];
     begin_after_previous();
     const unsigned turn = blockIdx.x / q.period;
     if (blockIdx.x != turn * q.period || turn >= q.rows_blocks) {
@@ -187,10 +200,10 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
     task /= split;
     int first, count;
     bool whole;
-    const int i0 = load_tile(pool, list, tile_no, tiles, rot.table ? rot.rows : 0x7FFFFFFF,
-                             L::kBytes, &tile, &first, &count, &whole);
+    const int i0 = load_tile<WHOLE>(pool, list, tile_no, tiles,
+                                    rot.table ? rot.rows : 0x7FFFFFFF, L::kBytes, &tile, &first,
+                                    &count, &whole);
     if (count <= 0 || task >= 2 * pool.kv_heads) return;
-    whole = whole && split == 1;                              // staged by one warp
     const bool is_v = task & 1;
     const int h = task >> 1;
     const long long head_bytes = (long long)h * pool.page_records * L::kBytes;
@@ -284,9 +297,20 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
             const float s = __half2float(sh);
             int z = 0, n8[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (s > 0.f) codes_of<L::kBits>(x, lo, hi, s, &z, n8);
-            // values: the bytes of a whole record go to shared memory first
-            unsigned char *to = whole ? staged[warp] : rec + L::kPart;
-            if constexpr (FMT == W4_KV_INT8) {
+            if (WHOLE && is_v && whole) {
+                // in 16 bits each, in the place of the row's own values (its
+                // pieces exchanged so that 8 rows lie in different banks)
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    asm("cvt.pack.sat.u16.s32 %0, %1, %2;"
+                        : "=r"(u[i])
+                        : "r"(n8[2 * i + 1]), "r"(n8[2 * i]));
+                    u[i] = __vminu2(u[i], L::kLevels * 0x00010001u);
+                }
+                __syncwarp();
+                rows[warp][32 * x0 + lane - c + (c ^ (n & 7))] = make_uint4(u[0], u[1], u[2], u[3]);
+            } else if constexpr (FMT == W4_KV_INT8) {
                 const uint32_t b0 = to_bytes(n8[0], n8[1], n8[2], n8[3]);
                 const uint32_t b1 = to_bytes(n8[4], n8[5], n8[6], n8[7]);
                 if (valid && !is_v)
@@ -294,7 +318,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                 if (valid && is_v) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        to[L::value(rr, 8 * c + i) - L::kPart] =
+                        rec[L::value(rr, 8 * c + i)] =
                             (unsigned char)((i < 4 ? b0 : b1) >> 8 * (i & 3));
                 }
             } else if (!is_v) {
@@ -315,7 +339,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                 if (valid) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        to[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i) - L::kPart] =
+                        rec[L::value(rr, 8 * (c & ~1) + (odd ? 4 : 0) + i)] =
                             (unsigned char)(bytes >> 8 * i);
                 }
             }
@@ -324,13 +348,44 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
                     (uint32_t)__half_as_ushort(sh) | (uint32_t)z << 16;
         }
     }
-    if (FMT == W4_KV_BF16 || !whole || !is_v) return;
-    __syncwarp();
-    uint4 *out = reinterpret_cast<uint4 *>(
-        tile.record[0] + head_bytes + L::kPart);
+    // a whole record's values: the rows' codes, turned, give every lane those
+    // of one d and tokens 2t, 2t + 1 (and 8 on), which are the bytes of its words
+    if constexpr (WHOLE) {
+        if (!whole || !is_v) return;
+        if (split == 1)
+            __syncwarp();
+        else
+            __syncthreads();                                  // the block has one task
+        const int n = lane & 15;
+        const uint32_t row = (uint32_t)__cvta_generic_to_shared(
+            &rows[split == 1 ? warp : (n / TOKENS) % kKvWarps][n * LANES]);
+        uint4 *out = reinterpret_cast<uint4 *>(tile.record[0] + head_bytes + L::kPart) + lane;
+        constexpr int PIECES = L::kPart / 512;
 #pragma unroll
-    for (int i = 0; i < L::kPart / 512; ++i)
-        out[32 * i + lane] = reinterpret_cast<const uint4 *>(staged[warp])[32 * i + lane];
+        for (int i = 0; i < PIECES; ++i) {
+            if (split != 1 && i % kKvWarps != part) continue;
+            uint32_t w[4];
+            const auto get = [&](int x, uint32_t *m) {        // d of 8 x .. 8 x + 15
+                asm volatile(
+                    "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                    : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
+                    : "r"(row + (((x + (lane >> 4)) ^ (n & 7)) << 4))
+                    : "memory");
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t m[4];
+                if constexpr (FMT == W4_KV_INT4) {
+                    get(8 * i + 2 * j, m);
+                    w[j] = (m[0] | m[1] << 8) | (m[2] | m[3] << 8) << 4;
+                } else if (j % 2 == 0) {
+                    get(4 * i + j, m);
+                    w[j] = m[0] | m[1] << 8, w[j + 1] = m[2] | m[3] << 8;
+                }
+            }
+            out[32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
 }
 
 // Eight values of a row from their codes, (u - z) s each; zm: -(2^23 + z).
@@ -465,8 +520,8 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split)
     task /= split;
     int first, count;
     bool whole;
-    const int i0 = load_tile(pool, list, tile_no, tiles, 0x7FFFFFFF, L::kBytes, &tile, &first, &count,
-                             &whole);
+    const int i0 = load_tile<FMT != W4_KV_BF16>(pool, list, tile_no, tiles, 0x7FFFFFFF, L::kBytes,
+                                                &tile, &first, &count, &whole);
     const bool is_v = task & 1;
     const int h = task >> 1;
     const long long head_bytes = (long long)h * pool.page_records * L::kBytes;
@@ -522,14 +577,16 @@ read_kernel(KvPool pool, Heads k, Heads v, TokenList list, int tiles, int split)
 // Tiles that a run of `run` tokens can touch, wherever in a record it starts.
 int tiles_of(int run) { return (run + 2 * (kRecTokens - 1)) / kRecTokens; }
 
-// Warps that share a tile's keys (values) of a head: one where the blocks fill
-// the GPU (then it can put a whole record together), four where the time is
-// that of one block, and always in bf16, which has nothing to put together.
+// Warps that share a tile's keys (values) of a head: four where the time is that
+// of one block, and always in bf16 (whose 16 bytes a lane have no other work);
+// one where the blocks fill the GPU.  Writing and reading back 4096 tokens of 4
+// heads of 128 in 8 bits (2056 warps of tiles): 23.9 us with four, 24.8 with one;
+// 16384 tokens in 4 bits: 81.8, 64.3; 8192 tokens of 2 heads of 64: 16.9, 13.9.
 int split_of(const KvPool &pool, int format, int head_dim, const TokenList &list, int tiles,
              int num_sms) {
     if (list.run <= 256 / head_dim) return 1;
     const long long warps = (long long)(list.tokens / list.run) * tiles * 2 * pool.kv_heads;
-    return format == W4_KV_BF16 || warps < 32LL * num_sms ? 4 : 1;
+    return format == W4_KV_BF16 || warps < (long long)(head_dim / 8) * num_sms ? 4 : 1;
 }
 unsigned blocks_of(const KvPool &pool, const TokenList &list, int tiles, int split) {
     return (unsigned)(list.tokens / list.run * tiles) *
@@ -544,9 +601,14 @@ cudaError_t append_dim(const KvPool &pool, int format, const Heads &k, const Hea
     q.rows_blocks = blocks_of(pool, list, tiles, split);
     const dim3 grid(q.rows_blocks + (q.all + kKvThreads - 1) / kKvThreads);
     q.period = grid.x / q.rows_blocks;
-    const auto kernel = format == W4_KV_BF16   ? append_kernel<W4_KV_BF16, D, HEADS>
-                        : format == W4_KV_INT8 ? append_kernel<W4_KV_INT8, D, HEADS>
-                                               : append_kernel<W4_KV_INT4, D, HEADS>;
+    const bool whole = list.run >= kRecTokens;
+    const auto kernel =
+        format == W4_KV_BF16 ? append_kernel<W4_KV_BF16, D, HEADS, false>
+        : format == W4_KV_INT8
+            ? whole ? append_kernel<W4_KV_INT8, D, HEADS, true>
+                    : append_kernel<W4_KV_INT8, D, HEADS, false>
+            : whole ? append_kernel<W4_KV_INT4, D, HEADS, true>
+                    : append_kernel<W4_KV_INT4, D, HEADS, false>;
     return launch_overlapped(kernel, grid, dim3(kKvThreads), 0, stream, pool, k, v, q, list, rot,
                              tiles, split);
 }
@@ -555,6 +617,7 @@ template <int D>
 cudaError_t read_dim(const KvPool &pool, int format, const Heads &k, const Heads &v,
                      const TokenList &list, int num_sms, cudaStream_t stream) {
     const int tiles = tiles_of(list.run);
+    // (one warp takes a whole record: 4096 tokens in 8 bits 26.4 us, 28.3 with four)
     const int split = format != W4_KV_BF16 && list.run >= kRecTokens
                           ? 1
                           : split_of(pool, format, D, list, tiles, num_sms);

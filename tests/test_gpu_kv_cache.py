@@ -259,3 +259,33 @@ def test_codes_of_many_values(w4, fmt, layout):
     k, v = cache.read(i32(pos), table)
     assert np.array_equal(bits(k), kv.bf16_bits(kv.held(xr, fmt)))
     assert np.array_equal(bits(v), kv.bf16_bits(kv.held(x, fmt)))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("D,H,T", [(64, 2, 10007), (128, 4, 6003), (128, 1, 700), (64, 1, 333)])
+def test_whole_records_and_others_agree(w4, fmt, D, H, T):
+    """A run from inside a record on, long enough for a warp a record (or
+    shorter, with four): its whole records are turned in shared memory; read
+    back in reverse order, every token goes by itself."""
+    rng = np.random.default_rng(T)
+    first, P = 5, 32
+    k, v = rows(rng, T, H, D), rows(rng, T, H, D)
+    pos = np.arange(first, first + T, dtype=np.int32)
+    pages = -(-(first + T) // P)
+    table = torch.from_numpy(rng.permutation(pages).astype(np.int32)).cuda().view(1, -1)
+    cache = w4.PagedCache.make(pages, kv.FMT[fmt], H, D, P)
+    cache.append(to_gpu(k), to_gpu(v), i32(pos), table)
+    forward = cache.read(i32(pos), table)
+    backward = cache.read(i32(pos[::-1].copy()), table)
+    cache.check()
+    for x, got, turned in zip((k, v), forward, backward):
+        want = kv.bf16_bits(kv.held(x, fmt))
+        assert np.array_equal(bits(got), want)
+        assert np.array_equal(bits(turned), want[::-1])
+    # written in reverse, byte by byte: the same records
+    again = w4.PagedCache.make(pages, kv.FMT[fmt], H, D, P)
+    again.pool.zero_(), cache.pool.zero_()
+    cache.append(to_gpu(k), to_gpu(v), i32(pos), table)
+    back = pos[::-1].copy()
+    again.append(to_gpu(k[::-1].copy()), to_gpu(v[::-1].copy()), i32(back), table)
+    assert torch.equal(again.pool, cache.pool)
