@@ -19,9 +19,10 @@
 //
 // What bounds it: one token of each of 64 sequences 6.0 us, two launches and a
 // chain of four dependent trips to memory (position, page, row, record); 4096
-// tokens in 8 bits 23.7 us, of which the instructions of the quantisation take
-// about half; from 16 k tokens on the traffic of the queries, which pass
-// through (58 % issue slots, 54 % of the DRAM's cycles in the writing kernel).
+// tokens in 8 bits 23.7 us, most of it the instructions of the quantisation and
+// the launches (its bytes take 12.7); from 16 k tokens on the traffic of the
+// queries, which pass through (the writing kernel: 58 % of the issue slots, 54 %
+// of the DRAM's).
 #include "w4_kv.cuh"
 
 namespace w4 {

@@ -40,6 +40,14 @@
 // block, two warps issue the copies, a record a bulk copy, running ahead over
 // the block's whole stretch; the others form KG groups of QG: a group takes
 // every KG-th record through its own ring, and its QG warps hold 8 NT rows each.
+//
+// Measured (28 query and 4 key/value heads of 128, one new token, captured calls;
+// a copy reaches 6788 GB/s).  bf16, bound by HBM: 32 x 16384 tokens 160 us =
+// 6690 GB/s; one sequence of 65536, 108 records a block, 29.8 us = 4500 GB/s,
+// 9 us of it around the records.  8 bits: 64 ragged sequences of up to 8192
+// 49.4 us = 5620 GB/s.  4 bits, bound by the instructions of conversion and
+// softmax (58 % of the issue slots, ALU 46 %, tensor pipe 23 %): 4 x 131072
+// 60.3 us = 4730 GB/s.
 #include <atomic>
 
 #include "w4_device.cuh"
@@ -719,7 +727,8 @@ __device__ __forceinline__ void warps_sync() {
 
 // Joins the pieces of the heads that blocks start and others go on with: block
 // (c, y) rows ROWS y .. of block c's head, in the pieces' order.  256 / ROWS
-// threads a row: groups of D / 4 take every other (or fourth) piece of it.
+// threads a row: groups of D / 4 take every other (or fourth) piece of it.  Bound
+// by two trips to L2, about 2 us after the pieces are there.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int block_rows) {
     constexpr int UNITS = D / 4, GROUPS = 256 / ROWS / UNITS;
