@@ -328,3 +328,28 @@ def test_refusals(w4):
     odd = torch.zeros(2 * 4 * 64 + 4, device="cuda", dtype=torch.bfloat16)[4:].view(2, 4, 64)
     assert status(q=odd) == w4.Status.INVALID_ARG
     assert status(out=odd) == w4.Status.INVALID_ARG
+
+
+@pytest.mark.parametrize("fmt", list(kv.FMT))
+@pytest.mark.parametrize("power", [-60, 60])
+def test_queries_of_any_size(w4, fmt, power):
+    """Queries times a power of two with the scale divided by it: the same
+    bits (every step scales exactly)."""
+    s = Setup(w4, fmt, 64, 2, 7, 16, 2, [70, 33], seed=11)
+    want, want_lse = run_both(w4, s)
+    got, lse = s.cache.attend(s.gq * 2.0 ** power, s.glens, s.table, scale=64 ** -0.5 * 2.0 ** -power)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("fmt", list(kv.FMT))
+def test_keys_of_zero(w4, fmt):
+    """All scores are 0 whatever the queries are: the mean of the values."""
+    s = Setup(w4, fmt, 128, 1, 4, 16, 1, [50], seed=12, spread=0.0)
+    s.q = kv.bf16(np.full_like(s.q, 1e35))
+    s.gq = to_gpu(s.q)
+    got, lse = s.cache.attend(s.gq, s.glens, s.table)
+    s.check(got, lse)
+    want = s.values[0].astype(np.float64).mean(0)              # [1, 128]
+    u = 2.0 ** -8
+    assert (np.abs(got[0].double().cpu().numpy() - want)
+            <= 2 * u * np.abs(s.values[0]).mean(0)).all()
