@@ -472,10 +472,12 @@ def _int32(t, n: int, what: str) -> int | None:
 
 
 def _block_table(t) -> bytes:
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.stride(1) != 1 or not t.is_cuda:
-        raise ValueError("block table: expected a CUDA int32 tensor [seqs, pages]")
-    seqs, width = t.shape
-    return _pack_table(t.data_ptr(), seqs, width, max(t.stride(0), width))
+    if t.dtype is torch.int32 and t.dim() == 2 and t.is_cuda:
+        seqs, width = t.shape
+        row, column = t.stride()
+        if column == 1:
+            return _pack_table(t.data_ptr(), seqs, width, row if row > width else width)
+    raise ValueError("block table: expected a CUDA int32 tensor [seqs, pages]")
 
 
 def _raw_stream(stream, like) -> int:
@@ -519,25 +521,29 @@ def kv_pool_bytes(fmt: int, kv_heads: int, head_dim: int, page_tokens: int, page
 def kv_append(cache: "PagedCache", k, v, positions, table, seq_ids=None, q=None, q_out=None,
               rotation: "RopeTable | None" = None, stream=None) -> None:
     """w4_kv_append: write tokens into the cache, rotating k and q (into q_out)."""
-    T = k.shape[0]
-    shape = (T, cache.kv_heads, cache.head_dim)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError(f"k, v: expected {shape}")
-    if q is not None and (q.shape[0] != T or q.shape[2] != cache.head_dim or q_out is None
-                          or q_out.shape != q.shape):
-        raise ValueError("q, q_out: expected [tokens, q_heads, head_dim]")
-    _ok(_kv_append(cache.ref, _heads(k), _heads(v), _heads(q), _heads(q_out),
-                   0 if q is None else q.shape[1], T, _int32(positions, T, "positions"),
-                   _int32(seq_ids, T, "seq_ids"), _block_table(table),
-                   rotation and rotation.packed, _raw_stream(stream, k)), "w4_kv_append")
+    shape = k.shape
+    if v.shape != shape or shape[1:] != cache.head_shape:
+        raise ValueError(f"k, v: expected [tokens, {cache.kv_heads}, {cache.head_dim}]")
+    T, q_heads = shape[0], 0
+    if q is not None:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != cache.head_dim or \
+                q_out is None or q_out.shape != q_shape:
+            raise ValueError("q, q_out: expected [tokens, q_heads, head_dim]")
+        q_heads = q_shape[1]
+    _ok(_kv_append(cache.ref, _heads(k), _heads(v), _heads(q), _heads(q_out), q_heads, T,
+                   _int32(positions, T, "positions"), _int32(seq_ids, T, "seq_ids"),
+                   _block_table(table), rotation and rotation.packed, _raw_stream(stream, k)),
+        "w4_kv_append")
 
 
 def kv_read(cache: "PagedCache", k_out, v_out, positions, table, seq_ids=None,
             stream=None) -> None:
     """w4_kv_read: the cached keys and values of the listed tokens, bfloat16."""
     T = positions.numel()
+    shape = (T, *cache.head_shape)
     for x in (k_out, v_out):
-        if x is not None and x.shape != (T, cache.kv_heads, cache.head_dim):
+        if x is not None and x.shape != shape:
             raise ValueError("k_out, v_out: expected [tokens, kv_heads, head_dim]")
     _ok(_kv_read(cache.ref, _heads(k_out), _heads(v_out), T,
                  _int32(positions, T, "positions"), _int32(seq_ids, T, "seq_ids"),
@@ -552,9 +558,10 @@ def paged_attn_workspace_bytes(cache: "PagedCache") -> int:
 
 
 def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, workspace, stream):
-    T, H, D = q.shape
+    shape = q.shape
+    T, H, D = shape
     B = table.shape[0]
-    if T % B or D != cache.head_dim or out.shape != q.shape:
+    if not B or T % B or D != cache.head_dim or out.shape != shape:
         raise ValueError("q, out: expected [seqs * tokens, q_heads, head_dim]")
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.numel() != T * H:
@@ -624,6 +631,7 @@ class PagedCache:
             raise ValueError(f"pool: expected a multiple of {per_page} bytes")
         self.pool, self.format = pool, fmt
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
+        self.head_shape = (kv_heads, head_dim)
         self.pages = nbytes // per_page
         self.error = torch.zeros(1, dtype=torch.int32, device=pool.device) if error is None \
             else error
