@@ -34,12 +34,12 @@
 // short heads came last, and 64 ragged sequences of up to 8192 tokens in 8 bits
 // took 64 us instead of 50.  A cut that would leave only a few records of a head
 // on one side moves to the head's border.
-// The pieces of cut heads are joined by a second kernel that is already
-// resident when the first one ends, a few rows a block: left to the block that
-// finished a head last, the joining of 5 pieces of 56 rows took 7 us.  In a
-// block, two warps issue the copies, a record a bulk copy, running ahead over
-// the block's whole stretch; the others form KG groups of QG: a group takes
-// every KG-th record through its own ring, and its QG warps hold 8 NT rows each.
+// The pieces of cut heads are joined by a second kernel, a few rows a block,
+// whose launch overlaps the first one's end: left to the block that finished a
+// head last, the joining of 5 pieces of 56 rows took 7 us.  In a block, two
+// warps issue the copies, a record a bulk copy, running ahead over the block's
+// whole stretch; the others form KG groups of QG: a group takes every KG-th
+// record through its own ring, and its QG warps hold 8 NT rows each.
 //
 // Measured (28 query and 4 key/value heads of 128, one new token, captured calls;
 // a copy reaches 6788 GB/s).  bf16, bound by HBM: 32 x 16384 tokens 160 us =
