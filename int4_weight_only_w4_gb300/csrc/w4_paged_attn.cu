@@ -27,6 +27,12 @@
 // probability, p s_v = exp2(y + log2 s_v - m), m taken over that sum, so that p
 // fits binary16 whatever the scales are.
 //
+// Roundings.  Scores, m, l and O are fp32; p is rounded to 16 bits because the
+// second product takes it so, to binary16 (11 bits) beside codes, to bfloat16 (8
+// bits) beside bfloat16 values, whose range binary16 does not have: the result
+// is then within 0.0023 of the fp64 one instead of 0.0017 (its own rounding to
+// bfloat16).  l sums p before that rounding.
+//
 // Schedule.  The blocks, one per SM, divide the list (sequence, head, record)
 // evenly among themselves, from the lengths on the device: block c takes the
 // records from cut c to cut c + 1.  A head counts for some records more than it
