@@ -13,7 +13,7 @@
 // of quantised values scatters a token over 64 sectors, so those of a whole
 // record are turned, by ldmatrix (by stmatrix on the way back), and moved with
 // 16-byte accesses: byte by byte 16384 tokens of 28 + 4 heads of 128 in 4 bits
-// took 95 us to write and read back, turned they take 64 (5.15 TB/s: 76 % of a
+// took 95 us to write and read back, turned they take 62 (5.28 TB/s: 78 % of a
 // copy's rate).  Tiles that are no whole record (decode steps, the ends of a
 // prompt, tokens in another order) go byte by byte.
 //
@@ -167,9 +167,14 @@ struct Queries {
 
 // Keys and values: D / 8 lanes take a row (a head of a token), 8 values a lane.
 // WHOLE: some tiles may be whole records; without that code, which short runs
-// do not need, one token of 64 sequences is written 1.3 us faster.
+// do not need, one token of 64 sequences is written 1.3 us faster.  Eight blocks
+// an SM (64 registers) where queries go by four heads of 128: 16384 tokens in 4
+// bits, written and read back, 62.1 us instead of 63.8; with heads of 64 it costs
+// (8192 tokens 14.4 instead of 13.8).  0: no such bound; with 1 the compiler
+// takes 61 registers instead of 48 for short runs, and they 7.1 us instead of 6.0.
 template <int FMT, int D, int HEADS, bool WHOLE>
-__global__ void __launch_bounds__(kKvThreads)
+__global__ void
+__launch_bounds__(kKvThreads, FMT != W4_KV_BF16 && D == 128 && HEADS == 4 ? 8 : 0)
 append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation rot, int tiles,
               int split) {
     using L = KvLayout<FMT, D>;
