@@ -21,7 +21,7 @@
 // chain of four dependent trips to memory (position, page, row, record); 4096
 // tokens in 8 bits 23.7 us, most of it the instructions of the quantisation and
 // the launches (its bytes take 12.7); from 16 k tokens on the traffic of the
-// queries, which pass through (the writing kernel: 58 % of the issue slots, 54 %
+// queries, which pass through (the writing kernel: 62 % of the issue slots, 57 %
 // of the DRAM's).
 #include "w4_kv.cuh"
 
