@@ -5,11 +5,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "w4_attn_plan.cuh"
 #include "w4_internal.cuh"
 
 namespace w4 {
-
-constexpr int kRecTokens = 16;    // tokens of a record = keys of one tensor-core tile
 
 // Byte offsets inside a record of format FMT (W4_KV_*) and head dimension D.
 template <int FMT, int D>

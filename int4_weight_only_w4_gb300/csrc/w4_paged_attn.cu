@@ -56,22 +56,14 @@
 // 60.3 us = 4730 GB/s.
 #include <atomic>
 
+#include "w4_attn_plan.cuh"
 #include "w4_device.cuh"
 #include "w4_kv.cuh"
 
 namespace w4 {
 namespace {
 
-constexpr int kRowsMax = 64;           // rows of a block
-// What a head's start and end cost, in records of one tile of rows.  Ragged
-// batches: 64 x 8k int8 64 us at 0, 50.8 at 28, 49.7 at 40, 50.5 at 56; 8 new
-// tokens over 8 x 8k bf16 44.1, 33.8, 30.4, 30.7; 64 x 8k int4 57.6, 43.6, 41.4,
-// 40.2; even ones lose a little (8 x 2k bf16 12.0, 13.5, 12.6, 12.7).
-constexpr int kHeadRecords = 40;
-constexpr int kMaxStages = 16;         // of one group's ring
-constexpr int kMaxGrid = 256;
 constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not there: past any length
-constexpr int kSharedBytes = 224256;   // rings and join: 219 of the 227 KB of a block
 constexpr float kCodeUnit = 0x1p-24f;  // what the bits of a code are in binary16
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen no key
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -133,24 +125,14 @@ __device__ __forceinline__ int token_of_row(const AttnArgs &a, int row) {
     return a.group == 1 ? row : (int)__umulhi((unsigned)row, a.group_magic);
 }
 
-struct Seq {
-    int len;           // visible tokens
-    int first;         // first record with a visible key
-    int records;       // records from there on (0: none)
-};
-
 __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
-    Seq s;
-    s.len = max(a.lens[b], 0);
+    int len = max(a.lens[b], 0);
     const int room = a.pool.width * a.pool.page_tokens;
-    if (s.len > room) {
+    if (len > room) {
         if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_LENGTH);
-        s.len = room;
+        len = room;
     }
-    const long long lo = (long long)s.len - a.tokens + 1 - a.window;
-    s.first = a.window > 0 && lo > 0 ? (int)(lo / kRecTokens) : 0;
-    s.records = (s.len + kRecTokens - 1) / kRecTokens - s.first;
-    return s;
+    return seen_records(len, a.tokens, a.window);
 }
 
 // A warp's NT tiles of 8 rows: its share of Q, and the running m, l, O.
@@ -627,40 +609,23 @@ __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) 
     o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
 }
 
-// How a launch divides a block (host).
-struct Plan {
-    int row_tiles;     // blocks of rows per key/value head
-    int QG, KG;        // warps on a record, groups of them
-    int stages;        // records of a group's ring
-    int ring_bytes;    // of all rings
-    int extra;         // see List
-};
-
-// A place in the list of records (the host refuses lists of 2^31).
-struct Cut {
-    int b, item, u;        // sequence, head (x row tile) of it, record of that
-};
-
 // The list, as a warp sees it: lane i holds sequences [b0, b1), whose items
 // cost [before, before + mine) * per_seq.
-struct List {
-    int b0, b1, before, mine, per_seq, work;
-    int extra;             // what a head costs beside its records
-    int blocks, least;     // blocks that have a stretch, records that are not cut off
-    int q, rest;           // work / blocks and its remainder
-    unsigned magic;        // 2^32 / blocks, rounded up
+struct List : Division {
+    int b0, b1, before, mine;
 
-    __device__ __forceinline__ int cost(const AttnArgs &a, int b) const {
-        return sequence(a, b).records + extra;
+    __device__ __forceinline__ int records(const AttnArgs &a, int b) const {
+        return sequence(a, b).records;
     }
 
-    __device__ __forceinline__ List(const AttnArgs &a, const Plan &plan) : extra(plan.extra) {
+    __device__ __forceinline__ List(const AttnArgs &a, const Plan &plan) {
         const int lane = threadIdx.x & 31, each = (a.pool.seqs + 31) >> 5;
+        extra = plan.extra;
         per_seq = a.pool.kv_heads * plan.row_tiles;
         b0 = min(lane * each, a.pool.seqs), b1 = min(b0 + each, a.pool.seqs);
         mine = 0;
 #pragma unroll 4
-        for (int b = b0; b < b1; ++b) mine += cost(a, b);
+        for (int b = b0; b < b1; ++b) mine += records(a, b) + extra;
         int upto = mine;
         if (a.pool.seqs > 1) {
 #pragma unroll
@@ -670,58 +635,31 @@ struct List {
             }
         }
         before = upto - mine;
-        work = __shfl_sync(0xFFFFFFFFu, upto, a.pool.seqs > 1 ? 31 : 0) * per_seq;
-        // as many blocks as heads, or that many times the parts of at least 4
-        // records a group that the mean head has (so heads of one length are
-        // cut alike), while there are blocks
-        const int heads = a.pool.seqs * per_seq;
-        blocks = min((int)gridDim.x, heads * max(1, (work / heads - extra) / (4 * plan.KG)));
-        q = work / blocks, rest = work - q * blocks;
-        magic = 0xFFFFFFFFu / (unsigned)blocks + 1;
-        least = max(plan.KG, extra / 2);
+        const int all = __shfl_sync(0xFFFFFFFFu, upto, a.pool.seqs > 1 ? 31 : 0) * per_seq;
+        divide(plan, a.pool.seqs, all, gridDim.x);
     }
 
-    // Start of block c's stretch.  rest * c < 2^16, so the product with magic
-    // gives rest * c / blocks exactly (blocks = 1: rest is 0).
-    __device__ __forceinline__ int start(int c) const {
-        return q * c + (int)__umulhi((unsigned)(rest * c), magic);
-    }
-
-    // The record at cost u of the list, moved to its head's border where fewer
-    // than `least` records would be cut off.
+    // The cut at cost u of the list.
     __device__ __forceinline__ Cut cut(const AttnArgs &a, int u) const {
         const bool here = u >= before * per_seq && u < (before + mine) * per_seq;
-        int b = b0, n = mine, in = u - before * per_seq;
+        int b = b0, n = mine - extra, in = u - before * per_seq;
         if (a.pool.seqs > 1) {
             if (here)
                 for (;; ++b) {
-                    n = cost(a, b);
-                    if (in < n * per_seq) break;
-                    in -= n * per_seq;
+                    n = records(a, b);
+                    if (in < (n + extra) * per_seq) break;
+                    in -= (n + extra) * per_seq;
                 }
         }
         const unsigned found = __ballot_sync(0xFFFFFFFFu, here);
         const int src = found ? __ffs(found) - 1 : 0;
-        Cut c;
-        c.b = __shfl_sync(0xFFFFFFFFu, b, src);
+        b = __shfl_sync(0xFFFFFFFFu, b, src);
         n = __shfl_sync(0xFFFFFFFFu, n, src);
         in = __shfl_sync(0xFFFFFFFFu, in, src);
-        c.item = found ? in / n : 0;
-        c.u = found ? in - c.item * n - extra : 0;
-        if (!found) c.b = a.pool.seqs;                        // the list's end
-        if (found && (c.u < least || n - extra - c.u < least)) {
-            if (2 * (c.u + extra) > n && ++c.item == per_seq) c.item = 0, ++c.b;
-            c.u = 0;
-        }
-        return c;
-    }
-
-    // First block c with start(c) >= u (u > 0).
-    __device__ __forceinline__ int block_from(int u) const {
-        int c = min((int)((float)u * ((float)blocks / (float)work)), blocks);
-        while (c > 0 && start(c) >= u) --c;
-        while (start(c) < u) ++c;
-        return c;
+        if (found) return cut_inside(b, in, n);
+        Cut end;                                              // of the list
+        end.b = a.pool.seqs, end.item = 0, end.u = 0;
+        return end;
     }
 };
 
@@ -795,14 +733,6 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int block_r
     if (there) store_row(a, head.x, head.y, head.z + row, d, o, m, l);
 }
 
-// Warps that compute; with the two that copy 20 of 96 registers, 16 of 128 or 12
-// of 168, by the values that a warp holds.
-constexpr int kCopyWarps = 2;
-template <int D, int NT>
-__host__ __device__ constexpr int compute_warps() {
-    return D * NT == 64 ? 18 : D * NT == 128 ? 14 : 10;
-}
-
 // A stretch's part of one head, as the copying warp tells the others.
 struct Piece {
     int b;             // sequence; -1: no more pieces
@@ -825,7 +755,6 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     const int lane = threadIdx.x & 31, KG = plan.KG, stages = plan.stages;
     const int copier = (threadIdx.x >> 5) - WARPS, kg = kCopyWarps * lane + copier;
     const List list(a, plan);
-    const int per_seq = list.per_seq;
     Cut c, to;
     c.b = 0, c.item = 0, c.u = 0;
     to = c;
@@ -839,7 +768,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     uint64_t *my_full = full + kg * stages, *my_empty = empty + kg * stages;
     unsigned char *ring = smem + kg * stages * L::kBytes;
     while (true) {
-        const bool more = c.b < to.b || c.item < to.item || c.u < to.u;
+        const bool more = has_more(c, to, a.pool.seqs);
         const Seq seq = sequence(a, more ? c.b : 0);
         const bool last = c.b == to.b && c.item == to.item;
         const int stop = last ? to.u : seq.records;
@@ -871,16 +800,14 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
             p.whole = c.u == 0 && stop == seq.records, p.starts = c.u == 0;
         }
         if (copier == 0 && more && c.u == 0 && stop != seq.records) {
-            // the cuts inside this head, at least `least` records from its borders
             const bool mine = c.b >= list.b0 && c.b < list.b1;
-            const int n = seq.records + list.extra;
-            int head = list.before * per_seq + c.item * n;
+            int head = list.before * list.per_seq + c.item * (seq.records + list.extra);
             if (mine)
-                for (int x = list.b0; x < c.b; ++x) head += list.cost(a, x) * per_seq;
+                for (int x = list.b0; x < c.b; ++x)
+                    head += (list.records(a, x) + list.extra) * list.per_seq;
             head = __shfl_sync(0xFFFFFFFFu, head, __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1);
-            const int c_lo = list.block_from(head + list.extra + list.least);
-            const int c_hi = list.block_from(head + n - list.least + 1) - 1;
-            if (tells) p.pieces = c_hi - c_lo + 2;
+            const int pieces = list.pieces(head, seq.records);
+            if (tells) p.pieces = pieces;
         }
         if (tells) mbar_arrive(&piece_full[slot]);
         ++told;
@@ -922,8 +849,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
         if (last) {
             c = to;
         } else {
-            c.u = 0;
-            if (++c.item == per_seq) c.item = 0, ++c.b;
+            list.advance(c);
         }
     }
     // nothing of the block's own is under way when it ends
@@ -935,11 +861,11 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(32 * (compute_warps<D, NT>() + kCopyWarps), 1)
+__global__ void __launch_bounds__(32 * (compute_warps(D, NT) + kCopyWarps), 1)
 attn_kernel(const AttnArgs a, const Plan plan) {
     extern __shared__ __align__(128) unsigned char smem[];
     using L = KvLayout<FMT, D>;
-    constexpr int WARPS = compute_warps<D, NT>();
+    constexpr int WARPS = compute_warps(D, NT);
     constexpr int OROW = D + 4;                               // floats; + 4: no bank conflicts
     __shared__ uint64_t full[WARPS * kMaxStages], empty[WARPS * kMaxStages];
     __shared__ uint64_t piece_full[2], piece_empty[2];
@@ -1060,7 +986,7 @@ attn_kernel(const AttnArgs a, const Plan plan) {
 
 template <int FMT, int D, int NT>
 cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    constexpr int bytes = KvLayout<FMT, D>::kBytes, WARPS = compute_warps<D, NT>();
+    constexpr int bytes = KvLayout<FMT, D>::kBytes, WARPS = compute_warps(D, NT);
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1071,27 +997,16 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
     }
-    const int tiles = (a.tokens * a.group + 8 * NT - 1) / (8 * NT), most = kRowsMax / (8 * NT);
-    Plan p;
-    p.row_tiles = (tiles + most - 1) / most;
-    p.QG = (tiles + p.row_tiles - 1) / p.row_tiles;
-    // groups: as many as the warps allow with three records in a ring
-    const int join_row = 8 * NT * p.QG * (D + 4) * 4;
-    p.KG = WARPS / p.QG;
-    while (p.KG > 1 && p.KG * (join_row + 3 * bytes) > kSharedBytes) --p.KG;
-    p.stages = (kSharedBytes - p.KG * join_row) / (p.KG * bytes);
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
-    p.ring_bytes = p.KG * p.stages * bytes;
-    p.extra = kHeadRecords / ((p.QG * NT + 1) / 2);
+    const int rows = a.tokens * a.group;
+    const Plan p = plan_of(D, NT, rows, bytes);
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
     e = launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
                           kSharedBytes, stream, a, p);
     if (e != cudaSuccess) return e;
-    // one sequence that is too short for a second part of a head: nothing to join
-    const long long longest = (long long)a.pool.width * a.pool.page_records;
-    if (a.pool.seqs == 1 && longest < 8 * p.KG && a.pool.kv_heads * p.row_tiles <= grid)
+    if (nothing_to_join(p, a.pool.seqs, a.pool.kv_heads,
+                        (long long)a.pool.width * a.pool.page_records, grid))
         return cudaSuccess;
-    const int block_rows = 8 * NT * p.QG, rows = a.tokens * a.group;
+    const int block_rows = 8 * NT * p.QG;
     constexpr int FEW = 2, MANY = 512 / D;                    // rows of a joining block
     if (rows <= 8)
         return launch_overlapped(join_kernel<D, FEW>, dim3(grid, (rows + FEW - 1) / FEW), dim3(256),
@@ -1101,18 +1016,10 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
                              dim3(256), 0, stream, a, block_rows);
 }
 
-// Two tiles a warp where that makes a third as many groups again: the operands
-// of a record serve both tiles, but fewer warps are there to wait.  Measured at
-// 48 x 4 k tokens of 64 bf16 values: 3 tiles 26.7 us with one, 27.9 with two;
-// 4 tiles 32.6, 28.3; 5 tiles 39.5, 34.8; 7 tiles 50.7, 42.9; at 8 x 8 k of 128:
-// 2 tiles 31.5, 33.2; 3 tiles 34.5, 37.1; 5 tiles 43.9, 41.7; 6 tiles 48.1, 43.2;
-// 7 tiles 50.0, 54.2.
 template <int FMT, int D>
 cudaError_t launch_rows(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    const int tiles = (a.tokens * a.group < kRowsMax ? a.tokens * a.group + 7 : kRowsMax) / 8;
-    const int one = compute_warps<D, 1>() / tiles, two = compute_warps<D, 2>() / ((tiles + 1) / 2);
-    return tiles > 2 && 3 * two >= 4 * one ? launch<FMT, D, 2>(a, num_sms, stream)
-                                           : launch<FMT, D, 1>(a, num_sms, stream);
+    return tiles_a_warp(D, a.tokens * a.group) == 2 ? launch<FMT, D, 2>(a, num_sms, stream)
+                                                    : launch<FMT, D, 1>(a, num_sms, stream);
 }
 
 }  // namespace
