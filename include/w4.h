@@ -637,7 +637,7 @@ w4_status w4_paged_attn_workspace_bytes(const w4_kv_cache *cache, size_t *bytes)
  *   tokens : 1..8;  q_heads : a multiple of kv_heads, at most 4096 times it
  *   lens   : device int32 [table->seqs]; negative counts as 0
  *   scale  : finite; usually head_dim^-0.5
- *   window : 0 for none
+ *   window : >= 0; 0, or as many as the table has room for, leave nothing out
  *   workspace : device, 256-byte aligned; calls that overlap on the device must
  *            not share one; what it holds between calls does not matter
  * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, or a table

@@ -140,7 +140,9 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     a.group_magic = a.group > 1 ? 0xFFFFFFFFu / (unsigned)a.group + 1 : 0;
     a.tokens = tokens;
     a.scale = scale;
-    a.window = window;
+    // a window as wide as the longest sequence leaves nothing out (and so the
+    // kernels may subtract one from a position of a token that is not there)
+    a.window = window < table->width * cache->page_tokens ? window : 0;
     a.workspace = workspace;
     return cuda_status(w4::launch_paged_attn(a, cache->format, cache->head_dim, sms,
                                              reinterpret_cast<cudaStream_t>(stream)));
