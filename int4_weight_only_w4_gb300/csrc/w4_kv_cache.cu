@@ -95,6 +95,12 @@ __device__ __forceinline__ Two twice(float v) {
     return r;
 }
 
+// The largest of three; NaN if any is (fmaxf would drop it).
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ int rint_quotient(float w, float s) {
     const float q = rintf(__fdiv_rn(w, s));
     return q == q ? (int)fminf(fmaxf(q, -512.f), 512.f) : 0;
@@ -105,7 +111,8 @@ __device__ __forceinline__ int rint_quotient(float w, float s) {
 // ulp of 1 / s, t = w r is within 2^-22.4 of the quotient's magnitude; adding and
 // subtracting 1.5 * 2^23 rounds t to the nearest integer (ties to even), and
 // where t is further than T * 2^-21 (T >= every |t| of the row) from a half,
-// that integer is the rule's.  In the rare other case the division decides.
+// that integer is the rule's.  In the rare other case, and where a value is NaN
+// (its distance is, too), the division decides; NaN gets the code of 0.
 template <int BITS>
 __device__ __forceinline__ void codes_of(const float (&w)[8], float lo, float hi, float s,
                                          int *zero, int (&n)[8]) {
@@ -125,7 +132,7 @@ __device__ __forceinline__ void codes_of(const float (&w)[8], float lo, float hi
         x.f = make_float2(w[i], w[i + 1]);
         const Two q = mul2(x, rr), y = add2(q, up);
         const Two d = add2(mul2(add2(y, down), minus), q);    // exact
-        far = fmaxf(far, fmaxf(fabsf(d.f.x), fabsf(d.f.y)));
+        far = max3_nan(far, fabsf(d.f.x), fabsf(d.f.y));
         n[i] = y.i.x + shift, n[i + 1] = y.i.y + shift;
     }
     if (!(0.5f - far > tol)) {

@@ -22,3 +22,40 @@ def test_windows_wider_than_any_length(w4, fmt, window):  # noqa: F811
         want, want_lse = run_both(w4, s)
         got, lse = run_both(w4, s, window=window)
         assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("layout", [None, 0, 1])
+@pytest.mark.parametrize("D,first,T", [(128, 0, 32), (64, 0, 48), (128, 3, 9), (64, 15, 2),
+                                       (128, 0, 4096)])
+def test_nan_is_held_as_zero(w4, fmt, layout, D, first, T):  # noqa: F811
+    """NaN beside values of both signs, of one sign, beside infinities and in
+    every place of a row, in whole records and in parts of them: held as 0, the
+    rest of the row as if it were not there."""
+    rng = np.random.default_rng(D + T)
+    H = 2
+    k, v = rows(rng, T, H, D), rows(rng, T, H, D)
+    for x in (k, v):
+        for t in range(T):
+            x[t, t % H, rng.integers(0, D, 1 + t % 3)] = np.nan
+        x[0, 1, :4] = [np.nan, 2.0, np.nan, -1.0]
+        if T > 4:
+            x[2], x[3] = np.abs(x[2]), -np.abs(x[3])
+            x[4, 0, 5:7] = [np.inf, np.nan]
+    pos = np.arange(first, first + T, dtype=np.int32)
+    rope, kr = None, k
+    if layout is not None:
+        tab = rng.uniform(0.1, 1, (first + T, D // 2, 2)).astype(np.float32)
+        rope = w4.RopeTable(torch.from_numpy(tab).cuda(), layout)
+        with np.errstate(invalid="ignore"):
+            kr = kv.rotate(k, pos, tab, layout)
+    cache = w4.PagedCache.make((first + T) // 16 + 1, kv.FMT[fmt], H, D)
+    table = torch.arange((first + T) // 16 + 1, dtype=torch.int32, device="cuda").view(1, -1)
+    cache.append(to_gpu(k), to_gpu(v), i32(pos), table, rope=rope)
+    got = cache.read(i32(pos), table)
+    cache.check()
+    for x, g in zip((kr, v), got):
+        # 0 widens no row's range; an infinite value is held as Q times the
+        # largest scale, which is the code of any value that large
+        x = np.nan_to_num(np.asarray(x, np.float32), nan=0.0, posinf=3e38, neginf=-3e38)
+        assert np.array_equal(bits(g), kv.bf16_bits(kv.held(x, fmt)))
