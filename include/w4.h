@@ -576,14 +576,14 @@ typedef struct w4_block_table {
 w4_status w4_kv_pool_bytes(const w4_kv_cache *cache, size_t *bytes);
 
 /*
- * Writes new tokens into the cache, rotating q and k on the way: the one
- * launch between the qkv product and the attention.  Token t is at
+ * Writes new tokens into the cache, rotating q (into q_out) and k on the way:
+ * the one launch between the qkv product and the attention.  Token t is at
  * positions[t] of sequence seq_ids[t]; no two tokens of a call may name the
  * same place, and other tokens of the records that are touched stay as they
  * are.  k is rotated in fp32 and quantised from there; v is taken as it is.
  *   k, v      : device [tokens][kv_heads][head_dim], rows 16-byte aligned
  *   q, q_out  : device [tokens][q_heads][head_dim], rows 16-byte aligned, or
- *               both NULL; q_out may be q; ignored without a rotation
+ *               both NULL; q_out may be q; without a rotation q is copied
  *   positions : device int32 [tokens]; a negative one marks padding: the token
  *               is left out
  *   seq_ids   : device int32 [tokens], or NULL: tokens is a multiple of

@@ -132,12 +132,14 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, 
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+inline bool same_place(const Heads &x, const Heads &y) {
+    return x.data == y.data && x.token_stride == y.token_stride && x.head_stride == y.head_stride;
+}
+
 // Units of a head that turn_unit takes (in place nothing is copied).
 inline int turn_units(const Heads &x, const Heads &y, int head_dim, const Rotation &rot) {
-    const bool in_place = x.data == y.data && x.token_stride == y.token_stride &&
-                          x.head_stride == y.head_stride;
     return (rot.layout == W4_ROPE_HALF ? rot.pairs / 8 : rot.pairs / 4) +
-           (in_place ? 0 : (head_dim - 2 * rot.pairs) / 8);
+           (same_place(x, y) ? 0 : (head_dim - 2 * rot.pairs) / 8);
 }
 
 #ifdef __CUDACC__

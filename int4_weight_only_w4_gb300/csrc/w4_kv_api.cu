@@ -232,7 +232,8 @@ w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_hea
                        const w4_block_table *table, const w4_rotation *rotation,
                        w4_stream_t stream) {
     if (!q != !q_out || (q && q_heads < 1)) return W4_ERR_INVALID_ARG;
-    if (!q || !rotation) q_heads = 0;
+    // (in place and without a rotation there is nothing to do with q)
+    if (!q || (!rotation && w4::same_place(heads_of(q), heads_of(q_out)))) q_heads = 0;
     const w4_status st = list_ok(cache, table, tokens, positions, seq_ids,
                                  2 * (cache ? cache->kv_heads : 0) + q_heads);
     if (st != W4_OK) return st;
@@ -248,7 +249,7 @@ w4_status w4_kv_append(const w4_kv_cache *cache, const w4_heads *k, const w4_hea
         return W4_ERR_INVALID_ARG;
     const int sms = device_sms();
     if (sms <= 0) return W4_ERR_CUDA;
-    w4::Rotation rot = {nullptr, 0, 0, 0};
+    w4::Rotation rot = {nullptr, 0, 0, W4_ROPE_HALF};
     if (rotation)
         rot = {rotation->table, rotation->rows, rotation->rotary_dim / 2, rotation->layout};
     const w4::TokenList list = {positions, seq_ids, tokens,

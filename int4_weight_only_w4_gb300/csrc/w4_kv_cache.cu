@@ -160,8 +160,8 @@ __device__ __forceinline__ uint32_t to_nibbles(const int (&n)[8]) {
     return w;
 }
 
-// The queries of a launch of append_kernel, turned as by w4_rope in blocks of
-// their own (in the rows' loop below every lane would turn its partner too:
+// The queries of a launch of append_kernel, turned (without a rotation: copied)
+// as by w4_rope in blocks of their own (in the rows' loop below every lane would turn its partner too:
 // 16 k tokens of 28 query heads, written and read back, 148 us against 95).
 struct Queries {
     Heads q, out;
@@ -196,7 +196,7 @@ append_kernel(KvPool pool, Heads k, Heads v, Queries q, TokenList list, Rotation
         if (e >= q.all) return;
         const unsigned tg = e / q.units, u = e - tg * q.units, t = tg / q.groups;
         TokenPlace at;
-        if (!kv_place(pool, list, t, rot.rows, &at)) return;
+        if (!kv_place(pool, list, t, rot.table ? rot.rows : 0x7FFFFFFF, &at)) return;
         if (rot.layout == W4_ROPE_HALF)
             turn_unit<W4_ROPE_HALF, HEADS>(q.q, q.out, t, u, tg - t * q.groups, q.groups, q.heads,
                                            rot, at.position, false);

@@ -520,7 +520,8 @@ def kv_pool_bytes(fmt: int, kv_heads: int, head_dim: int, page_tokens: int, page
 
 def kv_append(cache: "PagedCache", k, v, positions, table, seq_ids=None, q=None, q_out=None,
               rotation: "RopeTable | None" = None, stream=None) -> None:
-    """w4_kv_append: write tokens into the cache, rotating k and q (into q_out)."""
+    """w4_kv_append: write tokens into the cache, rotating k and q (into q_out;
+    without a rotation q is copied there)."""
     shape = k.shape
     if v.shape != shape or shape[1:] != cache.head_shape:
         raise ValueError(f"k, v: expected [tokens, {cache.kv_heads}, {cache.head_dim}]")
@@ -651,6 +652,8 @@ class PagedCache:
 
     def append(self, k, v, positions, table, seq_ids=None, q=None, q_out=None, rope=None,
                stream=None) -> None:
+        """Write tokens into the cache: k, and q into q_out, rotated by `rope`
+        (without one as they are), v as it is."""
         kv_append(self, k, v, positions, table, seq_ids, q, q_out, rope, stream)
 
     def read(self, positions, table, seq_ids=None, k=None, v=None, stream=None):

@@ -59,3 +59,34 @@ def test_nan_is_held_as_zero(w4, fmt, layout, D, first, T):  # noqa: F811
         # largest scale, which is the code of any value that large
         x = np.nan_to_num(np.asarray(x, np.float32), nan=0.0, posinf=3e38, neginf=-3e38)
         assert np.array_equal(bits(g), kv.bf16_bits(kv.held(x, fmt)))
+
+
+@pytest.mark.parametrize("fmt", list(kv.FMT))
+@pytest.mark.parametrize("T,HQ", [(1, 14), (5, 3), (700, 28)])
+def test_queries_without_a_rotation_are_copied(w4, fmt, T, HQ):  # noqa: F811
+    rng = np.random.default_rng(T)
+    H, D = 2, 64
+    k, v, q = rows(rng, T, H, D), rows(rng, T, H, D), rows(rng, T, HQ, D)
+    pages = T // 16 + 1
+    cache = w4.PagedCache.make(pages, kv.FMT[fmt], H, D)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    pos = np.arange(T, dtype=np.int32)
+    if T > 1:
+        pos[1] = -1                                            # padding: left out
+    wide = torch.full((T, HQ + 1, D), 9.0, device="cuda", dtype=torch.bfloat16)
+    gq = to_gpu(q)
+    cache.append(to_gpu(k), to_gpu(v), i32(pos), table, q=gq, q_out=wide[:, 1:])
+    cache.check()
+    there = pos >= 0
+    assert np.array_equal(bits(wide[:, 1:])[there], kv.bf16_bits(q)[there])
+    assert (wide[:, 0] == 9.0).all() and (wide[:, 1:][torch.from_numpy(~there).cuda()] == 9.0).all()
+    # in place there is nothing to do
+    before = gq.clone()
+    cache.append(to_gpu(k), to_gpu(v), i32(pos), table, q=gq, q_out=gq)
+    assert torch.equal(gq, before)
+    k2, v2 = cache.read(i32(pos), table)
+    assert np.array_equal(bits(v2)[there], kv.bf16_bits(kv.held(v, fmt))[there])
+    # q is looked at: its rows have to lie on 16-byte boundaries
+    odd = torch.zeros(T * HQ * D + 4, device="cuda", dtype=torch.bfloat16)[4:].view(T, HQ, D)
+    with pytest.raises(w4.W4Error):
+        cache.append(to_gpu(k), to_gpu(v), i32(pos), table, q=odd, q_out=wide[:, 1:])
