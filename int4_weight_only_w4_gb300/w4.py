@@ -475,9 +475,12 @@ def _block_table(t) -> bytes:
     if t.dtype is torch.int32 and t.dim() == 2 and t.is_cuda:
         seqs, width = t.shape
         row, column = t.stride()
-        if column == 1:
-            return _pack_table(t.data_ptr(), seqs, width, row if row > width else width)
-    raise ValueError("block table: expected a CUDA int32 tensor [seqs, pages]")
+        if row < width and seqs == 1:
+            row = width                     # of one row: any stride will do
+        if column == 1 and row >= width:
+            return _pack_table(t.data_ptr(), seqs, width, row)
+    raise ValueError("block table: expected a CUDA int32 tensor [seqs, pages] whose rows do not "
+                     "overlap (an expanded one has to be made contiguous)")
 
 
 def _raw_stream(stream, like) -> int:

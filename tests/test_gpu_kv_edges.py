@@ -90,3 +90,27 @@ def test_queries_without_a_rotation_are_copied(w4, fmt, T, HQ):  # noqa: F811
     odd = torch.zeros(T * HQ * D + 4, device="cuda", dtype=torch.bfloat16)[4:].view(T, HQ, D)
     with pytest.raises(w4.W4Error):
         cache.append(to_gpu(k), to_gpu(v), i32(pos), table, q=odd, q_out=wide[:, 1:])
+
+
+def test_block_tables_whose_rows_overlap_are_refused(w4):  # noqa: F811
+    """A row stride below the width (the rows of an expanded table): refused by
+    every call, before anything is launched."""
+    cache = w4.PagedCache.make(4, w4.KV_INT4, 1, 64)
+    x = torch.zeros(3, 1, 64, device="cuda", dtype=torch.bfloat16)
+    pos, lens = i32([0, 1, 2]), i32([1, 1, 1])
+    one = i32([[2, 1]])
+    overlapping = i32([0, 1, 2, 3]).as_strided((3, 2), (1, 1))
+    for table in (one.expand(3, -1), overlapping):
+        with pytest.raises(ValueError):
+            cache.append(x, x, pos, table)
+        with pytest.raises(ValueError):
+            cache.read(pos, table)
+        with pytest.raises(ValueError):
+            cache.attend(x, lens, table)
+    # one row: its stride does not matter; rows further apart than they are wide
+    for table in (one.as_strided((1, 2), (0, 1)), one.as_strided((1, 2), (1, 1)),
+                  i32(np.arange(9).reshape(3, 3) % 4)[:, :2]):
+        n = table.shape[0]
+        cache.append(x[:n], x[:n], pos[:n], table)
+        cache.attend(x[:n], lens[:n], table)
+    cache.check()
