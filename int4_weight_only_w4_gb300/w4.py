@@ -8,6 +8,7 @@ Importing this module raises if the CUDA library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import enum
 import os
@@ -490,6 +491,20 @@ def _raw_stream(stream, like) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+_no_stream = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """The context in which a call on `stream` makes what it makes by itself:
+    torch hands out memory, and fills it, by the current stream's order."""
+    if stream is None:
+        return _no_stream
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def rope_table(spec: dict, rows: int, table, stream=None) -> None:
     """w4_rope_table: fill `table`, float32 [rows, rotary_dim/2, 2] on the
     device.  spec: the fields of w4_rope_spec (missing ones: no scaling,
@@ -606,16 +621,19 @@ class RopeTable:
              stream=None, **scaling) -> "RopeTable":
         """A table filled by w4_rope_table; scaling: scaling, factor,
         original_context, low_turns, high_turns, amplitude of w4_rope_spec."""
-        t = torch.empty((rows, rotary_dim // 2, 2), dtype=torch.float32,
-                        device=device if device is not None else "cuda")
+        device = torch.device("cuda" if device is None else device)
+        with _on(stream, device):
+            t = torch.empty((rows, rotary_dim // 2, 2), dtype=torch.float32, device=device)
         rope_table(dict(rotary_dim=rotary_dim, base=base, **scaling), rows, t, stream)
         return cls(t, layout)
 
     def apply(self, x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor | None = None,
               error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        """x [tokens, heads, head_dim] bfloat16, rotated; out may be x."""
+        """x [tokens, heads, head_dim] bfloat16, rotated; out may be x (default:
+        a new tensor, made on `stream`)."""
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            with _on(stream, x.device):
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         rope(x, out, positions, self, error, stream)
         return out
 
@@ -623,7 +641,9 @@ class RopeTable:
 class PagedCache:
     """A paged key-value cache over a caller's pool (a contiguous CUDA tensor
     of kv_pool_bytes() bytes).  Its calls record what is out of range in
-    `error` (one int32 on the device; see check()).  attend() uses the cache's
+    `error` (one int32 on the device; see check()).  The error word, and make()'s
+    pool, are filled on torch's current stream; what a later call makes by itself
+    is made on the stream of that call.  attend() uses the cache's
     own workspace unless it is given one: calls that overlap on the device
     need one each."""
 
@@ -660,11 +680,15 @@ class PagedCache:
         kv_append(self, k, v, positions, table, seq_ids, q, q_out, rope, stream)
 
     def read(self, positions, table, seq_ids=None, k=None, v=None, stream=None):
+        """The cached keys and values of the listed tokens (default outputs: new
+        tensors, made on `stream`, zero where a token is left out)."""
         shape = (positions.numel(), self.kv_heads, self.head_dim)
-        if k is None:
-            k = torch.zeros(shape, dtype=torch.bfloat16, device=self.pool.device)
-        if v is None:
-            v = torch.zeros(shape, dtype=torch.bfloat16, device=self.pool.device)
+        if k is None or v is None:
+            with _on(stream, self.pool.device):
+                if k is None:
+                    k = torch.zeros(shape, dtype=torch.bfloat16, device=self.pool.device)
+                if v is None:
+                    v = torch.zeros(shape, dtype=torch.bfloat16, device=self.pool.device)
         kv_read(self, k, v, positions, table, seq_ids, stream)
         return k, v
 
@@ -675,21 +699,27 @@ class PagedCache:
 
     def attend(self, q, lens, table, scale=None, window: int = 0, out=None, lse=None,
                workspace=None, stream=None):
-        """Attention of the new tokens; returns (out bfloat16, lse float32)."""
+        """Attention of the new tokens; returns (out bfloat16, lse float32), by
+        default new tensors, made on `stream`."""
         if workspace is None:
             if self.workspace is None:
                 self.workspace = self.new_workspace()
             workspace = self.workspace
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        if out is None or lse is None:
+            with _on(stream, q.device):
+                if out is None:
+                    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+                if lse is None:
+                    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         paged_attn(self, q, out, lens, table, workspace, scale, window, lse, stream)
         return out, lse
 
     def check(self) -> None:
-        """Raise W4Error if a call recorded an error (synchronises), and clear it."""
+        """Raise W4Error if a call recorded an error, and clear it.  Waits for
+        the device: the calls may have been on any stream."""
+        torch.cuda.synchronize(self.error.device)
         bits = int(self.error.item())
         if bits:
             self.error.zero_()
+            torch.cuda.synchronize(self.error.device)
             raise W4Error(Status.INVALID_ARG, f"paged cache (error word {bits})")

@@ -114,3 +114,57 @@ def test_block_tables_whose_rows_overlap_are_refused(w4):  # noqa: F811
         cache.append(x[:n], x[:n], pos[:n], table)
         cache.attend(x[:n], lens[:n], table)
     cache.check()
+
+
+def busy(stream):
+    """Some milliseconds of work on a stream."""
+    x = torch.ones(8192, 8192, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(20):
+            x = x @ x * 0.0 + 1.0
+    return x
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_default_outputs_belong_to_the_calls_stream(w4, handle):  # noqa: F811
+    """What a call makes by itself is made, and filled, on the stream that the
+    call is given, whatever torch's current stream still has to do."""
+    rng = np.random.default_rng(3)
+    T, H, D = 64, 2, 64
+    k, v = rows(rng, T, H, D), rows(rng, T, H, D)
+    cache = w4.PagedCache.make(4, w4.KV_INT8, H, D)
+    table, pos = i32([[2, 0, 3, 1]]), i32(np.arange(T))
+    cache.append(to_gpu(k), to_gpu(v), pos, table)
+    rope = w4.RopeTable(torch.rand(T, D // 2, 2, device="cuda"))
+    q, lens = to_gpu(k[:8]), i32([T])
+    want = cache.read(pos, table), rope.apply(q, pos[:8]), cache.attend(q, lens, table)
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if handle else side
+    # memory that the current stream still writes to, free for its next tensors
+    for _ in range(3):
+        keep = busy(torch.cuda.current_stream())
+        for n in (T * H * D, 8 * H * D, 8 * H * 2):
+            torch.full((n,), 9.0, device="cuda", dtype=torch.bfloat16)
+        got = (cache.read(pos, table, stream=given), rope.apply(q, pos[:8], stream=given),
+               cache.attend(q, lens, table, stream=given))
+        made = w4.RopeTable.make(100, 64, 1e4, stream=given).table
+        torch.cuda.synchronize()
+        for a, b in ((got[0][0], want[0][0]), (got[0][1], want[0][1]), (got[1], want[1]),
+                     (got[2][0], want[2][0]), (got[2][1], want[2][1])):
+            assert torch.equal(a, b)
+        assert torch.equal(made, w4.RopeTable.make(100, 64, 1e4).table)
+        del keep
+
+
+def test_check_waits_for_calls_on_other_streams(w4):  # noqa: F811
+    cache = w4.PagedCache.make(1, w4.KV_INT4, 1, 64)
+    k = torch.zeros(1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        keep = busy(side)
+        cache.append(k, k, i32([16]), i32([[0]]), stream=side)     # past the block table
+        with pytest.raises(w4.W4Error):
+            cache.check()
+        cache.check()                                              # cleared
+        del keep
