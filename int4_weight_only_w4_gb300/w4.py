@@ -484,6 +484,9 @@ def _block_table(t) -> bytes:
                      "overlap (an expanded one has to be made contiguous)")
 
 
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
+
 def _raw_stream(stream, like) -> int:
     """As _stream, without making a Stream object for the current one."""
     if stream is None:
@@ -577,6 +580,7 @@ def paged_attn_workspace_bytes(cache: "PagedCache") -> int:
 
 
 def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, workspace, stream):
+    # workspace: its address and bytes; stream: a raw one
     shape = q.shape
     T, H, D = shape
     B = table.shape[0]
@@ -588,7 +592,7 @@ def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, work
         lse = _ptr(lse)
     _ok(fn(cache.ref, _heads(q), _heads(out, dtype), H, T // B, _int32(lens, B, "lens"),
            _block_table(table), D ** -0.5 if scale is None else scale, window, lse,
-           _ptr(workspace), workspace.nbytes, _raw_stream(stream, q)), where)
+           *workspace, stream), where)
 
 
 def paged_attn(cache: "PagedCache", q, out, lens, table, workspace, scale=None, window: int = 0,
@@ -596,14 +600,14 @@ def paged_attn(cache: "PagedCache", q, out, lens, table, workspace, scale=None, 
     """w4_paged_attn: out[b * tokens + i] (bfloat16) = attention of the new
     token i of sequence b over its cached tokens."""
     _attn(_paged_attn, "w4_paged_attn", torch.bfloat16, cache, q, out, lens, table, scale,
-          window, lse, workspace, stream)
+          window, lse, (_ptr(workspace), workspace.nbytes), _raw_stream(stream, q))
 
 
 def paged_attn_f32(cache: "PagedCache", q, out, lens, table, workspace, scale=None,
                    window: int = 0, lse=None, stream=None) -> None:
     """w4_paged_attn_f32: as paged_attn, fp32 result."""
     _attn(_paged_attn_f32, "w4_paged_attn_f32", torch.float32, cache, q, out, lens, table, scale,
-          window, lse, workspace, stream)
+          window, lse, (_ptr(workspace), workspace.nbytes), _raw_stream(stream, q))
 
 
 class RopeTable:
@@ -643,9 +647,10 @@ class PagedCache:
     of kv_pool_bytes() bytes).  Its calls record what is out of range in
     `error` (one int32 on the device; see check()).  The error word, and make()'s
     pool, are filled on torch's current stream; what a later call makes by itself
-    is made on the stream of that call.  attend() uses the cache's
-    own workspace unless it is given one: calls that overlap on the device
-    need one each."""
+    is made on the stream of that call.  attend() uses a workspace that the cache
+    keeps for the stream (see `workspace`), under graph capture one of the
+    graph's own, unless it is given one: calls that overlap on the device need
+    one each."""
 
     def __init__(self, pool: torch.Tensor, fmt: int, kv_heads: int, head_dim: int,
                  page_tokens: int = RECORD_TOKENS, error: torch.Tensor | None = None):
@@ -662,7 +667,7 @@ class PagedCache:
         self._struct = _KvCache(_ptr(pool), fmt, kv_heads, head_dim, page_tokens, self.pages,
                                 _ptr(self.error))
         self.ref = ctypes.byref(self._struct)
-        self.workspace = None
+        self._workspaces = {}              # by raw stream: (address, bytes), tensor
 
     @classmethod
     def make(cls, pages: int, fmt: int, kv_heads: int, head_dim: int,
@@ -697,21 +702,46 @@ class PagedCache:
         return torch.empty(paged_attn_workspace_bytes(self), dtype=torch.uint8,
                            device=self.pool.device)
 
+    @property
+    def workspace(self) -> torch.Tensor | None:
+        """The workspace that attend() has made for torch's current stream."""
+        kept = self._workspaces.get(_raw_stream(None, self.pool))
+        return kept and kept[1]
+
+    def _workspace_on(self, stream):
+        """A workspace that no call on another stream uses, as in _workspaces.  A
+        captured call's is the graph's: an eager one may run beside a replay, and
+        memory that was made under capture is not for others."""
+        with _on(stream, self.pool.device):
+            capturing = _capturing()
+            raw = _raw_stream(stream, self.pool)
+            kept = None if capturing else self._workspaces.get(raw)
+            if kept is None:
+                ws = self.new_workspace()
+                kept = (_ptr(ws), ws.nbytes), ws
+                if not capturing:
+                    self._workspaces[raw] = kept
+            return kept
+
     def attend(self, q, lens, table, scale=None, window: int = 0, out=None, lse=None,
                workspace=None, stream=None):
         """Attention of the new tokens; returns (out bfloat16, lse float32), by
         default new tensors, made on `stream`."""
-        if workspace is None:
-            if self.workspace is None:
-                self.workspace = self.new_workspace()
-            workspace = self.workspace
+        raw, kept = _raw_stream(stream, q), None
+        if workspace is not None:
+            kept = (_ptr(workspace), workspace.nbytes), workspace
+        elif stream is None and not _capturing():
+            kept = self._workspaces.get(raw)
+        if kept is None:
+            kept = self._workspace_on(stream)
         if out is None or lse is None:
             with _on(stream, q.device):
                 if out is None:
                     out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
                 if lse is None:
                     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        paged_attn(self, q, out, lens, table, workspace, scale, window, lse, stream)
+        _attn(_paged_attn, "w4_paged_attn", torch.bfloat16, self, q, out, lens, table, scale,
+              window, lse, kept[0], raw)
         return out, lse
 
     def check(self) -> None:

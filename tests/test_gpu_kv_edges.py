@@ -168,3 +168,56 @@ def test_check_waits_for_calls_on_other_streams(w4):  # noqa: F811
             cache.check()
         cache.check()                                              # cleared
         del keep
+
+
+def test_every_stream_and_graph_has_a_workspace_of_its_own(w4):  # noqa: F811
+    """attend() without a workspace: calls on two streams, and a replayed graph
+    beside either, share nothing."""
+    a = Setup(w4, "int8", 128, 4, 7, 16, 1, [3000, 900], seed=1)
+    b = Setup(w4, "int8", 128, 4, 7, 16, 2, [2500, 17, 1300], seed=2)
+    want_a = a.cache.attend(a.gq, a.glens, a.table)
+    # b over a's cache object: its pool and table, a's workspaces
+    b.cache.attend(b.gq, b.glens, b.table)
+    want_b = b.cache.attend(b.gq, b.glens, b.table, workspace=b.cache.new_workspace())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.cache.attend(a.gq, a.glens, a.table)
+        of_side = a.cache.workspace
+    assert of_side is not None and of_side.data_ptr() != a.cache.workspace.data_ptr()
+    a.cache.attend(a.gq, a.glens, a.table, stream=side)        # by argument: the same one
+    with torch.cuda.stream(side):
+        assert a.cache.workspace is of_side
+    torch.cuda.synchronize()
+    # a captured call leaves the eager ones' workspaces alone, and keeps none
+    mine, kept = a.cache.workspace, a.cache.workspace.clone()
+    out, lse = torch.empty_like(want_a[0]), torch.empty_like(want_a[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.cache.attend(a.gq, a.glens, a.table, out=out, lse=lse)
+        a.cache.attend(a.gq, a.glens, a.table, out=out, lse=lse)
+    assert a.cache.workspace is mine
+    torch.cuda.synchronize()
+    mine.fill_(0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want_a[0]) and torch.equal(lse, want_a[1])
+    assert (mine == 0).all()
+    mine.copy_(kept)
+    # the first call of a cache under capture
+    new = w4.PagedCache(a.cache.pool, a.cache.format, 4, 128)
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        new.attend(a.gq, a.glens, a.table, out=out, lse=lse)
+    assert new.workspace is None
+    # side by side
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        got.append(a.cache.attend(a.gq, a.glens, a.table))
+        graph.replay()
+        got.append(a.cache.attend(a.gq, a.glens, a.table, stream=side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want_a[0]) and torch.equal(x, want_a[1]) for o, x in got)
+    assert torch.equal(out, want_a[0])
+    got = b.cache.attend(b.gq, b.glens, b.table)
+    assert torch.equal(got[0], want_b[0]) and torch.equal(got[1], want_b[1])
