@@ -493,7 +493,8 @@ typedef struct w4_rope_spec {
  * its error does not grow with p (each entry is within 1 ulp of the exact
  * value of the double-precision f_i).
  *   table : device, float [rows][rotary_dim/2][2], 16-byte aligned
- * Errors: W4_ERR_INVALID_ARG, W4_ERR_CUDA.
+ * Errors: W4_ERR_INVALID_ARG (a base or frequency that comes out infinite
+ * too), W4_ERR_CUDA.
  */
 w4_status w4_rope_table(const w4_rope_spec *spec, int rows, float *table, w4_stream_t stream);
 

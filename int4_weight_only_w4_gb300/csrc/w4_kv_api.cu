@@ -175,6 +175,7 @@ w4_status w4_rope_table(const w4_rope_spec *spec, int rows, float *table, w4_str
             break;
         default: return W4_ERR_INVALID_ARG;
     }
+    if (!isfinite(base)) return W4_ERR_INVALID_ARG;
     const double two_pi = 6.283185307179586476925286766559;
     unsigned long long turns[256];
     for (int i = 0; i < rot / 2; ++i) {
@@ -187,6 +188,7 @@ w4_status w4_rope_table(const w4_rope_spec *spec, int rows, float *table, w4_str
             keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
             f = f * (keep + (1 - keep) / factor);
         }
+        if (!isfinite(f)) return W4_ERR_INVALID_ARG;
         f -= floor(f);                                    // whole turns change nothing
         const double scaled = ldexp(f, 64);
         turns[i] = scaled >= 18446744073709551615.0 ? 0ull : (unsigned long long)scaled;
