@@ -628,9 +628,10 @@ w4_status w4_paged_attn_workspace_bytes(const w4_kv_cache *cache, size_t *bytes)
  * What the pool holds past lens[b] is never looked at (it may be NaN).
  * Products on the tensor cores: bf16 operands for a bf16 cache, exact codes
  * against fp16 for the quantised ones; scores, maxima, sums and outputs are
- * fp32; probabilities enter the second product as bf16 (fp16).  The sums'
- * order depends on the lengths, the window and the device only, never on
- * which block finishes first: repeated calls give the same bits.
+ * fp32; probabilities enter the second product in two bf16 parts (16 bits in
+ * all), against codes as fp16.  The sums' order depends on the lengths, the
+ * window and the device only, never on which block finishes first: repeated
+ * calls give the same bits.
  *   q      : device [seqs * tokens][q_heads][head_dim] bf16, rows 16-byte aligned
  *   out    : device [seqs * tokens][q_heads][head_dim] bf16, rows 16-byte aligned
  *            (w4_paged_attn_f32: float, rows 16-byte aligned)

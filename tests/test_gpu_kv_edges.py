@@ -221,3 +221,40 @@ def test_every_stream_and_graph_has_a_workspace_of_its_own(w4):  # noqa: F811
     assert torch.equal(out, want_a[0])
     got = b.cache.attend(b.gq, b.glens, b.table)
     assert torch.equal(got[0], want_b[0]) and torch.equal(got[1], want_b[1])
+
+
+def test_infinite_values_of_visible_keys_stay_infinite(w4):  # noqa: F811
+    """bf16: an infinite value gives an infinite result of its sign in its
+    column for every row that sees it (however round its probability is), and
+    changes no other column."""
+    for M, n in ((1, 50), (4, 37), (1, 1)):
+        s = Setup(w4, "bf16", 64, 1, 2, 16, M, [n], seed=n)
+        want, want_lse = s.cache.attend(s.gq, s.glens, s.table)
+        for bad in (float("inf"), float("-inf")):
+            v = s.values[0].copy()
+            v[0, 0, 5] = v[n // 2, 0, 5] = bad                 # all rows see these keys
+            s.cache.append(to_gpu(s.keys[0]), to_gpu(v), i32(np.arange(n)), s.table)
+            got, lse = s.cache.attend(s.gq, s.glens, s.table)
+            assert (got[..., 5] == bad).all()
+            keep = torch.arange(64, device="cuda") != 5
+            assert torch.equal(got[..., keep], want[..., keep]) and torch.equal(lse, want_lse)
+    # equal scores: every probability is a power of two
+    s.gq.zero_()
+    got, _ = s.cache.attend(s.gq, s.glens, s.table)
+    assert (got[..., 5] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("D,H,group,M", [(128, 4, 7, 1), (64, 2, 7, 3), (128, 2, 4, 8)])
+def test_probabilities_beside_bf16_values_keep_16_bits(w4, D, H, group, M):  # noqa: F811
+    """The fp32 result of a bf16 cache: probabilities within 2^-15 of
+    themselves (their two parts), scores as in kv_testutil."""
+    lens = [900, 33, 8, 400]
+    s = Setup(w4, "bf16", D, H, group, 16, M, lens, seed=D + M)
+    out = torch.empty(s.gq.shape, device="cuda")
+    w4.paged_attn_f32(s.cache, s.gq, out, s.glens, s.table, s.cache.new_workspace())
+    ref, _, mag = kv.attention(s.q, s.keys, s.values, lens, M, D ** -0.5, 0)
+    dS = kv.score_error("bf16", s.q, s.keys, s.scales, lens, D ** -0.5)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= (2.0 ** -15 + 4 * dS + (max(lens) + 64) * 2.0 ** -23) * mag + 1e-30).all()
+    # the scores' errors have both signs and are far from their bound
+    assert np.linalg.norm(err) <= (2.0 ** -15 + 2.0 ** -15) * np.linalg.norm(mag)
