@@ -475,7 +475,9 @@ typedef struct w4_rotation {
 #define W4_ROPE_SCALE_BASE 2     /* base * factor^(rotary_dim/(rotary_dim-2)) instead of base */
 #define W4_ROPE_SCALE_PARTS 3    /* between f_i / factor, for pairs that make at most low_turns
                                     turns in original_context positions, and f_i, for those that
-                                    make at least high_turns; linear in the turns between */
+                                    make at least high_turns; linear in the turns between.  (A
+                                    model whose table is linear in the pair's index i instead,
+                                    between two whole indices, brings its own table.) */
 typedef struct w4_rope_spec {
     int rotary_dim;              /* even, 2..512 */
     int scaling;
@@ -490,8 +492,8 @@ typedef struct w4_rope_spec {
 /*
  * Fills rows 0..rows-1 of a rotation table: amplitude * (cos, sin)(p * f_i).
  * The angle p * f_i is reduced to a fraction of a turn in 64-bit integers, so
- * its error does not grow with p (each entry is within 1 ulp of the exact
- * value of the double-precision f_i).
+ * whole turns drop out exactly: the angle is within p * f_i * 2^-52 of that of
+ * the double-precision f_i, and the entry is that angle's within 1 ulp.
  *   table : device, float [rows][rotary_dim/2][2], 16-byte aligned
  * Errors: W4_ERR_INVALID_ARG (a base or frequency that comes out infinite
  * too), W4_ERR_CUDA.

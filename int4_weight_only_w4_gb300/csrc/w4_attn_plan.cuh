@@ -17,7 +17,8 @@ constexpr int kRowsMax = 64;           // rows of a block
 // What a head's start and end cost, in records of one tile of rows.  Ragged
 // batches: 64 x 8k int8 64 us at 0, 50.8 at 28, 49.7 at 40, 50.5 at 56; 8 new
 // tokens over 8 x 8k bf16 44.1, 33.8, 30.4, 30.7; 64 x 8k int4 57.6, 43.6, 41.4,
-// 40.2; even ones lose a little (8 x 2k bf16 12.0, 13.5, 12.6, 12.7).
+// 40.2; even ones lose a little (8 x 2k bf16 12.0, 13.5, 12.6, 12.7).  One number
+// for all formats: the three ragged ones want about the same.
 constexpr int kHeadRecords = 40;
 constexpr int kMaxStages = 16;         // of one group's ring
 constexpr int kMaxGrid = 256;
@@ -31,11 +32,19 @@ W4_HD constexpr int compute_warps(int D, int NT) {
 }
 
 // Two tiles a warp where that makes a third as many groups again: the operands
-// of a record serve both tiles, but fewer warps are there to wait.  Measured at
-// 48 x 4 k tokens of 64 bf16 values: 3 tiles 26.7 us with one, 27.9 with two;
-// 4 tiles 32.6, 28.3; 5 tiles 39.5, 34.8; 7 tiles 50.7, 42.9; at 8 x 8 k of 128:
-// 2 tiles 31.5, 33.2; 3 tiles 34.5, 37.1; 5 tiles 43.9, 41.7; 6 tiles 48.1, 43.2;
-// 7 tiles 50.0, 54.2.
+// of a record serve both tiles, but fewer warps are there to wait.  Measured, in
+// us with one and with two tiles a warp:
+//   tiles               2           3           4           5           6           7
+//   48 x 4 k of 64
+//     bf16                  -       27.9, 29.3  36.1, 29.7  42.3, 39.1      -       54.0, 48.5
+//     4 bits           24.9, 20.7  29.3, 28.7  38.1, 28.9  45.0, 37.6      -       55.9, 47.3
+//   8 x 8 k of 128
+//     bf16             30.6, 31.4  31.1, 33.9  35.4, 34.2  43.1, 45.0  46.2, 45.8  48.8, 55.4
+//   32 x 4 k of 128
+//     4 bits           38.8, 33.4  53.2, 51.5  68.0, 52.0  85.4, 75.2  92.7, 76.7  101.8, 95.7
+//     8 bits                -       51.4, 55.7      -       81.0, 80.9      -       98.8, 97.7
+// The rule is bf16's; 4-bit caches, whose conversion a second tile shares, would
+// gain by two from 2 tiles on, and at 7 of 128.
 inline int tiles_a_warp(int D, int rows) {
     const int tiles = (rows < kRowsMax ? rows + 7 : kRowsMax) / 8;
     const int one = compute_warps(D, 1) / tiles, two = compute_warps(D, 2) / ((tiles + 1) / 2);

@@ -17,12 +17,14 @@
 // copy's rate).  Tiles that are no whole record (decode steps, the ends of a
 // prompt, tokens in another order) go byte by byte.
 //
-// What bounds it: one token of each of 64 sequences 6.0 us, two launches and a
-// chain of four dependent trips to memory (position, page, row, record); 4096
-// tokens in 8 bits 23.7 us, most of it the instructions of the quantisation and
-// the launches (its bytes take 12.7); from 16 k tokens on the traffic of the
-// queries, which pass through (the writing kernel: 62 % of the issue slots, 57 %
-// of the DRAM's).
+// What bounds it (captured calls, written and read back; each by itself): one
+// token of each of 64 sequences 6.0 us (3.2, 2.8), two launches and a chain of
+// four dependent trips to memory (position, page, row, record); 4096 tokens in 8
+// bits 23.6 us (18.3, 4.5; the bytes take 10.8 and 1.9): writing issues in 57 % of
+// its cycles and waits for rows and table, reading is one wave of blocks that wait
+// at their tile's barriers; 16 k tokens in 4 bits 61.9 us (51.8, 10.1; bytes 42.1
+// and 6.3), the traffic of the queries, which pass through (writing: 62 % of the
+// issue slots, 57 % of the DRAM's).  Read back at once the records come from L2.
 #include "w4_kv.cuh"
 
 namespace w4 {

@@ -44,7 +44,7 @@
 // has, what it costs to start and to finish one: without that, blocks with many
 // short heads came last, and 64 ragged sequences of up to 8192 tokens in 8 bits
 // took 64 us instead of 50.  A cut that would leave only a few records of a head
-// on one side moves to the head's border.
+// on one side moves to the head's border on that side (w4_attn_plan.cuh).
 // The pieces of cut heads are joined by a second kernel, a few rows a block,
 // whose launch overlaps the first one's end: left to the block that finished a
 // head last, the joining of 5 pieces of 56 rows took 7 us.  In a block, two
@@ -54,11 +54,11 @@
 //
 // Measured (28 query and 4 key/value heads of 128, one new token, captured calls;
 // a copy reaches 6788 GB/s).  bf16, bound by HBM: 32 x 16384 tokens 160 us =
-// 6690 GB/s; one sequence of 65536, 108 records a block, 29.8 us = 4500 GB/s,
+// 6700 GB/s; one sequence of 65536, 108 records a block, 30.0 us = 4480 GB/s,
 // 9 us of it around the records.  8 bits: 64 ragged sequences of up to 8192
-// 49.4 us = 5620 GB/s.  4 bits, bound by the instructions of conversion and
-// softmax (58 % of the issue slots, ALU 46 %, tensor pipe 23 %): 4 x 131072
-// 60.3 us = 4730 GB/s.
+// 48.7 us = 5700 GB/s (other lengths up to 55).  4 bits: 4 x 131072 60.2 us = 4740
+// GB/s, most of it the instructions of conversion and softmax, though no unit is
+// full (58 % of the issue slots, ALU 46 %, tensor pipe 23 %, DRAM 59 %).
 #include <atomic>
 
 #include "w4_attn_plan.cuh"
