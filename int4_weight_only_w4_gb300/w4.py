@@ -704,9 +704,17 @@ class PagedCache:
 
     @property
     def workspace(self) -> torch.Tensor | None:
-        """The workspace that attend() has made for torch's current stream."""
+        """The workspace of attend() on torch's current stream: the one that it
+        has made, or that was set here."""
         kept = self._workspaces.get(_raw_stream(None, self.pool))
         return kept and kept[1]
+
+    @workspace.setter
+    def workspace(self, ws: torch.Tensor | None) -> None:
+        if ws is None:
+            self._workspaces.pop(_raw_stream(None, self.pool), None)
+        else:
+            self._workspaces[_raw_stream(None, self.pool)] = (_ptr(ws), ws.nbytes), ws
 
     def _workspace_on(self, stream):
         """A workspace that no call on another stream uses, as in _workspaces.  A

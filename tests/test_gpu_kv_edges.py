@@ -258,3 +258,16 @@ def test_probabilities_beside_bf16_values_keep_16_bits(w4, D, H, group, M):  # n
     assert (err <= (2.0 ** -15 + 4 * dS + (max(lens) + 64) * 2.0 ** -23) * mag + 1e-30).all()
     # the scores' errors have both signs and are far from their bound
     assert np.linalg.norm(err) <= (2.0 ** -15 + 2.0 ** -15) * np.linalg.norm(mag)
+
+
+def test_a_workspace_of_the_callers_can_be_set(w4):  # noqa: F811
+    s = Setup(w4, "int4", 64, 2, 3, 16, 1, [700, 40], seed=1)
+    want = s.cache.attend(s.gq, s.glens, s.table)
+    mine = s.cache.new_workspace().fill_(0)
+    s.cache.workspace = mine
+    got = s.cache.attend(s.gq, s.glens, s.table)
+    assert s.cache.workspace is mine and bool((mine != 0).any())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    s.cache.workspace = None
+    got = s.cache.attend(s.gq, s.glens, s.table)
+    assert s.cache.workspace is not mine and torch.equal(got[0], want[0])
