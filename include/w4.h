@@ -446,6 +446,7 @@ w4_status w4_stream_read(const void *src, size_t bytes, int mode, uint32_t *out,
 #define W4_KV_ERR_SEQUENCE 4u    /* a sequence number outside the block table */
 #define W4_KV_ERR_LENGTH 8u      /* a length past the block table (it is cut to it) */
 #define W4_KV_ERR_WAIT 16u       /* a kernel gave up waiting for its own copies */
+#define W4_KV_ERR_BLOCK 32u      /* a listed block outside its sequence, or out of order */
 
 /* A bfloat16 tensor [tokens][heads][head_dim] whose last dimension is
  * contiguous; strides in elements (may be those of a slice of a wider row,
@@ -655,6 +656,66 @@ w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w
                             int q_heads, int tokens, const int32_t *lens,
                             const w4_block_table *table, float scale, int window, float *lse,
                             void *workspace, size_t workspace_bytes, w4_stream_t stream);
+
+/* ======================================================================
+ * Long contexts: attention over the blocks of a cache that a cheap score
+ * selects, and eviction of the tokens that got little attention.  A block is a
+ * page of the cache: block n of a sequence is its tokens n * page_tokens ..
+ * (n+1) * page_tokens - 1.  (None of the pages has them; they work on the cache
+ * above, in its manner: lengths and lists are device memory, checked by the
+ * kernels.)
+ *
+ * A decode step that reads a part of the cache:
+ *   w4_kv_append, w4_key_bounds (the blocks that got new keys), w4_block_scores,
+ *   w4_select (unit = page_tokens), w4_sparse_attn.
+ * Cutting a cache down to `count` tokens a head:
+ *   w4_paged_attn, w4_attn_weights over the steps, then w4_select (unit = 1),
+ *   w4_kv_gather into other pages; its counts are the sequences' new lengths.
+ *   Kept keys stay rotated by the positions that they had.  A token that is
+ *   appended later goes to the place after the kept ones, while its rotation
+ *   goes by its position in the text: w4_rope, then w4_kv_append without a
+ *   rotation.
+ * ====================================================================== */
+
+/*
+ * Bounds of the keys of blocks: for every sequence, those that its last `tokens`
+ * tokens lie in (after a decode step one or two, after a prompt all of it), and
+ * every key/value head:
+ *   bounds[page][head][0][d] = max, bounds[page][head][1][d] = min
+ * over the block's tokens j < lens[b] of value d of key j, as w4_kv_read returns
+ * it; if one of them is NaN, both are.  They go by page: a page that several
+ * sequences share should be full in all of them, or it gets the bounds of one.
+ *   bounds : device, bfloat16 [pages][kv_heads][2][head_dim], 16-byte aligned
+ *   tokens : >= 1
+ *   lens   : device int32 [table->seqs]; negative counts as 0
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim; 2^31 or more
+ * tokens x heads in the table's room), W4_ERR_CUDA.
+ */
+w4_status w4_key_bounds(const w4_kv_cache *cache, uint16_t *bounds, int tokens,
+                        const int32_t *lens, const w4_block_table *table, w4_stream_t stream);
+
+/*
+ * How large q . k can be in a block, from its bounds:
+ *   scores[b][h][n] = max over the rows of sum_d (q_d >= 0 ? q_d hi_d : q_d lo_d)
+ * the rows being the new tokens of sequence b (at positions lens[b] - tokens + i
+ * >= 0) in the q_heads / kv_heads query heads of h; bf16 products summed in fp32.
+ * One that is not finite (bounds or queries that are not) counts as +infinity, a
+ * block whose page is not in the pool as -infinity.  Blocks from lens[b] on are
+ * left as they were.  New tokens of one call share their scores: a call for
+ * single tokens, or a table with a row for each, keeps them apart.
+ *   bounds  : as w4_key_bounds fills it
+ *   q       : device [seqs * tokens][q_heads][head_dim] bf16, rows 16-byte aligned
+ *   tokens  : 1..8;  q_heads : a multiple of kv_heads, at most 4096 times it
+ *   scores  : device float [seqs][kv_heads][columns]
+ *   columns : >= table->width
+ * The pool is not looked at.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, sizes as
+ * above), W4_ERR_CUDA.
+ */
+w4_status w4_block_scores(const w4_kv_cache *cache, const uint16_t *bounds, const w4_heads *q,
+                          int q_heads, int tokens, const int32_t *lens,
+                          const w4_block_table *table, float *scores, int columns,
+                          w4_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -113,6 +113,13 @@ size_t attn_workspace_bytes(int head_dim, int num_sms);
 cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, int num_sms,
                               cudaStream_t stream);
 
+cudaError_t launch_key_bounds(const KvPool &pool, int format, int head_dim, void *bounds,
+                              int tokens, const int32_t *lens, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_scores(const KvPool &pool, int head_dim, const void *bounds,
+                                const Heads &q, int group, unsigned group_magic, int tokens,
+                                const int32_t *lens, float *scores, int columns, int num_sms,
+                                cudaStream_t stream);
+
 // Launch with programmatic stream serialisation: the grid may start while the
 // previous kernel of the stream drains; every kernel launched this way calls
 // griddepcontrol.wait before it touches memory that another kernel writes.

@@ -96,6 +96,32 @@ w4_status list_ok(const w4_kv_cache *cache, const w4_block_table *table, int tok
     return W4_OK;
 }
 
+// Queries that meet a cache: the new tokens of every sequence.
+w4_status queries_ok(const w4_kv_cache *cache, const w4_heads *q, int q_heads, int tokens,
+                     const w4_block_table *table) {
+    if (!q || !q->data) return W4_ERR_INVALID_ARG;
+    if (tokens < 1 || tokens > W4_MAX_TOKENS) return W4_ERR_UNSUPPORTED;
+    if (q_heads < 1 || q_heads % cache->kv_heads) return W4_ERR_INVALID_ARG;
+    if (q_heads / cache->kv_heads > 4096) return W4_ERR_UNSUPPORTED;
+    if (!rows_aligned(q, 2)) return W4_ERR_INVALID_ARG;
+    return (long long)table->seqs * q_heads * tokens < (1LL << 31) ? W4_OK : W4_ERR_UNSUPPORTED;
+}
+
+// The cache, its table and the lengths of a call that walks all sequences: what
+// it counts in 32 bits are a sequence's tokens, and records of all heads.
+w4_status walk_ok(const w4_kv_cache *cache, const w4_block_table *table, const int32_t *lens) {
+    const w4_status st = cache_ok(cache, true);
+    if (st != W4_OK) return st;
+    if (!table_ok(table) || !lens || !aligned(lens, 4)) return W4_ERR_INVALID_ARG;
+    const long long room = (long long)table->width * cache->page_tokens;
+    if (room >= (1LL << 31) || (room / w4::kRecTokens * table->seqs) >= (1LL << 31) ||
+        room / w4::kRecTokens * table->seqs * cache->kv_heads >= (1LL << 31))
+        return W4_ERR_UNSUPPORTED;
+    return W4_OK;
+}
+
+unsigned magic_of(int group) { return group > 1 ? 0xFFFFFFFFu / (unsigned)group + 1 : 0; }
+
 w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
                             int q_heads, int tokens, const int32_t *lens,
                             const w4_block_table *table, float scale, int window, float *lse,
@@ -137,7 +163,7 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     a.lens = lens;
     a.q_heads = q_heads;
     a.group = q_heads / cache->kv_heads;
-    a.group_magic = a.group > 1 ? 0xFFFFFFFFu / (unsigned)a.group + 1 : 0;
+    a.group_magic = magic_of(a.group);
     a.tokens = tokens;
     a.scale = scale;
     // a window as wide as the longest sequence leaves nothing out (and so the
@@ -305,6 +331,36 @@ w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w
                             void *workspace, size_t workspace_bytes, w4_stream_t stream) {
     return paged_attn_common(cache, q, out, q_heads, tokens, lens, table, scale, window, lse,
                              workspace, workspace_bytes, true, stream);
+}
+
+w4_status w4_key_bounds(const w4_kv_cache *cache, uint16_t *bounds, int tokens,
+                        const int32_t *lens, const w4_block_table *table, w4_stream_t stream) {
+    const w4_status st = walk_ok(cache, table, lens);
+    if (st != W4_OK) return st;
+    if (!bounds || !aligned(bounds, 16) || tokens < 1) return W4_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0) return W4_ERR_CUDA;
+    return cuda_status(w4::launch_key_bounds(pool_of(cache, table), cache->format,
+                                             cache->head_dim, bounds, tokens, lens, sms,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4_status w4_block_scores(const w4_kv_cache *cache, const uint16_t *bounds, const w4_heads *q,
+                          int q_heads, int tokens, const int32_t *lens,
+                          const w4_block_table *table, float *scores, int columns,
+                          w4_stream_t stream) {
+    w4_status st = walk_ok(cache, table, lens);
+    if (st == W4_OK) st = queries_ok(cache, q, q_heads, tokens, table);
+    if (st != W4_OK) return st;
+    if (!bounds || !aligned(bounds, 16) || !scores || !aligned(scores, 4) ||
+        columns < table->width)
+        return W4_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0) return W4_ERR_CUDA;
+    const int group = q_heads / cache->kv_heads;
+    return cuda_status(w4::launch_block_scores(
+        pool_of(cache, table), cache->head_dim, bounds, heads_of(q), group, magic_of(group),
+        tokens, lens, scores, columns, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,275 @@
+// Blocks of the paged cache: bounds of their keys (w4_key_bounds) and what q . k
+// can be in them (w4_block_scores).
+#include "w4_device.cuh"
+#include "w4_kv_work.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kBlockWarps = 4;
+
+// Blocks of a sequence that hold its last tokens, and the first of them.
+struct Touched {
+    KvPool pool;
+    const int32_t *lens;
+    int tokens;
+
+    __device__ __forceinline__ int len(int b) const {
+        return cached_len(pool, lens, b, pool.width * pool.page_tokens);
+    }
+    __device__ __forceinline__ int first(int n) const {
+        return max(n - tokens, 0) / pool.page_tokens;
+    }
+    __device__ __forceinline__ int operator()(int b) const {
+        const int n = len(b);
+        return n ? (n - 1) / pool.page_tokens - first(n) + 1 : 0;
+    }
+};
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 16 neighbouring values of one key as they are stored.
+template <int FMT>
+struct Raw {
+    uint32_t w[FMT == W4_KV_BF16 ? 8 : FMT == W4_KV_INT8 ? 4 : 2];
+    uint32_t meta;
+};
+
+// A warp takes a block of a head: D / 16 lanes a key, 16 values each, so that
+// every load is 16 bytes (8 in 4 bits) of whole rows.
+template <int FMT, int D>
+__global__ void __launch_bounds__(32 * kBlockWarps)
+bounds_kernel(const Touched touched, uint32_t *bounds) {
+    using L = KvLayout<FMT, D>;
+    constexpr int LANES = D / 16, ROWS = 32 / LANES, LOADS = kRecTokens / ROWS;
+    begin_after_previous();
+    const KvPool &pool = touched.pool;
+    const int lane = threadIdx.x & 31, part = lane % LANES, row0 = lane / LANES;
+    Share s(touched, pool.seqs, pool.kv_heads, blockIdx.x * kBlockWarps + (threadIdx.x >> 5),
+            gridDim.x * kBlockWarps);
+    for (; s.left > 0; s.next(touched, pool.kv_heads)) {
+        const int len = touched.len(s.b), block = touched.first(len) + s.u;
+        const int page = pool.table[s.b * pool.stride + block];
+        const char *rec = page_records(pool, page, s.h, L::kBytes);
+        if (!rec) continue;
+        const int there = min(len - block * pool.page_tokens, pool.page_tokens);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hi[i] = 0xFF80FF80u, lo[i] = 0x7F807F80u;
+        for (int r0 = 0; r0 < there; r0 += kRecTokens, rec += L::kBytes) {
+            Raw<FMT> raw[LOADS];
+#pragma unroll
+            for (int x = 0; x < LOADS; ++x) {
+                const int r = row0 + x * ROWS;
+                if constexpr (FMT == W4_KV_BF16) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            rec + L::key(r, 16 * part + 8 * y));
+                        raw[x].w[4 * y] = v.x, raw[x].w[4 * y + 1] = v.y;
+                        raw[x].w[4 * y + 2] = v.z, raw[x].w[4 * y + 3] = v.w;
+                    }
+                } else {
+                    if constexpr (FMT == W4_KV_INT8) {
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(rec + L::key(r, 16 * part));
+                        raw[x].w[0] = v.x, raw[x].w[1] = v.y, raw[x].w[2] = v.z, raw[x].w[3] = v.w;
+                    } else {
+                        const uint2 v =
+                            *reinterpret_cast<const uint2 *>(rec + L::key(r, 16 * part));
+                        raw[x].w[0] = v.x, raw[x].w[1] = v.y;
+                    }
+                    raw[x].meta = *reinterpret_cast<const uint32_t *>(rec + L::kMeta + 4 * r);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < LOADS; ++x) {
+                if (r0 + row0 + x * ROWS >= there) continue;
+                uint32_t v[8];
+                if constexpr (FMT == W4_KV_BF16) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = raw[x].w[i];
+                } else {
+                    // (q - z) s is exact in fp32, and so is the difference below
+                    const float sc = __half2float(
+                        __ushort_as_half((unsigned short)(raw[x].meta & 0xFFFFu)));
+                    const float off = -(float)(raw[x].meta >> 16) * sc;
+                    const auto value = [&](int i) {
+                        const uint32_t q =
+                            FMT == W4_KV_INT8 ? raw[x].w[i >> 2] >> (8 * (i & 3)) & 255u
+                                              : raw[x].w[i >> 3] >> (4 * (i & 7)) & 15u;
+                        return fmaf((float)q, sc, off);
+                    };
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = bf16_pair(value(2 * i), value(2 * i + 1));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hi[i] = max2(hi[i], v[i]), lo[i] = min2(lo[i], v[i]);
+            }
+        }
+#pragma unroll
+        for (int x = LANES; x < 32; x <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                hi[i] = max2(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], x));
+                lo[i] = min2(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], x));
+            }
+        // the largest from the first lanes, the smallest from the next ones
+        if (row0 < 2) {
+            uint4 *out = reinterpret_cast<uint4 *>(
+                bounds + ((long long)page * pool.kv_heads + s.h) * D + row0 * (D / 2) + 8 * part);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                out[y] = row0 ? make_uint4(lo[4 * y], lo[4 * y + 1], lo[4 * y + 2], lo[4 * y + 3])
+                              : make_uint4(hi[4 * y], hi[4 * y + 1], hi[4 * y + 2], hi[4 * y + 3]);
+        }
+    }
+}
+
+// Tiles of 16 blocks of a sequence.
+struct Tiles {
+    KvPool pool;
+    const int32_t *lens;
+
+    __device__ __forceinline__ int len(int b) const {
+        return cached_len(pool, lens, b, pool.width * pool.page_tokens);
+    }
+    __device__ __forceinline__ int blocks(int len) const {
+        return (len + pool.page_tokens - 1) / pool.page_tokens;
+    }
+    __device__ __forceinline__ int operator()(int b) const { return (blocks(len(b)) + 15) / 16; }
+};
+
+// q+ . hi + q- . lo on the tensor cores: 16 blocks are the rows of a tile, 8 rows
+// of queries its columns, and the sum runs over 2 D values.  Which of them a
+// lane holds in which register does not matter as long as both sides agree, so
+// lane t takes the 16-byte pieces t, t + 4, ... of a row as they lie in memory.
+template <int D>
+__global__ void __launch_bounds__(32 * kBlockWarps)
+scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q, int group,
+              unsigned group_magic, int tokens, float *scores, int columns) {
+    constexpr int PIECES = D / 32;
+    begin_after_previous();
+    const KvPool &pool = tiles.pool;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rows = tokens * group;
+    Share s(tiles, pool.seqs, pool.kv_heads, blockIdx.x * kBlockWarps + (threadIdx.x >> 5),
+            gridDim.x * kBlockWarps);
+    for (; s.left > 0; s.next(tiles, pool.kv_heads)) {
+        const int len = tiles.len(s.b), blocks = tiles.blocks(len);
+        uint4 a[2][2][PIECES];                                // hi, lo of blocks g, g + 8
+        bool valid[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int block = 16 * s.u + g + 8 * y;
+            const int page = block < blocks ? pool.table[s.b * pool.stride + block] : -1;
+            valid[y] = page >= 0 && page < pool.pages;
+            if (block < blocks && !valid[y] && pool.error) atomicOr(pool.error, W4_KV_ERR_PAGE);
+            const uint4 *row =
+                bounds + ((long long)(valid[y] ? page : 0) * pool.kv_heads + s.h) * (D / 4) + t;
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int j = 0; j < PIECES; ++j)
+                    a[z][y][j] = valid[y] ? __ldg(row + z * (D / 8) + 4 * j)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float best[2] = {-INFINITY, -INFINITY};
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+            const int r = min(r0 + g, rows - 1);
+            const int i = group == 1 ? r : (int)__umulhi((unsigned)r, group_magic);
+            const uint4 *row = reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const __nv_bfloat16 *>(q.data) +
+                (long long)(s.b * tokens + i) * q.token_stride +
+                (long long)(s.h * group + r - i * group) * q.head_stride) + t;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+                const uint4 v = __ldg(row + 4 * j);
+                const uint4 up = make_uint4(max2(v.x, 0u), max2(v.y, 0u), max2(v.z, 0u),
+                                            max2(v.w, 0u));
+                const uint4 down = make_uint4(min2(v.x, 0u), min2(v.y, 0u), min2(v.z, 0u),
+                                              min2(v.w, 0u));
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const uint4 &k0 = a[z][0][j], &k1 = a[z][1][j], &b = z ? down : up;
+                    mma_bf16_16816(d, k0.x, k1.x, k0.y, k1.y, b.x, b.y);
+                    mma_bf16_16816(d, k0.z, k1.z, k0.w, k1.w, b.z, b.w);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // (columns past the last row repeat it)
+                const int rc = min(r0 + 2 * t + (c & 1), rows - 1);
+                const int ic = group == 1 ? rc : (int)__umulhi((unsigned)rc, group_magic);
+                const float v = fabsf(d[c]) < INFINITY ? d[c] : INFINITY;
+                if (len - tokens + ic >= 0) best[c >> 1] = fmaxf(best[c >> 1], v);
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            best[y] = fmaxf(best[y], __shfl_xor_sync(0xFFFFFFFFu, best[y], 1));
+            best[y] = fmaxf(best[y], __shfl_xor_sync(0xFFFFFFFFu, best[y], 2));
+            const int block = 16 * s.u + g + 8 * y;
+            if (t == 0 && block < blocks)
+                scores[((long long)s.b * pool.kv_heads + s.h) * columns + block] =
+                    valid[y] ? best[y] : -INFINITY;
+        }
+    }
+}
+
+// Blocks of warps for at most `units` units, a few waves of the device.
+int grid_of(long long units, int num_sms) {
+    const long long blocks = (units + kBlockWarps - 1) / kBlockWarps, most = 8LL * num_sms;
+    return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+cudaError_t launch_key_bounds(const KvPool &pool, int format, int head_dim, void *bounds,
+                              int tokens, const int32_t *lens, int num_sms,
+                              cudaStream_t stream) {
+    const Touched touched = {pool, lens, tokens};
+    const long long reach = ((long long)tokens + pool.page_tokens - 2) / pool.page_tokens + 1;
+    const int grid = grid_of(
+        (reach < pool.width ? reach : pool.width) * pool.seqs * pool.kv_heads, num_sms);
+    const auto run = [&](auto kernel) {
+        return launch_overlapped(kernel, dim3(grid), dim3(32 * kBlockWarps), 0, stream, touched,
+                                 static_cast<uint32_t *>(bounds));
+    };
+    if (head_dim == 128)
+        return format == W4_KV_BF16   ? run(bounds_kernel<W4_KV_BF16, 128>)
+               : format == W4_KV_INT8 ? run(bounds_kernel<W4_KV_INT8, 128>)
+                                      : run(bounds_kernel<W4_KV_INT4, 128>);
+    return format == W4_KV_BF16   ? run(bounds_kernel<W4_KV_BF16, 64>)
+           : format == W4_KV_INT8 ? run(bounds_kernel<W4_KV_INT8, 64>)
+                                  : run(bounds_kernel<W4_KV_INT4, 64>);
+}
+
+cudaError_t launch_block_scores(const KvPool &pool, int head_dim, const void *bounds,
+                                const Heads &q, int group, unsigned group_magic, int tokens,
+                                const int32_t *lens, float *scores, int columns, int num_sms,
+                                cudaStream_t stream) {
+    const Tiles tiles = {pool, lens};
+    const int grid =
+        grid_of((pool.width + 15LL) / 16 * pool.seqs * pool.kv_heads, num_sms);
+    const uint4 *b = static_cast<const uint4 *>(bounds);
+    return head_dim == 128
+               ? launch_overlapped(scores_kernel<128>, dim3(grid), dim3(32 * kBlockWarps), 0,
+                                   stream, tiles, b, q, group, group_magic, tokens, scores,
+                                   columns)
+               : launch_overlapped(scores_kernel<64>, dim3(grid), dim3(32 * kBlockWarps), 0,
+                                   stream, tiles, b, q, group, group_magic, tokens, scores,
+                                   columns);
+}
+
+}  // namespace w4

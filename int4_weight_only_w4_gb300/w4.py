@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import enum
+import math
 import os
 import struct
 from dataclasses import dataclass
@@ -416,6 +417,7 @@ KV_ERR_PAGE = 2           # W4_KV_ERR_PAGE
 KV_ERR_SEQUENCE = 4       # W4_KV_ERR_SEQUENCE
 KV_ERR_LENGTH = 8         # W4_KV_ERR_LENGTH
 KV_ERR_WAIT = 16          # W4_KV_ERR_WAIT
+KV_ERR_BLOCK = 32         # W4_KV_ERR_BLOCK
 RECORD_TOKENS = 16        # tokens of a cache record; page sizes are multiples of it
 
 _I64 = ctypes.c_int64
@@ -450,6 +452,8 @@ _paged_attn_workspace_bytes = _decl("w4_paged_attn_workspace_bytes", _ST, _P,
 _ATTN_ARGS = (_P, _P, _P, _I, _I, _P, _P, ctypes.c_float, _I, _P, _P, ctypes.c_size_t, _P)
 _paged_attn = _decl("w4_paged_attn", _ST, *_ATTN_ARGS)
 _paged_attn_f32 = _decl("w4_paged_attn_f32", _ST, *_ATTN_ARGS)
+_key_bounds = _decl("w4_key_bounds", _ST, _P, _P, _I, _P, _P, _P)
+_block_scores = _decl("w4_block_scores", _ST, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P)
 
 
 def _heads(t, dtype=torch.bfloat16) -> bytes | None:
@@ -610,6 +614,46 @@ def paged_attn_f32(cache: "PagedCache", q, out, lens, table, workspace, scale=No
           window, lse, (_ptr(workspace), workspace.nbytes), _raw_stream(stream, q))
 
 
+def _filled(t, shape, dtype, what: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape and type."""
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or \
+            not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} CUDA tensor {list(shape)}")
+    return t.data_ptr()
+
+
+def _new_tokens(cache: "PagedCache", q, table) -> tuple:
+    """(q_heads, new tokens of a sequence) of the queries of a call."""
+    T, H, D = q.shape
+    B = table.shape[0]
+    if not B or T % B or D != cache.head_dim:
+        raise ValueError("q: expected [seqs * tokens, q_heads, head_dim]")
+    return H, T // B
+
+
+def key_bounds(cache: "PagedCache", bounds, lens, table, tokens: int = 1, stream=None) -> None:
+    """w4_key_bounds: the largest and the smallest key values, bfloat16 [pages,
+    kv_heads, 2, head_dim], of the blocks that the last `tokens` tokens of every
+    sequence lie in."""
+    _ok(_key_bounds(cache.ref, _filled(bounds, cache.bounds_shape, torch.bfloat16, "bounds"),
+                    tokens, _int32(lens, table.shape[0], "lens"), _block_table(table),
+                    _raw_stream(stream, bounds)), "w4_key_bounds")
+
+
+def block_scores(cache: "PagedCache", bounds, q, lens, table, scores, stream=None) -> None:
+    """w4_block_scores: how large q . k can be in every block of a sequence,
+    float32 [seqs, kv_heads, columns]."""
+    H, M = _new_tokens(cache, q, table)
+    B = table.shape[0]
+    if scores.dim() != 3:
+        raise ValueError("scores: expected float32 [seqs, kv_heads, columns]")
+    columns = scores.shape[2]
+    _ok(_block_scores(cache.ref, _filled(bounds, cache.bounds_shape, torch.bfloat16, "bounds"),
+                      _heads(q), H, M, _int32(lens, B, "lens"), _block_table(table),
+                      _filled(scores, (B, cache.kv_heads, columns), torch.float32, "scores"),
+                      columns, _raw_stream(stream, q)), "w4_block_scores")
+
+
 class RopeTable:
     """A table of rotations: float32 [rows, rotary_dim/2, 2] (cos, sin) pairs
     on the device, and which values of a head form a pair."""
@@ -662,6 +706,7 @@ class PagedCache:
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.head_shape = (kv_heads, head_dim)
         self.pages = nbytes // per_page
+        self.bounds_shape = (self.pages, kv_heads, 2, head_dim)
         self.error = torch.zeros(1, dtype=torch.int32, device=pool.device) if error is None \
             else error
         self._struct = _KvCache(_ptr(pool), fmt, kv_heads, head_dim, page_tokens, self.pages,
@@ -751,6 +796,26 @@ class PagedCache:
         _attn(_paged_attn, "w4_paged_attn", torch.bfloat16, self, q, out, lens, table, scale,
               window, lse, kept[0], raw)
         return out, lse
+
+    def new_bounds(self) -> torch.Tensor:
+        """Bounds of the keys of all pages, for key_bounds() to fill."""
+        return torch.zeros(self.bounds_shape, dtype=torch.bfloat16, device=self.pool.device)
+
+    def key_bounds(self, bounds, lens, table, tokens: int = 1, stream=None) -> torch.Tensor:
+        """Bring `bounds` (see new_bounds) up to date for the blocks that the last
+        `tokens` tokens of every sequence lie in."""
+        key_bounds(self, bounds, lens, table, tokens, stream)
+        return bounds
+
+    def block_scores(self, bounds, q, lens, table, scores=None, stream=None) -> torch.Tensor:
+        """How large q . k can be in every block; [seqs, kv_heads, width] (default: a
+        new tensor, made on `stream`; -inf past a sequence's blocks)."""
+        if scores is None:
+            with _on(stream, q.device):
+                scores = torch.full((table.shape[0], self.kv_heads, table.shape[1]), -math.inf,
+                                    dtype=torch.float32, device=q.device)
+        block_scores(self, bounds, q, lens, table, scores, stream)
+        return scores
 
     def check(self) -> None:
         """Raise W4Error if a call recorded an error, and clear it.  Waits for

@@ -1,0 +1,46 @@
+"""Host-side checks of the calls for long contexts that need no GPU: argument
+errors (every call here fails validation, so no pointer is looked at)."""
+import pytest
+
+from tests.test_abi_host import FAKE, lib  # noqa: F401
+from tests.test_kv_host import I, P, cache, heads, ref, table
+
+
+def bounds(lib, c=cache(), out=FAKE, tokens=1, lens=FAKE, t=table()):  # noqa: F811
+    lib.w4_key_bounds.argtypes = [P, P, I, P, P, P]
+    return lib.w4_key_bounds(ref(c), out, tokens, lens, ref(t), None)
+
+
+def scores(lib, c=cache(), b=FAKE, q=heads(), hq=2, tokens=1, lens=FAKE, t=table(),  # noqa: F811
+           out=FAKE, columns=4):
+    lib.w4_block_scores.argtypes = [P, P, P, I, I, P, P, P, I, P]
+    return lib.w4_block_scores(ref(c), b, ref(q), hq, tokens, lens, ref(t), out, columns, None)
+
+
+WALK = [(dict(c=None), 1), (dict(c=cache(pool=None)), 1), (dict(c=cache(pool=FAKE + 64)), 1),
+        (dict(c=cache(error=FAKE + 1)), 1), (dict(c=cache(format=3)), 1),
+        (dict(c=cache(head_dim=96)), 2), (dict(c=cache(page_tokens=24)), 1), (dict(lens=None), 1),
+        (dict(lens=FAKE + 2), 1), (dict(t=None), 1), (dict(t=table(None)), 1),
+        (dict(t=table(seqs=0)), 1), (dict(t=table(width=0)), 1), (dict(t=table(stride=3)), 1),
+        (dict(t=table(width=1 << 27, stride=1 << 27)), 2),
+        (dict(t=table(seqs=1 << 30, width=1, stride=1)), 2),
+        (dict(t=table(seqs=1 << 28, width=4)), 2)]
+QUERIES = [(dict(q=None), 1), (dict(q=heads(None)), 1), (dict(q=heads(FAKE + 2)), 1),
+           (dict(q=heads(token=129)), 1), (dict(q=heads(head=60)), 1), (dict(tokens=0), 2),
+           (dict(tokens=9), 2), (dict(hq=0), 1), (dict(hq=3), 1), (dict(hq=2 * 4097), 2)]
+
+
+@pytest.mark.parametrize("kw,want", WALK + [(dict(out=None), 1), (dict(out=FAKE + 8), 1),
+                                            (dict(tokens=0), 1), (dict(tokens=-1), 1)])
+def test_key_bounds_errors(lib, kw, want):  # noqa: F811
+    assert bounds(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", WALK + QUERIES + [
+    (dict(b=None), 1), (dict(b=FAKE + 8), 1), (dict(out=None), 1), (dict(out=FAKE + 2), 1),
+    (dict(columns=3), 1)])
+def test_block_scores_errors(lib, kw, want):  # noqa: F811
+    kw = dict(kw)
+    if kw.get("t") is not None and kw["t"].width > 4:
+        kw["columns"] = 1 << 30
+    assert scores(lib, **kw) == want
