@@ -717,6 +717,27 @@ w4_status w4_block_scores(const w4_kv_cache *cache, const uint16_t *bounds, cons
                           const w4_block_table *table, float *scores, int columns,
                           w4_stream_t stream);
 
+/*
+ * The best `count` items of every row, in ascending order: row (b, h) has
+ * n = ceil(lens[b] / unit) items (`columns` at most) with a score each.  The first
+ * `first` and the last `last` items are always chosen, then those with the
+ * largest scores, of equal ones (0 and -0 are) the first; NaN counts as larger
+ * than any number.  With n <= count all are chosen.
+ *   index[b][h][i], i < counts[b] = min(n, count): the chosen items
+ * Entries from counts[b] on are left as they were.
+ *   scores : device float [seqs][heads][columns]
+ *   lens   : device int32 [seqs]; negative counts as 0
+ *   unit   : >= 1: page_tokens where items are blocks, 1 where they are tokens
+ *   first, last : >= 0;  count : >= 1, at least first + last
+ *   index  : device int32 [seqs][heads][count];  counts : device int32 [seqs]
+ * index and counts must not overlap what is read.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (2^27 or more rows, 2^30 or
+ * more columns), W4_ERR_CUDA.
+ */
+w4_status w4_select(const float *scores, int seqs, int heads, int columns, const int32_t *lens,
+                    int unit, int first, int last, int count, int32_t *index, int32_t *counts,
+                    w4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -120,6 +120,10 @@ cudaError_t launch_block_scores(const KvPool &pool, int head_dim, const void *bo
                                 const int32_t *lens, float *scores, int columns, int num_sms,
                                 cudaStream_t stream);
 
+cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
+                          const int32_t *lens, int unit, int first, int last, int count,
+                          int32_t *index, int32_t *counts, cudaStream_t stream);
+
 // Launch with programmatic stream serialisation: the grid may start while the
 // previous kernel of the stream drains; every kernel launched this way calls
 // griddepcontrol.wait before it touches memory that another kernel writes.

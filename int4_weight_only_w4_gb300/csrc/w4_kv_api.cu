@@ -363,4 +363,19 @@ w4_status w4_block_scores(const w4_kv_cache *cache, const uint16_t *bounds, cons
         tokens, lens, scores, columns, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+w4_status w4_select(const float *scores, int seqs, int heads, int columns, const int32_t *lens,
+                    int unit, int first, int last, int count, int32_t *index, int32_t *counts,
+                    w4_stream_t stream) {
+    if (seqs < 1 || heads < 1 || columns < 1 || unit < 1 || first < 0 || last < 0 || count < 1 ||
+        (long long)first + last > count)
+        return W4_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(scores), static_cast<const void *>(lens),
+                          static_cast<const void *>(index), static_cast<const void *>(counts)})
+        if (!p || !aligned(p, 4)) return W4_ERR_INVALID_ARG;
+    if ((long long)seqs * heads >= (1LL << 27) || columns >= (1 << 30)) return W4_ERR_UNSUPPORTED;
+    return cuda_status(w4::launch_select(scores, seqs, heads, columns, lens, unit, first, last,
+                                         count, index, counts,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

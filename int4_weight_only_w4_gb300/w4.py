@@ -454,6 +454,7 @@ _paged_attn = _decl("w4_paged_attn", _ST, *_ATTN_ARGS)
 _paged_attn_f32 = _decl("w4_paged_attn_f32", _ST, *_ATTN_ARGS)
 _key_bounds = _decl("w4_key_bounds", _ST, _P, _P, _I, _P, _P, _P)
 _block_scores = _decl("w4_block_scores", _ST, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P)
+_select = _decl("w4_select", _ST, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P)
 
 
 def _heads(t, dtype=torch.bfloat16) -> bytes | None:
@@ -652,6 +653,22 @@ def block_scores(cache: "PagedCache", bounds, q, lens, table, scores, stream=Non
                       _heads(q), H, M, _int32(lens, B, "lens"), _block_table(table),
                       _filled(scores, (B, cache.kv_heads, columns), torch.float32, "scores"),
                       columns, _raw_stream(stream, q)), "w4_block_scores")
+
+
+def select(scores, lens, index, counts, unit: int = 1, first: int = 0, last: int = 0,
+           stream=None) -> None:
+    """w4_select: of the ceil(lens[b] / unit) items of every row of scores, float32
+    [seqs, heads, columns], the first `first`, the last `last` and the best others,
+    as many as a row of index has (int32 [seqs, heads, count]), ascending; how many
+    there are goes into counts, int32 [seqs]."""
+    if scores.dim() != 3 or index.dim() != 3:
+        raise ValueError("scores, index: expected [seqs, heads, columns] and [seqs, heads, count]")
+    B, H, columns = scores.shape
+    count = index.shape[2]
+    _ok(_select(_filled(scores, (B, H, columns), torch.float32, "scores"), B, H, columns,
+                _int32(lens, B, "lens"), unit, first, last, count,
+                _filled(index, (B, H, count), torch.int32, "index"),
+                _int32(counts, B, "counts"), _raw_stream(stream, scores)), "w4_select")
 
 
 class RopeTable:

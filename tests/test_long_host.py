@@ -44,3 +44,22 @@ def test_block_scores_errors(lib, kw, want):  # noqa: F811
     if kw.get("t") is not None and kw["t"].width > 4:
         kw["columns"] = 1 << 30
     assert scores(lib, **kw) == want
+
+
+def select(lib, scores=FAKE, seqs=2, heads=2, columns=9, lens=FAKE, unit=1, first=0,  # noqa: F811
+           last=0, count=4, index=FAKE, counts=FAKE):
+    lib.w4_select.argtypes = [P, I, I, I, P, I, I, I, I, P, P, P]
+    return lib.w4_select(scores, seqs, heads, columns, lens, unit, first, last, count, index,
+                         counts, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(scores=None), 1), (dict(scores=FAKE + 2), 1), (dict(lens=None), 1),
+    (dict(lens=FAKE + 1), 1), (dict(index=None), 1), (dict(index=FAKE + 3), 1),
+    (dict(counts=None), 1), (dict(counts=FAKE + 2), 1), (dict(seqs=0), 1), (dict(heads=0), 1),
+    (dict(columns=0), 1), (dict(unit=0), 1), (dict(first=-1), 1), (dict(last=-1), 1),
+    (dict(count=0), 1), (dict(first=3, last=2), 1),
+    (dict(first=(1 << 31) - 1, last=(1 << 31) - 1), 1), (dict(seqs=1 << 26), 2),
+    (dict(columns=1 << 30), 2)])
+def test_select_errors(lib, kw, want):  # noqa: F811
+    assert select(lib, **kw) == want
