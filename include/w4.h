@@ -738,6 +738,31 @@ w4_status w4_select(const float *scores, int seqs, int heads, int columns, const
                     int unit, int first, int last, int count, int32_t *index, int32_t *counts,
                     w4_stream_t stream);
 
+/*
+ * w4_paged_attn over listed blocks only: new token i sees the keys of the blocks
+ * blocks[b][h][0 .. counts[b] - 1] at its own position p = lens[b] - tokens + i
+ * and before.  All of them ascending, it gives what w4_paged_attn gives, up to
+ * the order of sums.  The sums' order depends on the lengths, the lists and the
+ * device only.
+ *   blocks : device int32 [seqs][kv_heads][most], ascending; an entry that is not
+ *            above the one before it, or no block of the sequence, is left out
+ *            (W4_KV_ERR_BLOCK)
+ *   counts : device int32 [seqs]; taken as 0 below it, as most above it
+ *   most   : >= 1
+ * The other arguments, a row that sees no key, and the errors are those of
+ * w4_paged_attn, the workspace too.
+ */
+w4_status w4_sparse_attn(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                         int q_heads, int tokens, const int32_t *lens,
+                         const w4_block_table *table, const int32_t *blocks,
+                         const int32_t *counts, int most, float scale, float *lse,
+                         void *workspace, size_t workspace_bytes, w4_stream_t stream);
+w4_status w4_sparse_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                             int q_heads, int tokens, const int32_t *lens,
+                             const w4_block_table *table, const int32_t *blocks,
+                             const int32_t *counts, int most, float scale, float *lse,
+                             void *workspace, size_t workspace_bytes, w4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -107,6 +107,9 @@ struct AttnArgs {
     int tokens;      // new tokens per sequence
     float scale;
     int window;      // 0: none
+    const int32_t *blocks;    // the blocks to look at, `most` a head, or NULL: all
+    const int32_t *counts;    // how many of them, by sequence
+    int most;
     void *workspace;
 };
 size_t attn_workspace_bytes(int head_dim, int num_sms);

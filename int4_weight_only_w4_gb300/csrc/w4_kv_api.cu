@@ -124,7 +124,8 @@ unsigned magic_of(int group) { return group > 1 ? 0xFFFFFFFFu / (unsigned)group 
 
 w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
                             int q_heads, int tokens, const int32_t *lens,
-                            const w4_block_table *table, float scale, int window, float *lse,
+                            const w4_block_table *table, const int32_t *blocks,
+                            const int32_t *counts, int most, float scale, int window, float *lse,
                             void *workspace, size_t workspace_bytes, bool f32_out,
                             w4_stream_t stream) {
     const w4_status st = cache_ok(cache, true);
@@ -145,7 +146,8 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     // 128 records more)
     const long long row_tiles = ((long long)tokens * (q_heads / cache->kv_heads) + 63) / 64;
     const long long longest =
-        (long long)table->width * (cache->page_tokens / w4::kRecTokens) + 128;
+        (long long)(blocks && most > table->width ? most : table->width) *
+            (cache->page_tokens / w4::kRecTokens) + 128;
     if (longest * table->seqs >= (1LL << 31) ||
         longest * table->seqs * cache->kv_heads >= (1LL << 31) ||
         longest * table->seqs * cache->kv_heads * row_tiles >= (1LL << 31))
@@ -169,9 +171,24 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     // a window as wide as the longest sequence leaves nothing out (and so the
     // kernels may subtract one from a position of a token that is not there)
     a.window = window < table->width * cache->page_tokens ? window : 0;
+    a.blocks = blocks;
+    a.counts = counts;
+    a.most = most;
     a.workspace = workspace;
     return cuda_status(w4::launch_paged_attn(a, cache->format, cache->head_dim, sms,
                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4_status sparse_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                             int q_heads, int tokens, const int32_t *lens,
+                             const w4_block_table *table, const int32_t *blocks,
+                             const int32_t *counts, int most, float scale, float *lse,
+                             void *workspace, size_t workspace_bytes, bool f32_out,
+                             w4_stream_t stream) {
+    if (!blocks || !counts || !aligned(blocks, 4) || !aligned(counts, 4) || most < 1)
+        return W4_ERR_INVALID_ARG;
+    return paged_attn_common(cache, q, out, q_heads, tokens, lens, table, blocks, counts, most,
+                             scale, 0, lse, workspace, workspace_bytes, f32_out, stream);
 }
 
 }  // namespace
@@ -321,16 +338,16 @@ w4_status w4_paged_attn(const w4_kv_cache *cache, const w4_heads *q, const w4_he
                         int q_heads, int tokens, const int32_t *lens,
                         const w4_block_table *table, float scale, int window, float *lse,
                         void *workspace, size_t workspace_bytes, w4_stream_t stream) {
-    return paged_attn_common(cache, q, out, q_heads, tokens, lens, table, scale, window, lse,
-                             workspace, workspace_bytes, false, stream);
+    return paged_attn_common(cache, q, out, q_heads, tokens, lens, table, nullptr, nullptr, 0,
+                             scale, window, lse, workspace, workspace_bytes, false, stream);
 }
 
 w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
                             int q_heads, int tokens, const int32_t *lens,
                             const w4_block_table *table, float scale, int window, float *lse,
                             void *workspace, size_t workspace_bytes, w4_stream_t stream) {
-    return paged_attn_common(cache, q, out, q_heads, tokens, lens, table, scale, window, lse,
-                             workspace, workspace_bytes, true, stream);
+    return paged_attn_common(cache, q, out, q_heads, tokens, lens, table, nullptr, nullptr, 0,
+                             scale, window, lse, workspace, workspace_bytes, true, stream);
 }
 
 w4_status w4_key_bounds(const w4_kv_cache *cache, uint16_t *bounds, int tokens,
@@ -376,6 +393,24 @@ w4_status w4_select(const float *scores, int seqs, int heads, int columns, const
     return cuda_status(w4::launch_select(scores, seqs, heads, columns, lens, unit, first, last,
                                          count, index, counts,
                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4_status w4_sparse_attn(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                         int q_heads, int tokens, const int32_t *lens,
+                         const w4_block_table *table, const int32_t *blocks,
+                         const int32_t *counts, int most, float scale, float *lse,
+                         void *workspace, size_t workspace_bytes, w4_stream_t stream) {
+    return sparse_attn_common(cache, q, out, q_heads, tokens, lens, table, blocks, counts, most,
+                              scale, lse, workspace, workspace_bytes, false, stream);
+}
+
+w4_status w4_sparse_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
+                             int q_heads, int tokens, const int32_t *lens,
+                             const w4_block_table *table, const int32_t *blocks,
+                             const int32_t *counts, int most, float scale, float *lse,
+                             void *workspace, size_t workspace_bytes, w4_stream_t stream) {
+    return sparse_attn_common(cache, q, out, q_heads, tokens, lens, table, blocks, counts, most,
+                              scale, lse, workspace, workspace_bytes, true, stream);
 }
 
 }  // extern "C"

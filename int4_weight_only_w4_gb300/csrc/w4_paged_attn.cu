@@ -140,12 +140,21 @@ __device__ __forceinline__ int token_of_row(const AttnArgs &a, int row) {
     return a.group == 1 ? row : (int)__umulhi((unsigned)row, a.group_magic);
 }
 
+// LISTED: of the listed blocks' records (the last block's past its end too).
+template <bool LISTED>
 __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
     int len = max(a.lens[b], 0);
     const int room = a.pool.width * a.pool.page_tokens;
     if (len > room) {
         if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_LENGTH);
         len = room;
+    }
+    if constexpr (LISTED) {
+        Seq s;
+        s.len = len, s.first = 0;
+        const int listed = min(max(a.counts[b], 0), a.most);
+        s.records = len ? listed * a.pool.page_records : 0;
+        return s;
     }
     return seen_records(len, a.tokens, a.window);
 }
@@ -643,11 +652,12 @@ __device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &v) 
 
 // The list, as a warp sees it: lane i holds sequences [b0, b1), whose items
 // cost [before, before + mine) * per_seq.
+template <bool LISTED>
 struct List : Division {
     int b0, b1, before, mine;
 
     __device__ __forceinline__ int records(const AttnArgs &a, int b) const {
-        return sequence(a, b).records;
+        return sequence<LISTED>(a, b).records;
     }
 
     __device__ __forceinline__ List(const AttnArgs &a, const Plan &plan) {
@@ -778,7 +788,7 @@ struct Piece {
 
 // The copying warps: lane i of warp w fills the ring of group 2 i + w.  Two of
 // them, because a copy costs its warp about 100 cycles.
-template <int FMT, int D, int WARPS>
+template <int FMT, int D, int WARPS, bool LISTED>
 __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan, int block_rows,
                                              unsigned char *smem, uint64_t *full, uint64_t *empty,
                                              int *first_key, Piece *piece, uint64_t *piece_full,
@@ -786,7 +796,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     using L = KvLayout<FMT, D>;
     const int lane = threadIdx.x & 31, KG = plan.KG, stages = plan.stages;
     const int copier = (threadIdx.x >> 5) - WARPS, kg = kCopyWarps * lane + copier;
-    const List list(a, plan);
+    const List<LISTED> list(a, plan);
     Cut c, to;
     c.b = 0, c.item = 0, c.u = 0;
     to = c;
@@ -801,15 +811,28 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     unsigned char *ring = smem + kg * stages * L::kBytes;
     while (true) {
         const bool more = has_more(c, to, a.pool.seqs);
-        const Seq seq = sequence(a, more ? c.b : 0);
+        const Seq seq = sequence<LISTED>(a, more ? c.b : 0);
         const bool last = c.b == to.b && c.item == to.item;
         const int stop = last ? to.u : seq.records;
         const int h = c.item / plan.row_tiles;
         const int32_t *pages = a.pool.table + (more ? c.b : 0) * a.pool.stride;
         constexpr int AHEAD = 4;
-        int page[AHEAD];
+        int page[AHEAD], block[LISTED ? AHEAD : 1];
+        const int32_t *blocks = nullptr;
+        if constexpr (LISTED)
+            blocks = a.blocks + ((long long)(more ? c.b : 0) * a.pool.kv_heads + h) * a.most;
         const auto fetch = [&](int x, int u) {
-            page[x] = u < stop && kg < KG ? pages[page_slot(a.pool, seq.first + u)] : 0;
+            if constexpr (LISTED) {
+                block[x] = -1, page[x] = -1;
+                if (u < stop && kg < KG) {
+                    const int slot = page_slot(a.pool, u), k = blocks[slot];
+                    const int last = slot > 0 ? blocks[slot - 1] : -1;
+                    if (k > last && k >= 0 && (long long)k * a.pool.page_tokens < seq.len)
+                        block[x] = k, page[x] = pages[k];
+                }
+            } else {
+                page[x] = u < stop && kg < KG ? pages[page_slot(a.pool, seq.first + u)] : 0;
+            }
         };
         if (more) {
 #pragma unroll
@@ -848,7 +871,11 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
         for (int u0 = c.u; u0 < stop; u0 += AHEAD * KG)
 #pragma unroll
             for (int x = 0; x < AHEAD; ++x) {
-                const int u = u0 + kg + x * KG, r = seq.first + u, pg = page[x];
+                const int u = u0 + kg + x * KG, pg = page[x];
+                // record of the sequence and of its page
+                int r = seq.first + u, in_page = r - page_slot(a.pool, r) * a.pool.page_records;
+                const int listed = LISTED ? block[x] : 0;
+                if constexpr (LISTED) r = listed * a.pool.page_records + in_page;
                 fetch(x, u + AHEAD * KG);
                 const bool mine = kg < KG && u < stop && ok;
                 // the lanes leave the wait one by one: without the barrier
@@ -857,17 +884,21 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
                 __syncwarp();
                 if (mine && ok) {
                     fence_proxy_async();
-                    const bool valid = pg >= 0 && pg < a.pool.pages;
+                    const bool known = pg >= 0 && pg < a.pool.pages;
+                    // (records of the last listed block may lie past its end)
+                    const bool valid = known && (!LISTED || r * kRecTokens < seq.len);
                     first_key[kg * stages + put] = valid ? r * kRecTokens : kAbsent;
                     if (valid) {
                         const char *src =
                             a.pool.records +
-                            (((long long)pg * a.pool.kv_heads + h) * a.pool.page_records + r -
-                             page_slot(a.pool, r) * a.pool.page_records) * L::kBytes;
+                            (((long long)pg * a.pool.kv_heads + h) * a.pool.page_records +
+                             in_page) * L::kBytes;
                         mbar_expect_tx(&my_full[put], L::kBytes);
                         bulk_g2s(ring + put * L::kBytes, src, L::kBytes, &my_full[put]);
                     } else {
-                        if (a.pool.error) atomicOr(a.pool.error, W4_KV_ERR_PAGE);
+                        if (a.pool.error && !known)
+                            atomicOr(a.pool.error, LISTED && listed < 0 ? W4_KV_ERR_BLOCK
+                                                                        : W4_KV_ERR_PAGE);
                         mbar_arrive(&my_full[put]);
                     }
                     used = min(used + 1, stages);
@@ -892,7 +923,7 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
     }
 }
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, bool LISTED>
 __global__ void __launch_bounds__(32 * (compute_warps(D, NT) + kCopyWarps), 1)
 attn_kernel(const AttnArgs a, const Plan plan) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -919,8 +950,8 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     __syncthreads();
     begin_after_previous();
     if (warp >= WARPS) {
-        copy_records<FMT, D, WARPS>(a, plan, block_rows, smem, full, empty, first_key, piece,
-                                    piece_full, piece_empty);
+        copy_records<FMT, D, WARPS, LISTED>(a, plan, block_rows, smem, full, empty, first_key,
+                                            piece, piece_full, piece_empty);
         return;
     }
 
@@ -1016,7 +1047,7 @@ attn_kernel(const AttnArgs a, const Plan plan) {
     }
 }
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, bool LISTED>
 cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     constexpr int bytes = KvLayout<FMT, D>::kBytes, WARPS = compute_warps(D, NT);
     static std::atomic<bool> ready[64] = {};
@@ -1024,7 +1055,7 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(attn_kernel<FMT, D, NT>,
+        e = cudaFuncSetAttribute(attn_kernel<FMT, D, NT, LISTED>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
@@ -1032,11 +1063,11 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
     const int rows = a.tokens * a.group;
     const Plan p = plan_of(D, NT, rows, bytes);
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    e = launch_overlapped(attn_kernel<FMT, D, NT>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
+    e = launch_overlapped(attn_kernel<FMT, D, NT, LISTED>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
                           kSharedBytes, stream, a, p);
     if (e != cudaSuccess) return e;
     if (nothing_to_join(p, a.pool.seqs, a.pool.kv_heads,
-                        (long long)a.pool.width * a.pool.page_records, grid))
+                        (long long)(LISTED ? a.most : a.pool.width) * a.pool.page_records, grid))
         return cudaSuccess;
     const int block_rows = 8 * NT * p.QG;
     constexpr int FEW = 2, MANY = 512 / D;                    // rows of a joining block
@@ -1048,10 +1079,18 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
                              dim3(256), 0, stream, a, block_rows);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool LISTED>
 cudaError_t launch_rows(const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    return tiles_a_warp(D, a.tokens * a.group) == 2 ? launch<FMT, D, 2>(a, num_sms, stream)
-                                                    : launch<FMT, D, 1>(a, num_sms, stream);
+    return tiles_a_warp(D, a.tokens * a.group) == 2
+               ? launch<FMT, D, 2, LISTED>(a, num_sms, stream)
+               : launch<FMT, D, 1, LISTED>(a, num_sms, stream);
+}
+
+template <int D, bool LISTED>
+cudaError_t launch_format(const AttnArgs &a, int format, int num_sms, cudaStream_t stream) {
+    return format == W4_KV_BF16   ? launch_rows<W4_KV_BF16, D, LISTED>(a, num_sms, stream)
+           : format == W4_KV_INT8 ? launch_rows<W4_KV_INT8, D, LISTED>(a, num_sms, stream)
+                                  : launch_rows<W4_KV_INT4, D, LISTED>(a, num_sms, stream);
 }
 
 }  // namespace
@@ -1063,13 +1102,11 @@ size_t attn_workspace_bytes(int head_dim, int num_sms) {
 
 cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, int num_sms,
                               cudaStream_t stream) {
-    if (head_dim == 128)
-        return format == W4_KV_BF16   ? launch_rows<W4_KV_BF16, 128>(a, num_sms, stream)
-               : format == W4_KV_INT8 ? launch_rows<W4_KV_INT8, 128>(a, num_sms, stream)
-                                      : launch_rows<W4_KV_INT4, 128>(a, num_sms, stream);
-    return format == W4_KV_BF16   ? launch_rows<W4_KV_BF16, 64>(a, num_sms, stream)
-           : format == W4_KV_INT8 ? launch_rows<W4_KV_INT8, 64>(a, num_sms, stream)
-                                  : launch_rows<W4_KV_INT4, 64>(a, num_sms, stream);
+    if (a.blocks)
+        return head_dim == 128 ? launch_format<128, true>(a, format, num_sms, stream)
+                               : launch_format<64, true>(a, format, num_sms, stream);
+    return head_dim == 128 ? launch_format<128, false>(a, format, num_sms, stream)
+                           : launch_format<64, false>(a, format, num_sms, stream);
 }
 
 }  // namespace w4

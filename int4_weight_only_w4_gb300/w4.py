@@ -452,6 +452,10 @@ _paged_attn_workspace_bytes = _decl("w4_paged_attn_workspace_bytes", _ST, _P,
 _ATTN_ARGS = (_P, _P, _P, _I, _I, _P, _P, ctypes.c_float, _I, _P, _P, ctypes.c_size_t, _P)
 _paged_attn = _decl("w4_paged_attn", _ST, *_ATTN_ARGS)
 _paged_attn_f32 = _decl("w4_paged_attn_f32", _ST, *_ATTN_ARGS)
+_SPARSE_ARGS = (_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, ctypes.c_float, _P, _P, ctypes.c_size_t,
+                _P)
+_sparse_attn = _decl("w4_sparse_attn", _ST, *_SPARSE_ARGS)
+_sparse_attn_f32 = _decl("w4_sparse_attn_f32", _ST, *_SPARSE_ARGS)
 _key_bounds = _decl("w4_key_bounds", _ST, _P, _P, _I, _P, _P, _P)
 _block_scores = _decl("w4_block_scores", _ST, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P)
 _select = _decl("w4_select", _ST, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P)
@@ -585,6 +589,7 @@ def paged_attn_workspace_bytes(cache: "PagedCache") -> int:
 
 
 def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, workspace, stream):
+    # window: what the call has between scale and lse, or (blocks, counts) ahead of scale;
     # workspace: its address and bytes; stream: a raw one
     shape = q.shape
     T, H, D = shape
@@ -595,9 +600,16 @@ def _attn(fn, where, dtype, cache, q, out, lens, table, scale, window, lse, work
         if lse.dtype is not torch.float32 or lse.numel() != T * H:
             raise ValueError("lse: expected float32 [seqs * tokens, q_heads]")
         lse = _ptr(lse)
+    scale = D ** -0.5 if scale is None else scale
+    if type(window) is tuple:
+        blocks, counts = window
+        most = blocks.shape[-1]
+        middle = (_filled(blocks, (B, cache.kv_heads, most), torch.int32, "blocks"),
+                  _int32(counts, B, "counts"), most, scale)
+    else:
+        middle = (scale, window)
     _ok(fn(cache.ref, _heads(q), _heads(out, dtype), H, T // B, _int32(lens, B, "lens"),
-           _block_table(table), D ** -0.5 if scale is None else scale, window, lse,
-           *workspace, stream), where)
+           _block_table(table), *middle, lse, *workspace, stream), where)
 
 
 def paged_attn(cache: "PagedCache", q, out, lens, table, workspace, scale=None, window: int = 0,
@@ -613,6 +625,22 @@ def paged_attn_f32(cache: "PagedCache", q, out, lens, table, workspace, scale=No
     """w4_paged_attn_f32: as paged_attn, fp32 result."""
     _attn(_paged_attn_f32, "w4_paged_attn_f32", torch.float32, cache, q, out, lens, table, scale,
           window, lse, (_ptr(workspace), workspace.nbytes), _raw_stream(stream, q))
+
+
+def sparse_attn(cache: "PagedCache", q, out, lens, table, blocks, counts, workspace, scale=None,
+                lse=None, stream=None) -> None:
+    """w4_sparse_attn: as paged_attn, over the blocks that blocks[b, h, :counts[b]]
+    (int32 [seqs, kv_heads, most], ascending) lists for every key/value head."""
+    _attn(_sparse_attn, "w4_sparse_attn", torch.bfloat16, cache, q, out, lens, table, scale,
+          (blocks, counts), lse, (_ptr(workspace), workspace.nbytes), _raw_stream(stream, q))
+
+
+def sparse_attn_f32(cache: "PagedCache", q, out, lens, table, blocks, counts, workspace,
+                    scale=None, lse=None, stream=None) -> None:
+    """w4_sparse_attn_f32: as sparse_attn, fp32 result."""
+    _attn(_sparse_attn_f32, "w4_sparse_attn_f32", torch.float32, cache, q, out, lens, table,
+          scale, (blocks, counts), lse, (_ptr(workspace), workspace.nbytes),
+          _raw_stream(stream, q))
 
 
 def _filled(t, shape, dtype, what: str) -> int:
@@ -797,6 +825,17 @@ class PagedCache:
                workspace=None, stream=None):
         """Attention of the new tokens; returns (out bfloat16, lse float32), by
         default new tensors, made on `stream`."""
+        return self._attend(_paged_attn, "w4_paged_attn", q, lens, table, scale, window, out, lse,
+                            workspace, stream)
+
+    def attend_blocks(self, q, lens, table, blocks, counts, scale=None, out=None, lse=None,
+                      workspace=None, stream=None):
+        """Attention of the new tokens over the blocks blocks[b, h, :counts[b]] (ascending,
+        int32 [seqs, kv_heads, most]) alone; as attend() otherwise."""
+        return self._attend(_sparse_attn, "w4_sparse_attn", q, lens, table, scale,
+                            (blocks, counts), out, lse, workspace, stream)
+
+    def _attend(self, fn, where, q, lens, table, scale, window, out, lse, workspace, stream):
         raw, kept = _raw_stream(stream, q), None
         if workspace is not None:
             kept = (_ptr(workspace), workspace.nbytes), workspace
@@ -810,8 +849,8 @@ class PagedCache:
                     out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
                 if lse is None:
                     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        _attn(_paged_attn, "w4_paged_attn", torch.bfloat16, self, q, out, lens, table, scale,
-              window, lse, kept[0], raw)
+        _attn(fn, where, torch.bfloat16, self, q, out, lens, table, scale, window, lse, kept[0],
+              raw)
         return out, lse
 
     def new_bounds(self) -> torch.Tensor:

@@ -1,5 +1,7 @@
 """Host-side checks of the calls for long contexts that need no GPU: argument
 errors (every call here fails validation, so no pointer is looked at)."""
+import ctypes
+
 import pytest
 
 from tests.test_abi_host import FAKE, lib  # noqa: F401
@@ -63,3 +65,24 @@ def select(lib, scores=FAKE, seqs=2, heads=2, columns=9, lens=FAKE, unit=1, firs
     (dict(columns=1 << 30), 2)])
 def test_select_errors(lib, kw, want):  # noqa: F811
     assert select(lib, **kw) == want
+
+
+def sparse(lib, c=cache(), q=heads(), out=heads(), hq=2, tokens=1, lens=FAKE,  # noqa: F811
+           t=table(), blocks=FAKE, counts=FAKE, most=4, scale=0.125, lse=None, ws=FAKE, nbytes=0,
+           name="w4_sparse_attn"):
+    f = getattr(lib, name)
+    f.argtypes = [P, P, P, I, I, P, P, P, P, I, ctypes.c_float, P, P, ctypes.c_size_t, P]
+    return f(ref(c), ref(q), ref(out), hq, tokens, lens, ref(t), blocks, counts, most, scale, lse,
+             ws, nbytes, None)
+
+
+@pytest.mark.parametrize("name", ["w4_sparse_attn", "w4_sparse_attn_f32"])
+@pytest.mark.parametrize("kw,want", [k for k in WALK if "t" not in k[0]] + QUERIES + [
+    (dict(t=None), 1), (dict(t=table(None)), 1), (dict(t=table(seqs=1 << 28, width=4)), 2),
+    (dict(blocks=None), 1), (dict(blocks=FAKE + 2), 1), (dict(counts=None), 1),
+    (dict(counts=FAKE + 1), 1), (dict(most=0), 1), (dict(most=(1 << 31) - 1), 2),
+    (dict(out=None), 1), (dict(out=heads(None)), 1), (dict(out=heads(FAKE + 2)), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(lse=FAKE + 2), 1),
+    (dict(ws=None), 1), (dict(ws=FAKE + 128), 1)])
+def test_sparse_attn_errors(lib, kw, want, name):  # noqa: F811
+    assert sparse(lib, name=name, **kw) == want
