@@ -763,6 +763,32 @@ w4_status w4_sparse_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const 
                              const int32_t *counts, int most, float scale, float *lse,
                              void *workspace, size_t workspace_bytes, w4_stream_t stream);
 
+/*
+ * What the cached tokens get of the new tokens' attention, added to what they had:
+ *   weights[b][h][j] = (j < lens[b] - tokens ? decay * before[b][h][j] : 0)
+ *                      + sum over the rows that see key j of exp(scale q . k_j - lse)
+ * for j < lens[b], the rows being those of w4_paged_attn (new tokens x query heads
+ * of h) with its window, and lse what it returned for them: each row adds 1 in all.
+ * The new tokens' own places start at 0, so weights need not be cleared.  Entries
+ * from lens[b] on are left as they were.  A row whose lse is infinite gives
+ * nothing; a key that no row sees, or whose page is not in the pool, gets nothing.
+ * Sums are fp32, in an order that depends on the sizes alone.
+ *   q       : as for w4_paged_attn
+ *   lse     : device float [seqs * tokens][q_heads]
+ *   before  : device float [seqs][kv_heads][columns], or NULL: 0; not read where
+ *             decay is 0; may be weights, otherwise must not overlap it
+ *   decay   : finite
+ *   weights : device float [seqs][kv_heads][columns]
+ *   columns : >= 1; a longer sequence is cut to it (W4_KV_ERR_LENGTH)
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, sizes as for
+ * w4_key_bounds), W4_ERR_CUDA.
+ */
+w4_status w4_attn_weights(const w4_kv_cache *cache, const w4_heads *q, const float *lse,
+                          int q_heads, int tokens, const int32_t *lens,
+                          const w4_block_table *table, float scale, int window,
+                          const float *before, float decay, float *weights, int columns,
+                          w4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -113,6 +113,10 @@ struct AttnArgs {
     void *workspace;
 };
 size_t attn_workspace_bytes(int head_dim, int num_sms);
+// (a.lse is read; a.most: columns or the table's room, the smaller one)
+cudaError_t launch_attn_weights(const AttnArgs &a, int format, int head_dim, const float *before,
+                                float decay, float *weights, int columns, int num_sms,
+                                cudaStream_t stream);
 cudaError_t launch_paged_attn(const AttnArgs &a, int format, int head_dim, int num_sms,
                               cudaStream_t stream);
 

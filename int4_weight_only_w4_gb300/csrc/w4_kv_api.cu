@@ -413,4 +413,35 @@ w4_status w4_sparse_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const 
                               scale, lse, workspace, workspace_bytes, true, stream);
 }
 
+w4_status w4_attn_weights(const w4_kv_cache *cache, const w4_heads *q, const float *lse,
+                          int q_heads, int tokens, const int32_t *lens,
+                          const w4_block_table *table, float scale, int window,
+                          const float *before, float decay, float *weights, int columns,
+                          w4_stream_t stream) {
+    w4_status st = walk_ok(cache, table, lens);
+    if (st == W4_OK) st = queries_ok(cache, q, q_heads, tokens, table);
+    if (st != W4_OK) return st;
+    if (!lse || !weights || !aligned(lse, 4) || !aligned(before, 4) || !aligned(weights, 4) ||
+        !isfinite(scale) || !isfinite(decay) || window < 0 || columns < 1)
+        return W4_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0) return W4_ERR_CUDA;
+    const int room = table->width * cache->page_tokens;
+    w4::AttnArgs a = {};
+    a.pool = pool_of(cache, table);
+    a.q = heads_of(q);
+    a.lse = const_cast<float *>(lse);
+    a.lens = lens;
+    a.q_heads = q_heads;
+    a.group = q_heads / cache->kv_heads;
+    a.group_magic = magic_of(a.group);
+    a.tokens = tokens;
+    a.scale = scale;
+    a.window = window < room ? window : 0;
+    a.most = columns < room ? columns : room;
+    return cuda_status(w4::launch_attn_weights(a, cache->format, cache->head_dim, before, decay,
+                                               weights, columns, sms,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -459,6 +459,8 @@ _sparse_attn_f32 = _decl("w4_sparse_attn_f32", _ST, *_SPARSE_ARGS)
 _key_bounds = _decl("w4_key_bounds", _ST, _P, _P, _I, _P, _P, _P)
 _block_scores = _decl("w4_block_scores", _ST, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P)
 _select = _decl("w4_select", _ST, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P)
+_attn_weights = _decl("w4_attn_weights", _ST, _P, _P, _P, _I, _I, _P, _P, ctypes.c_float, _I, _P,
+                      ctypes.c_float, _P, _I, _P)
 
 
 def _heads(t, dtype=torch.bfloat16) -> bytes | None:
@@ -699,6 +701,25 @@ def select(scores, lens, index, counts, unit: int = 1, first: int = 0, last: int
                 _int32(counts, B, "counts"), _raw_stream(stream, scores)), "w4_select")
 
 
+def attn_weights(cache: "PagedCache", q, lse, lens, table, weights, before=None,
+                 decay: float = 1.0, scale=None, window: int = 0, stream=None) -> None:
+    """w4_attn_weights: weights, float32 [seqs, kv_heads, columns], = decay * before (may
+    be weights; None: 0) + what every cached token gets of the new tokens' attention,
+    whose log-sum-exp is lse, float32 [seqs * tokens, q_heads]."""
+    H, M = _new_tokens(cache, q, table)
+    T, B, shape = q.shape[0], table.shape[0], weights.shape
+    if len(shape) != 3:
+        raise ValueError("weights: expected float32 [seqs, kv_heads, columns]")
+    expected = (B, cache.kv_heads, shape[2])
+    _ok(_attn_weights(cache.ref, _heads(q), _filled(lse, (T, H), torch.float32, "lse"), H, M,
+                      _int32(lens, B, "lens"), _block_table(table),
+                      q.shape[2] ** -0.5 if scale is None else scale, window,
+                      before if before is None else
+                      _filled(before, expected, torch.float32, "before"), decay,
+                      _filled(weights, expected, torch.float32, "weights"), shape[2],
+                      _raw_stream(stream, q)), "w4_attn_weights")
+
+
 class RopeTable:
     """A table of rotations: float32 [rows, rotary_dim/2, 2] (cos, sin) pairs
     on the device, and which values of a head form a pair."""
@@ -872,6 +893,23 @@ class PagedCache:
                                     dtype=torch.float32, device=q.device)
         block_scores(self, bounds, q, lens, table, scores, stream)
         return scores
+
+    def attn_weights(self, q, lse, lens, table, scale=None, window: int = 0, before=None,
+                     decay: float = 1.0, weights=None, columns: int | None = None,
+                     stream=None) -> torch.Tensor:
+        """decay * before + what every cached token gets of the new tokens' attention, by
+        key/value head; q, lens, table, scale and window as attend() had them, lse as it
+        returned it.  before may be weights.  [seqs, kv_heads, columns] (default: a new
+        tensor, made on `stream`, with before's columns, or room for all of a table's
+        tokens; 0 past a sequence's tokens)."""
+        if weights is None:
+            if columns is None:
+                columns = table.shape[1] * self.page_tokens if before is None else before.shape[2]
+            with _on(stream, q.device):
+                weights = torch.zeros((table.shape[0], self.kv_heads, columns),
+                                      dtype=torch.float32, device=q.device)
+        attn_weights(self, q, lse, lens, table, weights, before, decay, scale, window, stream)
+        return weights
 
     def check(self) -> None:
         """Raise W4Error if a call recorded an error, and clear it.  Waits for

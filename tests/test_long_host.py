@@ -86,3 +86,19 @@ def sparse(lib, c=cache(), q=heads(), out=heads(), hq=2, tokens=1, lens=FAKE,  #
     (dict(ws=None), 1), (dict(ws=FAKE + 128), 1)])
 def test_sparse_attn_errors(lib, kw, want, name):  # noqa: F811
     assert sparse(lib, name=name, **kw) == want
+
+
+def weights(lib, c=cache(), q=heads(), lse=FAKE, hq=2, tokens=1, lens=FAKE, t=table(),  # noqa: F811
+            scale=0.125, window=0, before=None, decay=1.0, out=FAKE, columns=64):
+    lib.w4_attn_weights.argtypes = [P, P, P, I, I, P, P, ctypes.c_float, I, P, ctypes.c_float, P,
+                                    I, P]
+    return lib.w4_attn_weights(ref(c), ref(q), lse, hq, tokens, lens, ref(t), scale, window,
+                               before, decay, out, columns, None)
+
+
+@pytest.mark.parametrize("kw,want", WALK + QUERIES + [
+    (dict(lse=None), 1), (dict(lse=FAKE + 2), 1), (dict(out=None), 1), (dict(out=FAKE + 1), 1),
+    (dict(before=FAKE + 2), 1), (dict(columns=0), 1), (dict(window=-1), 1),
+    (dict(scale=float("nan")), 1), (dict(decay=float("inf")), 1)])
+def test_attn_weights_errors(lib, kw, want):  # noqa: F811
+    assert weights(lib, **kw) == want
