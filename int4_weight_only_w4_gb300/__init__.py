@@ -16,7 +16,7 @@ _BINDING_NAMES = {
     "RopeTable", "rope", "rope_table", "PagedCache", "kv_pool_bytes", "kv_append", "kv_read",
     "paged_attn", "paged_attn_f32", "paged_attn_workspace_bytes",
     "key_bounds", "block_scores", "select", "sparse_attn",
-    "sparse_attn_f32", "attn_weights",
+    "sparse_attn_f32", "attn_weights", "kv_gather",
 }
 
 

@@ -461,6 +461,7 @@ _block_scores = _decl("w4_block_scores", _ST, _P, _P, _P, _I, _I, _P, _P, _P, _I
 _select = _decl("w4_select", _ST, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P)
 _attn_weights = _decl("w4_attn_weights", _ST, _P, _P, _P, _I, _I, _P, _P, ctypes.c_float, _I, _P,
                       ctypes.c_float, _P, _I, _P)
+_kv_gather = _decl("w4_kv_gather", _ST, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P)
 
 
 def _heads(t, dtype=torch.bfloat16) -> bytes | None:
@@ -720,6 +721,26 @@ def attn_weights(cache: "PagedCache", q, lse, lens, table, weights, before=None,
                       _raw_stream(stream, q)), "w4_attn_weights")
 
 
+def kv_gather(cache: "PagedCache", table, lens, index, counts, to, weights=None,
+              weights_out=None, stream=None) -> None:
+    """w4_kv_gather: place i of sequence b in the pages of `to` gets token index[b, h, i]
+    of those of `table`, for i < counts[b] and every key/value head h (index int32
+    [seqs, kv_heads, most]); weights_out[b, h, i] (float32 [seqs, kv_heads, most]) its
+    entry of weights (float32 [seqs, kv_heads, columns])."""
+    B, H = table.shape[0], cache.kv_heads
+    most, columns = index.shape[-1], 0
+    if (weights is None) != (weights_out is None):
+        raise ValueError("weights, weights_out: expected both or neither")
+    if weights is not None:
+        columns = weights.shape[-1]
+        weights = _filled(weights, (B, H, columns), torch.float32, "weights")
+        weights_out = _filled(weights_out, (B, H, most), torch.float32, "weights_out")
+    _ok(_kv_gather(cache.ref, _block_table(table), _int32(lens, B, "lens"),
+                   _filled(index, (B, H, most), torch.int32, "index"),
+                   _int32(counts, B, "counts"), most, _block_table(to), weights, columns,
+                   weights_out, _raw_stream(stream, index)), "w4_kv_gather")
+
+
 class RopeTable:
     """A table of rotations: float32 [rows, rotary_dim/2, 2] (cos, sin) pairs
     on the device, and which values of a head form a pair."""
@@ -910,6 +931,18 @@ class PagedCache:
                                       dtype=torch.float32, device=q.device)
         attn_weights(self, q, lse, lens, table, weights, before, decay, scale, window, stream)
         return weights
+
+    def gather(self, table, lens, index, counts, to, weights=None, weights_out=None,
+               stream=None):
+        """Move listed tokens to other pages: place i of sequence b in `to` gets token
+        index[b, h, i] in `table`, for i < counts[b] and every head; returns weights_out, the
+        tokens' weights (default, where weights are given: a new tensor, made on
+        `stream`, 0 past the counts)."""
+        if weights is not None and weights_out is None:
+            with _on(stream, index.device):
+                weights_out = torch.zeros(index.shape, dtype=torch.float32, device=index.device)
+        kv_gather(self, table, lens, index, counts, to, weights, weights_out, stream)
+        return weights_out
 
     def check(self) -> None:
         """Raise W4Error if a call recorded an error, and clear it.  Waits for
