@@ -20,6 +20,12 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ void ldsm4(uint32_t *r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ void lds128(uint32_t *r, uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -48,9 +54,8 @@ __device__ __forceinline__ int token_of_row(const AttnArgs &a, int row) {
     return a.group == 1 ? row : (int)__umulhi((unsigned)row, a.group_magic);
 }
 
-// A warp's NT tiles of 8 rows of queries.  DIRECT: of keys in bf16 a lane takes the
-// 16-byte pieces t, t + 4, ... of a row from memory, not what ldmatrix hands out.
-template <int FMT, int D, int NT, bool DIRECT>
+// A warp's NT tiles of 8 rows of queries.
+template <int FMT, int D, int NT>
 struct Queries {
     static constexpr int KS = D / 16;                     // k-steps of a score
     uint32_t qf[NT][KS][2];      // Q as the column operand
@@ -59,7 +64,6 @@ struct Queries {
 
     // Which value of the head goes with half e of register i of k-step ks.
     __device__ static constexpr int q_index(int ks, int i, int e, int t) {
-        if (FMT == W4_KV_BF16 && DIRECT) return 8 * (t + 4 * (ks >> 1)) + 4 * (ks & 1) + 2 * i + e;
         if (FMT == W4_KV_BF16) return 16 * ks + 8 * i + 2 * t + e;
         if (FMT == W4_KV_INT8) return 64 * (ks >> 2) + 16 * t + 4 * (ks & 3) + i + 2 * e;
         return (D / 4) * t + 8 * (ks >> 1) + 2 * (ks & 1) + i + 4 * e;

@@ -71,16 +71,17 @@ struct Share {
         h = in / n, u = in - h * n;
     }
 
-    // `k` units on, all of the same head (k <= n - u).
+    // `k` units on.
     template <class Units>
     __device__ __forceinline__ void next(const Units &units, int heads, int k = 1) {
         left -= k, u += k;
-        if (u < n || left <= 0) return;
-        u = 0;
-        if (++h < heads) return;
-        h = 0;
-        do n = units(++b);                                    // left > 0: there is one
-        while (n == 0);
+        while (u >= n && left > 0) {
+            u -= n;
+            if (++h < heads) continue;
+            h = 0;
+            do n = units(++b);                                // left > 0: there is one
+            while (n == 0);
+        }
     }
 };
 

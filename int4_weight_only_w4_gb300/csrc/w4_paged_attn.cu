@@ -71,12 +71,6 @@ constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not ther
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen no key
 constexpr float kLn2 = 0.693147180559945309417f;
 
-__device__ __forceinline__ void ldsm4(uint32_t *r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
 __device__ __forceinline__ void ldsm4_t(uint32_t *r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -139,12 +133,12 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
 
 // A warp's NT tiles of 8 rows: its share of Q, and the running m, l, O.
 template <int FMT, int D, int NT>
-struct Tile : Queries<FMT, D, NT, false> {
+struct Tile : Queries<FMT, D, NT> {
     using L = KvLayout<FMT, D>;
-    using Queries<FMT, D, NT, false>::KS;                 // k-steps of S, m-tiles of O
-    using Queries<FMT, D, NT, false>::qf;
-    using Queries<FMT, D, NT, false>::sc;
-    using Queries<FMT, D, NT, false>::qs;
+    using Queries<FMT, D, NT>::KS;                 // k-steps of S, m-tiles of O
+    using Queries<FMT, D, NT>::qf;
+    using Queries<FMT, D, NT>::sc;
+    using Queries<FMT, D, NT>::qs;
     static constexpr float kBias = FMT == W4_KV_BF16 ? 0.f : 6.f;
     static constexpr float kSlack = FMT == W4_KV_BF16 ? 8.f : 14.f;
 
