@@ -20,8 +20,8 @@
 namespace w4 {
 namespace {
 
-constexpr int kWeightWarps = 8;
 constexpr int kTilesMax = 8;             // tiles of 8 rows that a launch takes
+constexpr int kWeightWarps = 8;          // of a block; two blocks an SM
 
 struct Weights {
     const float *before;                 // NULL: none
@@ -32,9 +32,17 @@ struct Weights {
                                          // on it adds to what the one before left
 };
 
+// Operands of one tile of rows in shared memory, by lane.
+template <int D>
+struct SharedTile {
+    uint4 q[D / 32][32];                 // two k-steps each
+    float4 factors[32];                  // sc, qs of columns 2t, 2t + 1
+    float2 minus[32];                    // their lse in units of log2; infinite: no row
+};
+
 // A unit is RECS neighbouring records, 4 KB of keys where D is 128: what a warp does
 // at a time.
-template <int FMT, int D>
+template <int FMT, int D, bool ONE>
 struct Stage {
     using L = KvLayout<FMT, D>;
     static constexpr int kRecs = L::kPart >= 4096 ? 1 : L::kPart >= 2048 ? 2 : 4;
@@ -42,7 +50,7 @@ struct Stage {
     // of a stage of a warp's ring: keys, their descriptors, weights before
     static constexpr int kMetaAt = kRecs * L::kPart, kBeforeAt = kMetaAt + 64 * kRecs,
                          kBytes = kBeforeAt + 4 * kTokens;
-    static constexpr int kStages = 3;
+    static constexpr int kStages = ONE ? 3 : 2;      // (more rows take longer over a unit)
 };
 
 // Units of a sequence.
@@ -56,14 +64,6 @@ struct Units {
     __device__ __forceinline__ int operator()(int b) const {
         return (len(b) + TOKENS - 1) / TOKENS;
     }
-};
-
-// Operands of one tile of rows in shared memory, by lane.
-template <int D>
-struct SharedTile {
-    uint4 q[D / 32][32];                 // two k-steps each
-    float4 factors[32];                  // sc, qs of columns 2t, 2t + 1
-    float2 minus[32];                    // their lse in units of log2; infinite: no row
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
@@ -116,8 +116,8 @@ template <int FMT, int D, bool ONE>
 __global__ void __launch_bounds__(32 * kWeightWarps, 2)
 weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
     using L = KvLayout<FMT, D>;
-    using S = Stage<FMT, D>;
-    constexpr int KS = D / 16, R = S::kRecs, LANES = 32 / R;
+    using S = Stage<FMT, D, ONE>;
+    constexpr int KS = D / 16, R = S::kRecs, LANES = 32 / R, WARPS = kWeightWarps;
     extern __shared__ __align__(128) unsigned char smem[];
     SharedTile<D> *tiles = reinterpret_cast<SharedTile<D> *>(smem);
     begin_after_previous();
@@ -176,7 +176,7 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
                         copy4(to + S::kBeforeAt + 4 * k, j < upto ? old + j : old, j < upto);
                 }
             }
-            ahead.next(units, heads, kWeightWarps);
+            ahead.next(units, heads, WARPS);
             look();
         }
         copies_end();
@@ -224,7 +224,7 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
             if (u < stop) load_tile(0, q1, f1, m1);
         } else {
             __syncthreads();                                  // no warp is in the last head
-            for (int n = warp; n < n_tiles; n += kWeightWarps) {
+            for (int n = warp; n < n_tiles; n += WARPS) {
                 uint4 q4[D / 32];
                 load_tile(n, q4, tiles[n].factors[lane], tiles[n].minus[lane]);
 #pragma unroll
@@ -232,7 +232,7 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
             }
             __syncthreads();
         }
-        for (; u < stop; u += kWeightWarps) {
+        for (; u < stop; u += WARPS) {
             copies_wait<S::kStages - 2>();
             __syncwarp();                                     // everyone's copies are there, and
                                                               // the stage before is free
@@ -353,7 +353,7 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
 template <int FMT, int D, bool ONE>
 cudaError_t launch(const AttnArgs &a, const Weights &out, int n_tiles, int num_sms,
                    cudaStream_t stream) {
-    using S = Stage<FMT, D>;
+    using S = Stage<FMT, D, ONE>;
     const auto bytes = [](int tiles) {
         return tiles * (int)sizeof(SharedTile<D>) + kWeightWarps * S::kStages * S::kBytes;
     };

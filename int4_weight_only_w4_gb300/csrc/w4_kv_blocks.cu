@@ -7,6 +7,7 @@ namespace w4 {
 namespace {
 
 constexpr int kBlockWarps = 4;
+constexpr int kDirectBlocks = 32;      // blocks an SM up to which units have one worker each
 
 // Blocks of a sequence that hold its last tokens, and the first of them.
 struct Touched {
@@ -44,18 +45,24 @@ struct Raw {
     uint32_t meta;
 };
 
-// A warp takes a block of a head: D / 16 lanes a key, 16 values each, so that
-// every load is 16 bytes (8 in 4 bits) of whole rows.
-template <int FMT, int D>
+// PARTS warps take a block of a head, every PARTS-th record each, and a key's
+// values D / 16 lanes, 16 each, so that every load is 16 bytes (8 in 4 bits) of whole
+// rows.
+template <int FMT, int D, int PARTS>
 __global__ void __launch_bounds__(32 * kBlockWarps)
-bounds_kernel(const Touched touched, uint32_t *bounds) {
+bounds_kernel(const Touched touched, uint32_t *bounds, int most) {
     using L = KvLayout<FMT, D>;
     constexpr int LANES = D / 16, ROWS = 32 / LANES, LOADS = kRecTokens / ROWS;
+    constexpr int UNITS = kBlockWarps / PARTS;
+    __shared__ uint4 joined[UNITS][PARTS][4][LANES];
     begin_after_previous();
     const KvPool &pool = touched.pool;
     const int lane = threadIdx.x & 31, part = lane % LANES, row0 = lane / LANES;
-    Share s(touched, pool.seqs, pool.kv_heads, blockIdx.x * kBlockWarps + (threadIdx.x >> 5),
-            gridDim.x * kBlockWarps);
+    const int warp = threadIdx.x >> 5, mine = warp % PARTS, unit = warp / PARTS;
+    Share s = most ? Share::one(touched, pool.seqs, pool.kv_heads, most,
+                                blockIdx.x * UNITS + unit)
+                   : Share(touched, pool.seqs, pool.kv_heads, blockIdx.x * UNITS + unit,
+                           gridDim.x * UNITS);
     for (; s.left > 0; s.next(touched, pool.kv_heads)) {
         const int len = touched.len(s.b), block = touched.first(len) + s.u;
         const int page = pool.table[s.b * pool.stride + block];
@@ -65,7 +72,9 @@ bounds_kernel(const Touched touched, uint32_t *bounds) {
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) hi[i] = 0xFF80FF80u, lo[i] = 0x7F807F80u;
-        for (int r0 = 0; r0 < there; r0 += kRecTokens, rec += L::kBytes) {
+        rec += mine * L::kBytes;
+        for (int r0 = mine * kRecTokens; r0 < there;
+             r0 += PARTS * kRecTokens, rec += PARTS * L::kBytes) {
             Raw<FMT> raw[LOADS];
 #pragma unroll
             for (int x = 0; x < LOADS; ++x) {
@@ -124,7 +133,37 @@ bounds_kernel(const Touched touched, uint32_t *bounds) {
                 lo[i] = min2(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], x));
             }
         // the largest from the first lanes, the smallest from the next ones
-        if (row0 < 2) {
+        if constexpr (PARTS > 1) {
+            const auto sync = [&]() {                         // of the block's warps
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "n"(32 * PARTS) : "memory");
+            };
+            if (row0 == 0) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    joined[unit][mine][y][part] =
+                        make_uint4(hi[4 * y], hi[4 * y + 1], hi[4 * y + 2], hi[4 * y + 3]);
+                    joined[unit][mine][2 + y][part] =
+                        make_uint4(lo[4 * y], lo[4 * y + 1], lo[4 * y + 2], lo[4 * y + 3]);
+                }
+            }
+            sync();
+            if (mine == 0 && row0 < 2) {
+#pragma unroll
+                for (int x = 1; x < PARTS; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint4 a = joined[unit][x][y][part], b = joined[unit][x][2 + y][part];
+                        hi[4 * y] = max2(hi[4 * y], a.x), hi[4 * y + 1] = max2(hi[4 * y + 1], a.y);
+                        hi[4 * y + 2] = max2(hi[4 * y + 2], a.z);
+                        hi[4 * y + 3] = max2(hi[4 * y + 3], a.w);
+                        lo[4 * y] = min2(lo[4 * y], b.x), lo[4 * y + 1] = min2(lo[4 * y + 1], b.y);
+                        lo[4 * y + 2] = min2(lo[4 * y + 2], b.z);
+                        lo[4 * y + 3] = min2(lo[4 * y + 3], b.w);
+                    }
+            }
+            sync();                                           // joined is free again
+        }
+        if (mine == 0 && row0 < 2) {
             uint4 *out = reinterpret_cast<uint4 *>(
                 bounds + ((long long)page * pool.kv_heads + s.h) * D + row0 * (D / 2) + 8 * part);
 #pragma unroll
@@ -156,14 +195,15 @@ struct Tiles {
 template <int D>
 __global__ void __launch_bounds__(32 * kBlockWarps)
 scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q, int group,
-              unsigned group_magic, int tokens, float *scores, int columns) {
+              unsigned group_magic, int tokens, float *scores, int columns, int most) {
     constexpr int PIECES = D / 32;
     begin_after_previous();
     const KvPool &pool = tiles.pool;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rows = tokens * group;
-    Share s(tiles, pool.seqs, pool.kv_heads, blockIdx.x * kBlockWarps + (threadIdx.x >> 5),
-            gridDim.x * kBlockWarps);
+    const int w = blockIdx.x * kBlockWarps + (threadIdx.x >> 5);
+    Share s = most ? Share::one(tiles, pool.seqs, pool.kv_heads, most, w)
+                   : Share(tiles, pool.seqs, pool.kv_heads, w, gridDim.x * kBlockWarps);
     for (; s.left > 0; s.next(tiles, pool.kv_heads)) {
         const int len = tiles.len(s.b), blocks = tiles.blocks(len);
         uint4 a[2][2][PIECES];                                // hi, lo of blocks g, g + 8
@@ -227,10 +267,34 @@ scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q
     }
 }
 
-// Blocks of warps for at most `units` units, a few waves of the device.
-int grid_of(long long units, int num_sms) {
-    const long long blocks = (units + kBlockWarps - 1) / kBlockWarps, most = 8LL * num_sms;
-    return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+// The blocks of a launch for at most `most` units a head, `each` of them a block.  A
+// worker for every unit that there could be while they are few: it finds its own
+// without adding up all sequences' lengths, and those without one end at once.  With
+// more, as where tables are much wider than the sequences, as many as the device
+// holds share the units that there are (*most = 0).
+int grid_of(const KvPool &pool, int *most, int each, int num_sms) {
+    const long long units = (long long)*most * pool.seqs * pool.kv_heads;
+    const long long blocks = (units + each - 1) / each;
+    if (blocks <= (long long)kDirectBlocks * num_sms) return (int)blocks;
+    *most = 0;
+    return 4 * num_sms;
+}
+
+template <int FMT, int D, int PARTS>
+cudaError_t launch_bounds(const Touched &touched, void *bounds, int most, int num_sms,
+                          cudaStream_t stream) {
+    const int grid = grid_of(touched.pool, &most, kBlockWarps / PARTS, num_sms);
+    return launch_overlapped(bounds_kernel<FMT, D, PARTS>, dim3(grid), dim3(32 * kBlockWarps), 0,
+                             stream, touched, static_cast<uint32_t *>(bounds), most);
+}
+
+template <int FMT, int D>
+cudaError_t launch_parts(const Touched &touched, void *bounds, int most, int num_sms,
+                         cudaStream_t stream) {
+    const int records = touched.pool.page_records;
+    return records >= 4   ? launch_bounds<FMT, D, 4>(touched, bounds, most, num_sms, stream)
+           : records >= 2 ? launch_bounds<FMT, D, 2>(touched, bounds, most, num_sms, stream)
+                          : launch_bounds<FMT, D, 1>(touched, bounds, most, num_sms, stream);
 }
 
 }  // namespace
@@ -240,19 +304,15 @@ cudaError_t launch_key_bounds(const KvPool &pool, int format, int head_dim, void
                               cudaStream_t stream) {
     const Touched touched = {pool, lens, tokens};
     const long long reach = ((long long)tokens + pool.page_tokens - 2) / pool.page_tokens + 1;
-    const int grid = grid_of(
-        (reach < pool.width ? reach : pool.width) * pool.seqs * pool.kv_heads, num_sms);
-    const auto run = [&](auto kernel) {
-        return launch_overlapped(kernel, dim3(grid), dim3(32 * kBlockWarps), 0, stream, touched,
-                                 static_cast<uint32_t *>(bounds));
-    };
+    const int most = (int)(reach < pool.width ? reach : pool.width);
+    const auto run = [&](auto f) { return f(touched, bounds, most, num_sms, stream); };
     if (head_dim == 128)
-        return format == W4_KV_BF16   ? run(bounds_kernel<W4_KV_BF16, 128>)
-               : format == W4_KV_INT8 ? run(bounds_kernel<W4_KV_INT8, 128>)
-                                      : run(bounds_kernel<W4_KV_INT4, 128>);
-    return format == W4_KV_BF16   ? run(bounds_kernel<W4_KV_BF16, 64>)
-           : format == W4_KV_INT8 ? run(bounds_kernel<W4_KV_INT8, 64>)
-                                  : run(bounds_kernel<W4_KV_INT4, 64>);
+        return format == W4_KV_BF16   ? run(launch_parts<W4_KV_BF16, 128>)
+               : format == W4_KV_INT8 ? run(launch_parts<W4_KV_INT8, 128>)
+                                      : run(launch_parts<W4_KV_INT4, 128>);
+    return format == W4_KV_BF16   ? run(launch_parts<W4_KV_BF16, 64>)
+           : format == W4_KV_INT8 ? run(launch_parts<W4_KV_INT8, 64>)
+                                  : run(launch_parts<W4_KV_INT4, 64>);
 }
 
 cudaError_t launch_block_scores(const KvPool &pool, int head_dim, const void *bounds,
@@ -260,16 +320,14 @@ cudaError_t launch_block_scores(const KvPool &pool, int head_dim, const void *bo
                                 const int32_t *lens, float *scores, int columns, int num_sms,
                                 cudaStream_t stream) {
     const Tiles tiles = {pool, lens};
-    const int grid =
-        grid_of((pool.width + 15LL) / 16 * pool.seqs * pool.kv_heads, num_sms);
-    const uint4 *b = static_cast<const uint4 *>(bounds);
-    return head_dim == 128
-               ? launch_overlapped(scores_kernel<128>, dim3(grid), dim3(32 * kBlockWarps), 0,
-                                   stream, tiles, b, q, group, group_magic, tokens, scores,
-                                   columns)
-               : launch_overlapped(scores_kernel<64>, dim3(grid), dim3(32 * kBlockWarps), 0,
-                                   stream, tiles, b, q, group, group_magic, tokens, scores,
-                                   columns);
+    int most = (pool.width + 15) / 16;
+    const int grid = grid_of(pool, &most, kBlockWarps, num_sms);
+    const auto run = [&](auto kernel) {
+        return launch_overlapped(kernel, dim3(grid), dim3(32 * kBlockWarps), 0, stream, tiles,
+                                 static_cast<const uint4 *>(bounds), q, group, group_magic,
+                                 tokens, scores, columns, most);
+    };
+    return head_dim == 128 ? run(scores_kernel<128>) : run(scores_kernel<64>);
 }
 
 }  // namespace w4

@@ -37,6 +37,7 @@ struct Share {
     int b, h, u, n;     // unit u of n
     int left;
 
+    Share() = default;
     template <class Units>
     __device__ __forceinline__ Share(const Units &units, int seqs, int heads, int w, int W) {
         const int lane = threadIdx.x & 31, each = (seqs + 31) >> 5;
@@ -69,6 +70,18 @@ struct Share {
         in = __shfl_sync(0xFFFFFFFFu, in, src);
         if (!found) left = 0;                                 // there is no unit at all
         h = in / n, u = in - h * n;
+    }
+
+    // Unit `w` of a list in which every sequence has `most` units a head, if it is
+    // there: for grids that have a worker for each.
+    template <class Units>
+    __device__ __forceinline__ static Share one(const Units &units, int seqs, int heads, int most,
+                                                int w) {
+        Share s;
+        const int row = w / most;
+        s.u = w - row * most, s.b = row / heads, s.h = row - s.b * heads, s.n = most;
+        s.left = s.b < seqs && s.u < units(s.b) ? 1 : 0;
+        return s;
     }
 
     // `k` units on.

@@ -115,9 +115,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Job j, int blocks
         each_key([&](uint32_t key, int) {
             const bool counts = top == 32 || key >> top == found >> top;
             const int bin = counts ? (int)(key >> shift & ((1u << bits) - 1)) : -1;
-            int same;
-            __match_all_sync(0xFFFFFFFFu, bin, &same);
-            if (same) {                                       // often, where scores are equal
+            if (__all_sync(0xFFFFFFFFu, bin == __shfl_sync(0xFFFFFFFFu, bin, 0))) {
+                // often, where many scores are equal
                 if (lane == 0 && counts) atomicAdd(&h[bin], 32);
             } else if (counts) {
                 atomicAdd(&h[bin], 1);
