@@ -3,22 +3,25 @@
 // A score becomes an unsigned key in the scores' order.  The count-th largest key
 // is found digit by digit (11, 11 and 10 bits): a histogram of the keys that
 // share the digits found so far, and a sum over its bins from the top until
-// `count` is reached.  Then an item is chosen if its key is above that one, or
-// equal to it and among the first of those; how many are chosen before it is its
-// place in the list, so nothing is sorted.
+// `count` is reached.  Once few keys are left in the bin where it is, they are
+// compared with one another instead.  Then an item is chosen if its key is above
+// that one, or equal to it and among the first of those; how many are chosen before
+// it is its place in the list, so nothing is sorted.
 //
-// A row is shared by a cluster of up to 8 blocks, whose keys stay in registers
-// through all passes (131072 items at 16 a thread; longer rows are read again by
-// each pass); the blocks add up each other's histograms through distributed
-// shared memory.
+// A row's keys stay in registers through all passes.  Long rows are shared by a
+// cluster of up to 8 blocks, which add up each other's histograms through
+// distributed shared memory; rows of more than 262144 items are read again by each
+// pass.
+#include <atomic>
+
 #include "w4_device.cuh"
 #include "w4_kv.cuh"
 
 namespace w4 {
 namespace {
 
-constexpr int kKeys = 16;                 // items of a thread that stays resident
 constexpr int kBins = 2048;
+constexpr int kFew = 256;                 // keys that are compared with one another
 constexpr uint32_t kAlways = 0xFFFFFFFFu, kNan = 0xFFFFFFFEu;
 
 struct Job {
@@ -51,61 +54,92 @@ __device__ __forceinline__ void cluster_sync() {
         "barrier.cluster.arrive.release.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A word of block `rank`'s shared memory, by its address in the own one.
-__device__ __forceinline__ int cluster_load(const int *p, int rank) {
+// Words of block `rank`'s shared memory, by their address in the own one.
+__device__ __forceinline__ uint32_t cluster_address(const int *p, int rank) {
     uint32_t at;
-    int r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return at;
+}
+__device__ __forceinline__ int2 cluster_load(const int *p, int rank) {
+    int2 r;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(r.x), "=r"(r.y)
+                 : "r"(cluster_address(p, rank))
+                 : "memory");
     return r;
 }
 
-template <int THREADS, bool RESIDENT>
-__global__ void __launch_bounds__(THREADS) select_kernel(const Job j, int blocks) {
+// What lanes below this one have, and all of them.
+__device__ __forceinline__ int scan(int v, int *all) {
+    const int lane = threadIdx.x & 31;
+    int upto = v;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, upto, x);
+        if (lane >= x) upto += u;
+    }
+    *all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    return upto - v;
+}
+
+// KEYS items a thread, or (0) as many as it takes, which are read again by each
+// pass.  blocks: of a cluster, 1, 2, 4 or 8.
+template <int THREADS, int KEYS>
+__global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blocks) {
     constexpr int WARPS = THREADS / 32, EACH = kBins / THREADS;
-    __shared__ int hist[3][kBins];
-    __shared__ int sums[WARPS], above[WARPS], equal[WARPS], total[2];
-    __shared__ int found_bin, found_need, found_in;
+    constexpr bool SHARED = THREADS == 1024;                  // rows of several blocks
+    __shared__ __align__(16) int hist[3][kBins];
+    __shared__ int sums[WARPS], above[WARPS], equal[WARPS];
+    __shared__ __align__(8) int total[2];
+    __shared__ int found_bin, found_need, found_in, few;
+    __shared__ uint32_t few_keys[kFew];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < 3 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 3 * kBins / 4; i += THREADS)
+        reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
+    if (tid == 0) few = 0;
     begin_after_previous();
-    const int rank = blocks > 1 ? cluster_rank() : 0;
-    const long long row = blockIdx.x / blocks;
-    const int b = (int)(row / j.heads), n = items_of(j, b);
-    int32_t *out = j.index + row * j.count;
-    if (rank == 0 && tid == 0 && row % j.heads == 0) j.counts[b] = min(n, j.count);
+    const bool shared = SHARED && blocks > 1;
+    const int rank = shared ? cluster_rank() : 0;
+    const unsigned row = shared ? blockIdx.x / blocks : blockIdx.x;
+    const int b = row / j.heads, n = items_of(j, b);
+    int32_t *out = j.index + (long long)row * j.count;
+    if (rank == 0 && tid == 0 && row == (unsigned)b * j.heads) j.counts[b] = min(n, j.count);
     if (n <= j.count) {                                       // all of them, in every block
         for (int i = rank * THREADS + tid; i < n; i += blocks * THREADS) out[i] = i;
         return;
     }
     // a block, and a warp of it, has neighbouring items: 32 a round
     const int rounds = ((n + blocks - 1) / blocks + THREADS - 1) / THREADS;
-    const int start = (rank * WARPS + warp) * 32 * rounds;
-    const float *in = j.scores + row * j.columns;
-    const auto key_at = [&](int k) -> uint32_t {
-        const int i = start + 32 * k + lane;
-        if (i >= n) return 0u;
-        return i < j.first || i >= n - j.last ? kAlways : key_of(in[i]);
+    const int start = (rank * WARPS + warp) * 32 * rounds + lane;
+    const float *in = j.scores + (long long)row * j.columns;
+    const auto key_at = [&](int i, float v) -> uint32_t {
+        return i >= n ? 0u : i < j.first || i >= n - j.last ? kAlways : key_of(v);
     };
-    uint32_t keys[RESIDENT ? kKeys : 1];
-    if constexpr (RESIDENT) {
+    uint32_t keys[KEYS > 0 ? KEYS : 1];
+    if constexpr (KEYS > 0) {
+        float v[KEYS];                                        // all under way together
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k) keys[k] = k < rounds ? key_at(k) : 0u;
+        for (int k = 0; k < KEYS; ++k) v[k] = in[min(start + 32 * k, n - 1)];
+#pragma unroll
+        for (int k = 0; k < KEYS; ++k) keys[k] = k < rounds ? key_at(start + 32 * k, v[k]) : 0u;
     }
     // f(key) of each of the thread's items, all lanes of a warp together
     const auto each_key = [&](auto f) {
-        if constexpr (RESIDENT) {
+        if constexpr (KEYS > 0) {
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
+            for (int k = 0; k < KEYS; ++k)
                 if (k < rounds) f(keys[k], k);
         } else {
-            for (int k = 0; k < rounds; ++k) f(key_at(k), k);
+            for (int k = 0; k < rounds; ++k) {
+                const int i = start + 32 * k;
+                f(key_at(i, in[min(i, n - 1)]), k);
+            }
         }
     };
 
     // ---- the count-th largest key, and how many equal to it are chosen
     uint32_t found = 0;                                       // its upper digits
-    int need = j.count, shift = 32;
+    int need = j.count, shift = 32, left = n;
     __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
@@ -122,46 +156,75 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Job j, int blocks
                 atomicAdd(&h[bin], 1);
             }
         });
-        if (blocks > 1)
+        if (shared)
             cluster_sync();
         else
             __syncthreads();
         // thread t: bins from the top, EACH of them
-        const int bin0 = kBins - 1 - tid * EACH;
-        int in_bin[EACH], mine = 0;
+        const int bin0 = kBins - (tid + 1) * EACH;
+        int in_bin[EACH], mine = 0, whole;
+        if constexpr (SHARED) {
+            static_assert(!SHARED || EACH == 2, "a pair of bins a thread");
+            int2 part[8];
 #pragma unroll
-        for (int x = 0; x < EACH; ++x) {
-            in_bin[x] = 0;
-            if (blocks > 1)
-                for (int r = 0; r < blocks; ++r) in_bin[x] += cluster_load(&h[bin0 - x], r);
-            else
-                in_bin[x] = h[bin0 - x];
-            mine += in_bin[x];
-        }
-        int upto = mine;
+            for (int r = 0; r < 8; ++r) {
+                part[r] = make_int2(0, 0);
+                if (!shared && r == 0)
+                    part[0] = *reinterpret_cast<const int2 *>(&h[bin0]);
+                else if (shared && r < blocks)
+                    part[r] = cluster_load(&h[bin0], r);
+            }
+            in_bin[0] = in_bin[1] = 0;
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, x);
-            if (lane >= x) upto += v;
+            for (int r = 0; r < 8; ++r) in_bin[0] += part[r].x, in_bin[1] += part[r].y;
+        } else {
+#pragma unroll
+            for (int x = 0; x < EACH; x += 4)
+                *reinterpret_cast<int4 *>(&in_bin[x]) =
+                    *reinterpret_cast<const int4 *>(&h[bin0 + x]);
         }
-        if (lane == 31) sums[warp] = upto;
+#pragma unroll
+        for (int x = 0; x < EACH; ++x) mine += in_bin[x];
+        int before = scan(mine, &whole);
+        if (lane == 0) sums[warp] = whole;
         __syncthreads();
-        int before = upto - mine;
-        for (int w = 0; w < warp; ++w) before += sums[w];
+        int all;
+        const int below = scan(lane < WARPS ? sums[lane] : 0, &all);
+        before += __shfl_sync(0xFFFFFFFFu, below, warp);
         if (before < need && need <= before + mine) {
 #pragma unroll
-            for (int x = 0; x < EACH; ++x) {
+            for (int x = EACH - 1; x >= 0; --x) {
                 if (before < need && need <= before + in_bin[x])
-                    found_bin = bin0 - x, found_need = need - before, found_in = in_bin[x];
+                    found_bin = bin0 + x, found_need = need - before, found_in = in_bin[x];
                 before += in_bin[x];
             }
         }
         __syncthreads();
         found |= (uint32_t)found_bin << shift;
-        need = found_need;
-        if (need == found_in) break;                          // every one of the bin
+        need = found_need, left = found_in;
+        if (need == left) break;                              // every one of the bin
+        if (!shared && left <= kFew && pass < 2) {
+            // the few that are left: each counts the larger and the equal ones
+            each_key([&](uint32_t key, int) {
+                if (key >> shift == found >> shift) few_keys[atomicAdd(&few, 1)] = key;
+            });
+            __syncthreads();
+            for (int i = tid; i < left; i += THREADS) {
+                const uint32_t key = few_keys[i];
+                int larger = 0, same = 0;
+                for (int x = 0; x < left; ++x) {
+                    const uint32_t other = few_keys[x];
+                    larger += other > key, same += other == key;
+                }
+                if (larger < need && need <= larger + same)
+                    found_bin = (int)key, found_need = need - larger, found_in = same;
+            }
+            __syncthreads();
+            found = (uint32_t)found_bin, need = found_need, left = found_in;
+            break;
+        }
     }
-    if (need == found_in) --found, need = 0;                  // (found is no score's 0)
+    if (need == left) --found, need = 0;                      // (found is no score's 0)
 
     // ---- how many are above it, or equal to it, before a warp's first item
     int n_above = 0, n_equal = 0;
@@ -171,13 +234,21 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Job j, int blocks
     });
     if (lane == 0) above[warp] = n_above, equal[warp] = n_equal;
     __syncthreads();
-    int at_above = 0, at_equal = 0;
-    for (int w = 0; w < warp; ++w) at_above += above[w], at_equal += equal[w];
-    if (blocks > 1) {
-        if (tid == THREADS - 1) total[0] = at_above + n_above, total[1] = at_equal + n_equal;
+    int all_above, all_equal;
+    const int more_below = scan(lane < WARPS ? above[lane] : 0, &all_above);
+    const int same_below = scan(lane < WARPS ? equal[lane] : 0, &all_equal);
+    int at_above = __shfl_sync(0xFFFFFFFFu, more_below, warp);
+    int at_equal = __shfl_sync(0xFFFFFFFFu, same_below, warp);
+    if (shared) {
+        if (tid == 0) total[0] = all_above, total[1] = all_equal;
         cluster_sync();
-        for (int r = 0; r < rank; ++r)
-            at_above += cluster_load(&total[0], r), at_equal += cluster_load(&total[1], r);
+        if (rank > 0) {
+            // lane r: block r's
+            const int2 v = lane < rank ? cluster_load(total, lane) : make_int2(0, 0);
+            int sum_above, sum_equal;
+            scan(v.x, &sum_above), scan(v.y, &sum_equal);
+            at_above += sum_above, at_equal += sum_equal;
+        }
         // (no block ends while another reads its shared memory)
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
@@ -187,27 +258,58 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Job j, int blocks
         const unsigned lower = (1u << lane) - 1;
         const int e = at_equal + __popc(same & lower);
         if (key > found || (key == found && e < need))
-            out[at_above + __popc(more & lower) + min(e, need)] = start + 32 * k + lane;
+            out[at_above + __popc(more & lower) + min(e, need)] = start + 32 * k;
         at_above += __popc(more), at_equal += __popc(same);
     });
-    if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (shared) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int THREADS, bool RESIDENT>
-cudaError_t launch(const Job &job, long long rows, int blocks, cudaStream_t stream) {
+template <int THREADS, int KEYS>
+cudaLaunchConfig_t config(long long rows, int blocks, cudaLaunchAttribute *attr,
+                          cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * blocks));
     cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = blocks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = blocks > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, select_kernel<THREADS, RESIDENT>, job, blocks);
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+template <int THREADS, int KEYS>
+cudaError_t launch(const Job &job, long long rows, int blocks, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config<THREADS, KEYS>(rows, blocks, attr, stream);
+    if (blocks == 1) cfg.attrs = attr + 1, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, select_kernel<THREADS, KEYS>, job, blocks);
+}
+
+// Clusters of `blocks` blocks that the device runs at a time (0: it does not say),
+// kept by device.
+int clusters_held(int blocks) {
+    static std::atomic<int> kept[64][4] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int size = blocks == 8 ? 3 : blocks == 4 ? 2 : blocks == 2 ? 1 : 0;
+    if (dev >= 0 && dev < 64) {
+        const int v = kept[dev][size].load(std::memory_order_relaxed);
+        if (v > 0) return v;
+    }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config<1024, 32>(1, blocks, attr, nullptr);
+    cfg.numAttrs = 1;
+    int v = 0;
+    if (cudaOccupancyMaxActiveClusters(&v, select_kernel<1024, 32>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev >= 0 && dev < 64) kept[dev][size].store(v, std::memory_order_relaxed);
+    return v;
 }
 
 }  // namespace
@@ -217,11 +319,18 @@ cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
                           int32_t *index, int32_t *counts, cudaStream_t stream) {
     const Job job = {scores, lens, index, counts, heads, columns, unit, first, last, count};
     const long long rows = (long long)seqs * heads;
-    if (columns <= 256 * kKeys) return launch<256, true>(job, rows, 1, stream);
-    int blocks = 1;
-    while (blocks < 8 && (long long)blocks * 1024 * kKeys < columns) blocks *= 2;
-    return columns <= blocks * 1024 * kKeys ? launch<1024, true>(job, rows, blocks, stream)
-                                            : launch<1024, false>(job, rows, blocks, stream);
+    if (columns <= 256 * 8) return launch<256, 8>(job, rows, 1, stream);
+    if (columns <= 512 * 8) return launch<512, 8>(job, rows, 1, stream);
+    // the largest cluster of which the device runs all rows' at a time, as long as a
+    // block has 4096 items; or the smallest one that keeps a row in registers
+    int blocks = 8;
+    while (blocks > 1 && (columns <= 2048 * blocks || rows > clusters_held(blocks))) blocks /= 2;
+    while (blocks < 8 && columns > 32 * 1024 * blocks) blocks *= 2;
+    const int each = (columns + blocks - 1) / blocks;
+    return each <= 1024 * 8    ? launch<1024, 8>(job, rows, blocks, stream)
+           : each <= 1024 * 16 ? launch<1024, 16>(job, rows, blocks, stream)
+           : each <= 1024 * 32 ? launch<1024, 32>(job, rows, blocks, stream)
+                               : launch<1024, 0>(job, rows, blocks, stream);
 }
 
 }  // namespace w4

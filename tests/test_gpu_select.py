@@ -51,7 +51,8 @@ def check(w4, scores, lens, count, unit=1, first=0, last=0, **kw):
 
 
 @pytest.mark.parametrize("columns", [1, 2, 31, 33, 255, 257, 1000, 4095, 4096, 4097, 8191, 16384,
-                                     16385, 32768, 32769, 65537, 131072, 131073, 200001])
+                                     16385, 32768, 32769, 65537, 131072, 131073, 200001, 262144,
+                                     262145, 300001])
 def test_row_lengths(w4, columns):
     rng = np.random.default_rng(columns)
     B, H = (5, 3) if columns < 20000 else (2, 2)
@@ -63,7 +64,7 @@ def test_row_lengths(w4, columns):
         check(w4, scores, lens, count, first=min(4, count // 2), last=count // 3)
 
 
-@pytest.mark.parametrize("columns", [700, 9000, 40000, 150000])
+@pytest.mark.parametrize("columns", [700, 3000, 9000, 40000, 150000, 270000])
 @pytest.mark.parametrize("kind", ["equal", "few", "zeros", "special", "decades", "negative",
                                   "close"])
 def test_score_values(w4, columns, kind):
@@ -108,6 +109,13 @@ def test_many_rows(w4):
     rng = np.random.default_rng(1)
     lens = rng.integers(0, 300, 500).tolist()
     check(w4, rng.standard_normal((500, 4, 300)).astype(np.float32), lens, 16, first=1, last=2)
+
+
+def test_many_long_rows(w4):
+    """More rows than the device has clusters for at a time."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(9000, 40001, 60).tolist()
+    check(w4, rng.integers(0, 9000, (60, 2, 40000)).astype(np.float32), lens, 700, first=1, last=2)
 
 
 def test_stream_graph_and_repeats(w4):
