@@ -3,15 +3,16 @@
 // A score becomes an unsigned key in the scores' order.  The count-th largest key
 // is found digit by digit (11, 11 and 10 bits): a histogram of the keys that
 // share the digits found so far, and a sum over its bins from the top until
-// `count` is reached.  Once few keys are left in the bin where it is, they are
-// compared with one another instead.  Then an item is chosen if its key is above
+// `count` is reached.  As soon as few enough keys are left in the bin where it is,
+// they are listed and the other digits found among those; once very few are, they
+// are compared with one another instead.  Then an item is chosen if its key is above
 // that one, or equal to it and among the first of those; how many are chosen before
 // it is its place in the list, so nothing is sorted.
 //
-// A row's keys stay in registers through all passes.  Long rows are shared by a
-// cluster of up to 8 blocks, which add up each other's histograms through
-// distributed shared memory; rows of more than 262144 items are read again by each
-// pass.
+// A row's keys stay in registers from beginning to end.  Long rows are shared by a
+// cluster of up to 8 blocks, which add up each other's histograms, and read each
+// other's listed keys, through distributed shared memory; rows of more than 262144
+// items are read again by each pass.
 #include <atomic>
 
 #include "w4_device.cuh"
@@ -21,6 +22,7 @@ namespace w4 {
 namespace {
 
 constexpr int kBins = 2048;
+constexpr int kListed = 4096;             // keys of a block that are listed
 constexpr int kFew = 256;                 // keys that are compared with one another
 constexpr uint32_t kAlways = 0xFFFFFFFFu, kNan = 0xFFFFFFFEu;
 
@@ -36,12 +38,11 @@ __device__ __forceinline__ int items_of(const Job &j, int b) {
     return min(len / j.unit + (len % j.unit != 0), j.columns);
 }
 
-// Larger scores have larger keys, -0 and 0 the same one, NaN the largest.  (0 is
-// no score's key.)
+// Larger scores have larger keys, -0 and 0 the same one, NaN (of which a sum is
+// 0x7FFFFFFF) the largest.  0 is no score's key.
 __device__ __forceinline__ uint32_t key_of(float s) {
     const uint32_t b = __float_as_uint(s + 0.f);
-    if (s != s) return kNan;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    return min(b ^ ((uint32_t)((int)b >> 31) | 0x80000000u), kNan);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -69,6 +70,15 @@ __device__ __forceinline__ int2 cluster_load(const int *p, int rank) {
     return r;
 }
 
+__device__ __forceinline__ int cluster_load1(const int *p, int rank) {
+    int r;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                 : "=r"(r)
+                 : "r"(cluster_address(p, rank))
+                 : "memory");
+    return r;
+}
+
 // What lanes below this one have, and all of them.
 __device__ __forceinline__ int scan(int v, int *all) {
     const int lane = threadIdx.x & 31;
@@ -91,12 +101,12 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
     __shared__ __align__(16) int hist[3][kBins];
     __shared__ int sums[WARPS], above[WARPS], equal[WARPS];
     __shared__ __align__(8) int total[2];
-    __shared__ int found_bin, found_need, found_in, few;
-    __shared__ uint32_t few_keys[kFew];
+    __shared__ int found_bin, found_need, found_in, found_most, listed, few;
+    __shared__ uint32_t list[kListed], few_keys[kFew];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < 3 * kBins / 4; i += THREADS)
         reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
-    if (tid == 0) few = 0;
+    if (tid == 0) listed = few = 0;
     begin_after_previous();
     const bool shared = SHARED && blocks > 1;
     const int rank = shared ? cluster_rank() : 0;
@@ -115,13 +125,20 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
     const auto key_at = [&](int i, float v) -> uint32_t {
         return i >= n ? 0u : i < j.first || i >= n - j.last ? kAlways : key_of(v);
     };
+    // (all of a warp's items have scores that count)
+    const bool inner = start - lane >= j.first && start - lane + 32 * rounds <= n - j.last;
     uint32_t keys[KEYS > 0 ? KEYS : 1];
     if constexpr (KEYS > 0) {
         float v[KEYS];                                        // all under way together
 #pragma unroll
         for (int k = 0; k < KEYS; ++k) v[k] = in[min(start + 32 * k, n - 1)];
+        if (inner) {
 #pragma unroll
-        for (int k = 0; k < KEYS; ++k) keys[k] = k < rounds ? key_at(start + 32 * k, v[k]) : 0u;
+            for (int k = 0; k < KEYS; ++k) keys[k] = k < rounds ? key_of(v[k]) : 0u;
+        } else {
+#pragma unroll
+            for (int k = 0; k < KEYS; ++k) keys[k] = k < rounds ? key_at(start + 32 * k, v[k]) : 0u;
+        }
     }
     // f(key) of each of the thread's items, all lanes of a warp together
     const auto each_key = [&](auto f) {
@@ -138,50 +155,78 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
     };
 
     // ---- the count-th largest key, and how many equal to it are chosen
-    uint32_t found = 0;                                       // its upper digits
+    constexpr int LEFT = kListed / (THREADS < 512 ? 512 : THREADS);
+    uint32_t found = 0, mine_left[LEFT];                      // its upper digits
     int need = j.count, shift = 32, left = n;
+    bool in_list = false;
     __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int bits = pass < 2 ? 11 : 10, top = shift;
         shift -= bits;
         int *h = hist[pass];
-        each_key([&](uint32_t key, int) {
-            const bool counts = top == 32 || key >> top == found >> top;
-            const int bin = counts ? (int)(key >> shift & ((1u << bits) - 1)) : -1;
-            if (__all_sync(0xFFFFFFFFu, bin == __shfl_sync(0xFFFFFFFFu, bin, 0))) {
-                // often, where many scores are equal
-                if (lane == 0 && counts) atomicAdd(&h[bin], 32);
-            } else if (counts) {
-                atomicAdd(&h[bin], 1);
+        const bool together = shared && !in_list;             // all blocks' keys
+        const auto add = [&](uint32_t key, int n_same) {
+            atomicAdd(&h[key >> shift & ((1u << bits) - 1)], n_same);
+        };
+        if (in_list) {
+#pragma unroll
+            for (int k = 0; k < LEFT; ++k)
+                if (mine_left[k] != 0u && mine_left[k] >> top == found >> top) add(mine_left[k], 1);
+        } else {
+            // (a warp whose keys all fall into one bin, as where all scores are
+            // equal, does not add them one after another)
+            uint32_t ones = 0u, zeros = 0u;
+            if constexpr (KEYS > 0) {
+                each_key([&](uint32_t key, int) { ones |= key, zeros |= ~key; });
+                ones = __reduce_or_sync(0xFFFFFFFFu, ones);
+                zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
             }
-        });
-        if (shared)
+            if (KEYS > 0 && (ones & zeros) >> shift == 0u) {
+                if (lane == 0 && (top == 32 || ones >> top == found >> top)) add(ones, 32 * rounds);
+            } else if (top == 32) {
+                each_key([&](uint32_t key, int) { add(key, 1); });
+            } else {
+                each_key([&](uint32_t key, int) {
+                    if (key >> top == found >> top) add(key, 1);
+                });
+            }
+        }
+        if (together)
             cluster_sync();
         else
             __syncthreads();
         // thread t: bins from the top, EACH of them
         const int bin0 = kBins - (tid + 1) * EACH;
-        int in_bin[EACH], mine = 0, whole;
+        int in_bin[EACH], most[EACH], mine = 0, whole;        // most: of any block
         if constexpr (SHARED) {
             static_assert(!SHARED || EACH == 2, "a pair of bins a thread");
-            int2 part[8];
+            const int2 own = *reinterpret_cast<const int2 *>(&h[bin0]);
+            in_bin[0] = most[0] = own.x, in_bin[1] = most[1] = own.y;
+            if (together) {
+                int2 part[7];                                 // of the blocks after this one
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                part[r] = make_int2(0, 0);
-                if (!shared && r == 0)
-                    part[0] = *reinterpret_cast<const int2 *>(&h[bin0]);
-                else if (shared && r < blocks)
-                    part[r] = cluster_load(&h[bin0], r);
+                for (int r = 1; r < 8; ++r)
+                    if (r < blocks) {
+                        const int other = rank + r;
+                        part[r - 1] = cluster_load(&h[bin0], other < blocks ? other : other - blocks);
+                    }
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < blocks) {
+                        in_bin[0] += part[r - 1].x, in_bin[1] += part[r - 1].y;
+                        most[0] = max(most[0], part[r - 1].x);
+                        most[1] = max(most[1], part[r - 1].y);
+                    }
             }
-            in_bin[0] = in_bin[1] = 0;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) in_bin[0] += part[r].x, in_bin[1] += part[r].y;
         } else {
 #pragma unroll
-            for (int x = 0; x < EACH; x += 4)
-                *reinterpret_cast<int4 *>(&in_bin[x]) =
-                    *reinterpret_cast<const int4 *>(&h[bin0 + x]);
+            for (int x = 0; x < EACH; x += 4) {
+                const int4 v = *reinterpret_cast<const int4 *>(&h[bin0 + x]);
+                in_bin[x] = v.x, in_bin[x + 1] = v.y, in_bin[x + 2] = v.z, in_bin[x + 3] = v.w;
+            }
+#pragma unroll
+            for (int x = 0; x < EACH; ++x) most[x] = in_bin[x];
         }
 #pragma unroll
         for (int x = 0; x < EACH; ++x) mine += in_bin[x];
@@ -194,24 +239,61 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
         if (before < need && need <= before + mine) {
 #pragma unroll
             for (int x = EACH - 1; x >= 0; --x) {
-                if (before < need && need <= before + in_bin[x])
-                    found_bin = bin0 + x, found_need = need - before, found_in = in_bin[x];
+                if (before < need && need <= before + in_bin[x]) {
+                    found_bin = bin0 + x, found_need = need - before;
+                    found_in = in_bin[x], found_most = most[x];
+                }
                 before += in_bin[x];
             }
         }
         __syncthreads();
         found |= (uint32_t)found_bin << shift;
         need = found_need, left = found_in;
-        if (need == left) break;                              // every one of the bin
-        if (!shared && left <= kFew && pass < 2) {
-            // the few that are left: each counts the larger and the equal ones
+        if (need == left || pass == 2) break;                 // every one of the bin
+        if (!in_list && left <= LEFT * THREADS && found_most <= kListed) {
+            in_list = true;
             each_key([&](uint32_t key, int) {
-                if (key >> shift == found >> shift) few_keys[atomicAdd(&few, 1)] = key;
+                if (key >> shift == found >> shift) list[atomicAdd(&listed, 1)] = key;
             });
+            if (shared)
+                cluster_sync();
+            else
+                __syncthreads();
+            // the keys of all blocks, one block's after another's
+            int upto = shared && lane < blocks ? cluster_load1(&listed, lane) : 0;
+            if (shared) {
+                int all_of;
+                upto += scan(upto, &all_of);                  // lane r: of blocks 0 .. r
+            }
+#pragma unroll
+            for (int k = 0; k < LEFT; ++k) {
+                const int i = tid + k * THREADS;
+                mine_left[k] = 0u;
+                if (!shared) {
+                    if (i < left) mine_left[k] = list[i];
+                    continue;
+                }
+                int r = 0, from = 0;
+                for (int x = 0; x < blocks - 1; ++x) {
+                    const int end = __shfl_sync(0xFFFFFFFFu, upto, x);
+                    if (i >= end) r = x + 1, from = end;
+                }
+                if (i < left)
+                    mine_left[k] =
+                        (uint32_t)cluster_load1(reinterpret_cast<const int *>(&list[i - from]), r);
+            }
+        }
+        if (in_list && left <= kFew) {
+            // each of the few counts the larger and the equal ones
+#pragma unroll
+            for (int k = 0; k < LEFT; ++k)
+                if (mine_left[k] != 0u && mine_left[k] >> shift == found >> shift)
+                    few_keys[atomicAdd(&few, 1)] = mine_left[k];
             __syncthreads();
-            for (int i = tid; i < left; i += THREADS) {
-                const uint32_t key = few_keys[i];
+            if (tid < left) {
+                const uint32_t key = few_keys[tid];
                 int larger = 0, same = 0;
+#pragma unroll 4
                 for (int x = 0; x < left; ++x) {
                     const uint32_t other = few_keys[x];
                     larger += other > key, same += other == key;
@@ -230,8 +312,9 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
     int n_above = 0, n_equal = 0;
     each_key([&](uint32_t key, int) {
         n_above += __popc(__ballot_sync(0xFFFFFFFFu, key > found));
-        n_equal += __popc(__ballot_sync(0xFFFFFFFFu, key == found));
+        n_equal += key == found;
     });
+    n_equal = __reduce_add_sync(0xFFFFFFFFu, n_equal);
     if (lane == 0) above[warp] = n_above, equal[warp] = n_equal;
     __syncthreads();
     int all_above, all_equal;
@@ -252,19 +335,28 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
         // (no block ends while another reads its shared memory)
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
-    each_key([&](uint32_t key, int k) {
-        const unsigned more = __ballot_sync(0xFFFFFFFFu, key > found);
-        const unsigned same = __ballot_sync(0xFFFFFFFFu, key == found);
-        const unsigned lower = (1u << lane) - 1;
-        const int e = at_equal + __popc(same & lower);
-        if (key > found || (key == found && e < need))
-            out[at_above + __popc(more & lower) + min(e, need)] = start + 32 * k;
-        at_above += __popc(more), at_equal += __popc(same);
-    });
+    const unsigned lower = (1u << lane) - 1;
+    if (n_equal == 0 || need <= at_equal) {                   // no item here is chosen for equality
+        int32_t *to = out + min(at_equal, need);
+        each_key([&](uint32_t key, int k) {
+            const unsigned more = __ballot_sync(0xFFFFFFFFu, key > found);
+            if (key > found) to[at_above + __popc(more & lower)] = start + 32 * k;
+            at_above += __popc(more);
+        });
+    } else {
+        each_key([&](uint32_t key, int k) {
+            const unsigned more = __ballot_sync(0xFFFFFFFFu, key > found);
+            const unsigned same = __ballot_sync(0xFFFFFFFFu, key == found);
+            const int e = at_equal + __popc(same & lower);
+            if (key > found || (key == found && e < need))
+                out[at_above + __popc(more & lower) + min(e, need)] = start + 32 * k;
+            at_above += __popc(more), at_equal += __popc(same);
+        });
+    }
     if (shared) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int THREADS, int KEYS>
+template <int THREADS>
 cudaLaunchConfig_t config(long long rows, int blocks, cudaLaunchAttribute *attr,
                           cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
@@ -284,7 +376,7 @@ cudaLaunchConfig_t config(long long rows, int blocks, cudaLaunchAttribute *attr,
 template <int THREADS, int KEYS>
 cudaError_t launch(const Job &job, long long rows, int blocks, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config<THREADS, KEYS>(rows, blocks, attr, stream);
+    cudaLaunchConfig_t cfg = config<THREADS>(rows, blocks, attr, stream);
     if (blocks == 1) cfg.attrs = attr + 1, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, select_kernel<THREADS, KEYS>, job, blocks);
 }
@@ -292,23 +384,22 @@ cudaError_t launch(const Job &job, long long rows, int blocks, cudaStream_t stre
 // Clusters of `blocks` blocks that the device runs at a time (0: it does not say),
 // kept by device.
 int clusters_held(int blocks) {
-    static std::atomic<int> kept[64][4] = {};
+    static std::atomic<int> kept[64][9] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const int size = blocks == 8 ? 3 : blocks == 4 ? 2 : blocks == 2 ? 1 : 0;
     if (dev >= 0 && dev < 64) {
-        const int v = kept[dev][size].load(std::memory_order_relaxed);
+        const int v = kept[dev][blocks].load(std::memory_order_relaxed);
         if (v > 0) return v;
     }
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config<1024, 32>(1, blocks, attr, nullptr);
+    cudaLaunchConfig_t cfg = config<1024>(1, blocks, attr, nullptr);
     cfg.numAttrs = 1;
     int v = 0;
     if (cudaOccupancyMaxActiveClusters(&v, select_kernel<1024, 32>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
-    if (dev >= 0 && dev < 64) kept[dev][size].store(v, std::memory_order_relaxed);
+    if (dev >= 0 && dev < 64) kept[dev][blocks].store(v, std::memory_order_relaxed);
     return v;
 }
 
@@ -324,11 +415,12 @@ cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
     // the largest cluster of which the device runs all rows' at a time, as long as a
     // block has 4096 items; or the smallest one that keeps a row in registers
     int blocks = 8;
-    while (blocks > 1 && (columns <= 2048 * blocks || rows > clusters_held(blocks))) blocks /= 2;
-    while (blocks < 8 && columns > 32 * 1024 * blocks) blocks *= 2;
+    while (blocks > 1 && (columns <= 4096 * (blocks - 1) || rows > clusters_held(blocks))) --blocks;
+    while (blocks < 8 && columns > 32 * 1024 * blocks) ++blocks;
     const int each = (columns + blocks - 1) / blocks;
     return each <= 1024 * 8    ? launch<1024, 8>(job, rows, blocks, stream)
            : each <= 1024 * 16 ? launch<1024, 16>(job, rows, blocks, stream)
+           : each <= 1024 * 20 ? launch<1024, 20>(job, rows, blocks, stream)
            : each <= 1024 * 32 ? launch<1024, 32>(job, rows, blocks, stream)
                                : launch<1024, 0>(job, rows, blocks, stream);
 }
