@@ -133,7 +133,7 @@ cudaError_t launch_kv_gather(const KvPool &from, const KvPool &to, int format, i
                              int num_sms, cudaStream_t stream);
 cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
                           const int32_t *lens, int unit, int first, int last, int count,
-                          int32_t *index, int32_t *counts, cudaStream_t stream);
+                          int32_t *index, int32_t *counts, int num_sms, cudaStream_t stream);
 
 // Launch with programmatic stream serialisation: the grid may start while the
 // previous kernel of the stream drains; every kernel launched this way calls

@@ -390,8 +390,10 @@ w4_status w4_select(const float *scores, int seqs, int heads, int columns, const
                           static_cast<const void *>(index), static_cast<const void *>(counts)})
         if (!p || !aligned(p, 4)) return W4_ERR_INVALID_ARG;
     if ((long long)seqs * heads >= (1LL << 27) || columns >= (1 << 30)) return W4_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (sms <= 0) return W4_ERR_CUDA;
     return cuda_status(w4::launch_select(scores, seqs, heads, columns, lens, unit, first, last,
-                                         count, index, counts,
+                                         count, index, counts, sms,
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -43,33 +43,62 @@ gather_kernel(const KvPool from, const int32_t *lens, const Lists lists, const M
     const KvPool &to = lists.to;
     Share s(lists, to.seqs, to.kv_heads, blockIdx.x * kGatherWarps + (threadIdx.x >> 5),
             gridDim.x * kGatherWarps);
+    // What a lane knows of a unit, asked for while the one before is moved: places
+    // there are, the new page, and the token of place r = lane % 16 with its old page.
+    struct Ahead {
+        int there, page, token, from_page;
+    };
+    const int r = lane & 15;
+    const auto token_of = [&](const Share &s, Ahead &x) {
+        const int first = kRecTokens * s.u;
+        x.there = min(lists.count(s.b) - first, kRecTokens);
+        x.page = to.table[s.b * to.stride + s.u / to.page_records];
+        x.token = -1;
+        if (r < x.there)
+            x.token = m.index[((long long)s.b * to.kv_heads + s.h) * lists.most + first + r];
+    };
+    const auto page_of = [&](const Share &s, Ahead &x) {
+        if (x.token < 0) return;
+        int len = cached_len(from, lens, s.b, from.width * from.page_tokens);
+        if (m.weights) len = min(len, m.columns);
+        if (x.token >= len) {
+            if (from.error) atomicOr(from.error, W4_KV_ERR_POSITION);
+            x.token = -1;
+        } else {
+            x.from_page = from.table[s.b * from.stride + x.token / from.page_tokens];
+        }
+    };
+    Share ahead = s, after = s;
+    Ahead next, third;
+    if (s.left > 0) token_of(s, next), page_of(s, next);
+    after.next(lists, to.kv_heads);
+    if (after.left > 0) token_of(after, third);
     for (; s.left > 0; s.next(lists, to.kv_heads)) {
-        const int first = kRecTokens * s.u, there = min(lists.count(s.b) - first, kRecTokens);
-        const int slot = s.u / to.page_records;
-        char *dst = page_records(to, to.table[s.b * to.stride + slot], s.h, L::kBytes);
+        const Ahead now = next;
+        next = third;
+        ahead = after;
+        if (ahead.left > 0) {
+            page_of(ahead, next);
+            after.next(lists, to.kv_heads);
+            if (after.left > 0) token_of(after, third);
+        }
+        const int first = kRecTokens * s.u, slot = s.u / to.page_records;
+        char *dst = page_records(to, now.page, s.h, L::kBytes);
         if (!dst) continue;
         dst += (s.u - slot * to.page_records) * L::kBytes;
         // lane r (and r + 16): the record that place r's token comes from, and its
         // place there
         const long long row = (long long)s.b * to.kv_heads + s.h;
-        const int r = lane & 15;
         const char *src = nullptr;
         int src_r = r;
-        if (r < there) {
-            const int j = m.index[row * lists.most + first + r];
-            int len = cached_len(from, lens, s.b, from.width * from.page_tokens);
-            if (m.weights) len = min(len, m.columns);
-            if (j >= len) {
-                if (from.error) atomicOr(from.error, W4_KV_ERR_POSITION);
-            } else if (j >= 0) {
-                const int page = j / from.page_tokens, in_page = j - page * from.page_tokens;
-                src = page_records(from, from.table[s.b * from.stride + page], s.h, L::kBytes);
-                if (src) {
-                    src += in_page / kRecTokens * L::kBytes, src_r = in_page % kRecTokens;
-                    if (m.weights && lane < 16)
-                        m.weights_out[row * lists.most + first + r] =
-                            m.weights[row * m.columns + j];
-                }
+        if (now.token >= 0) {
+            const int in_page = now.token % from.page_tokens;
+            src = page_records(from, now.from_page, s.h, L::kBytes);
+            if (src) {
+                src += in_page / kRecTokens * L::kBytes, src_r = in_page % kRecTokens;
+                if (m.weights && lane < 16)
+                    m.weights_out[row * lists.most + first + r] =
+                        m.weights[row * m.columns + now.token];
             }
         }
         const unsigned comes = __ballot_sync(0xFFFFFFFFu, src != nullptr) & 0xFFFFu;

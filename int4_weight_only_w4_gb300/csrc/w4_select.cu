@@ -95,7 +95,8 @@ __device__ __forceinline__ int scan(int v, int *all) {
 // KEYS items a thread, or (0) as many as it takes, which are read again by each
 // pass.  blocks: of a cluster, 1, 2, 4 or 8.
 template <int THREADS, int KEYS>
-__global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blocks) {
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1)
+select_kernel(const Job j, int blocks) {
     constexpr int WARPS = THREADS / 32, EACH = kBins / THREADS;
     constexpr bool SHARED = THREADS == 1024;                  // rows of several blocks
     __shared__ __align__(16) int hist[3][kBins];
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
         return;
     }
     // a block, and a warp of it, has neighbouring items: 32 a round
-    const int rounds = ((n + blocks - 1) / blocks + THREADS - 1) / THREADS;
+    const int rounds =
+        KEYS > 0 ? KEYS : (int)((((long long)n + blocks - 1) / blocks + THREADS - 1) / THREADS);
     const int start = (rank * WARPS + warp) * 32 * rounds + lane;
     const float *in = j.scores + (long long)row * j.columns;
     const auto key_at = [&](int i, float v) -> uint32_t {
@@ -132,20 +134,22 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
         float v[KEYS];                                        // all under way together
 #pragma unroll
         for (int k = 0; k < KEYS; ++k) v[k] = in[min(start + 32 * k, n - 1)];
-        if (inner) {
 #pragma unroll
-            for (int k = 0; k < KEYS; ++k) keys[k] = k < rounds ? key_of(v[k]) : 0u;
-        } else {
+        for (int k = 0; k < KEYS; ++k) keys[k] = key_of(v[k]);
+        if (!inner) {
 #pragma unroll
-            for (int k = 0; k < KEYS; ++k) keys[k] = k < rounds ? key_at(start + 32 * k, v[k]) : 0u;
+            for (int k = 0; k < KEYS; ++k) {
+                const int i = start + 32 * k;
+                if (i < j.first || i >= n - j.last) keys[k] = kAlways;
+                if (i >= n) keys[k] = 0u;                     // there is no item
+            }
         }
     }
     // f(key) of each of the thread's items, all lanes of a warp together
     const auto each_key = [&](auto f) {
         if constexpr (KEYS > 0) {
 #pragma unroll
-            for (int k = 0; k < KEYS; ++k)
-                if (k < rounds) f(keys[k], k);
+            for (int k = 0; k < KEYS; ++k) f(keys[k], k);
         } else {
             for (int k = 0; k < rounds; ++k) {
                 const int i = start + 32 * k;
@@ -183,9 +187,12 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
                 zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
             }
             if (KEYS > 0 && (ones & zeros) >> shift == 0u) {
-                if (lane == 0 && (top == 32 || ones >> top == found >> top)) add(ones, 32 * rounds);
+                if (lane == 0 && ones != 0u && (top == 32 || ones >> top == found >> top))
+                    add(ones, 32 * rounds);
             } else if (top == 32) {
-                each_key([&](uint32_t key, int) { add(key, 1); });
+                each_key([&](uint32_t key, int) {
+                    if (key != 0u) add(key, 1);
+                });
             } else {
                 each_key([&](uint32_t key, int) {
                     if (key >> top == found >> top) add(key, 1);
@@ -252,35 +259,43 @@ __global__ void __launch_bounds__(THREADS, 1) select_kernel(const Job j, int blo
         if (need == left || pass == 2) break;                 // every one of the bin
         if (!in_list && left <= LEFT * THREADS && found_most <= kListed) {
             in_list = true;
-            each_key([&](uint32_t key, int) {
-                if (key >> shift == found >> shift) list[atomicAdd(&listed, 1)] = key;
-            });
+            int own = 0, whole_warp;
+            each_key([&](uint32_t key, int) { own += key >> shift == found >> shift; });
+            own = scan(own, &whole_warp);
+            int at = 0;
+            if (lane == 0 && whole_warp) at = atomicAdd(&listed, whole_warp);
+            at = __shfl_sync(0xFFFFFFFFu, at, 0) + own;
+            if (whole_warp)
+                each_key([&](uint32_t key, int) {
+                    if (key >> shift == found >> shift) list[at++] = key;
+                });
             if (shared)
                 cluster_sync();
             else
                 __syncthreads();
             // the keys of all blocks, one block's after another's
-            int upto = shared && lane < blocks ? cluster_load1(&listed, lane) : 0;
+            int end[7];
             if (shared) {
-                int all_of;
+                int all_of, upto = lane < blocks ? cluster_load1(&listed, lane) : 0;
                 upto += scan(upto, &all_of);                  // lane r: of blocks 0 .. r
+#pragma unroll
+                for (int x = 0; x < 7; ++x) end[x] = __shfl_sync(0xFFFFFFFFu, upto, x);
             }
 #pragma unroll
             for (int k = 0; k < LEFT; ++k) {
                 const int i = tid + k * THREADS;
                 mine_left[k] = 0u;
+                if (i >= left) continue;
                 if (!shared) {
-                    if (i < left) mine_left[k] = list[i];
+                    mine_left[k] = list[i];
                     continue;
                 }
                 int r = 0, from = 0;
-                for (int x = 0; x < blocks - 1; ++x) {
-                    const int end = __shfl_sync(0xFFFFFFFFu, upto, x);
-                    if (i >= end) r = x + 1, from = end;
-                }
-                if (i < left)
-                    mine_left[k] =
-                        (uint32_t)cluster_load1(reinterpret_cast<const int *>(&list[i - from]), r);
+#pragma unroll
+                for (int x = 0; x < 7; ++x)
+                    if (i >= end[x]) r = x + 1, from = end[x];
+                mine_left[k] =
+                    (uint32_t)cluster_load1(reinterpret_cast<const int *>(&list[i - from]), r);
             }
         }
         if (in_list && left <= kFew) {
@@ -407,11 +422,13 @@ int clusters_held(int blocks) {
 
 cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
                           const int32_t *lens, int unit, int first, int last, int count,
-                          int32_t *index, int32_t *counts, cudaStream_t stream) {
+                          int32_t *index, int32_t *counts, int num_sms, cudaStream_t stream) {
     const Job job = {scores, lens, index, counts, heads, columns, unit, first, last, count};
     const long long rows = (long long)seqs * heads;
+    if (columns <= 256 * 2) return launch<256, 2>(job, rows, 1, stream);
     if (columns <= 256 * 8) return launch<256, 8>(job, rows, 1, stream);
     if (columns <= 512 * 8) return launch<512, 8>(job, rows, 1, stream);
+    if (columns <= 512 * 16 && rows > num_sms) return launch<512, 16>(job, rows, 1, stream);
     // the largest cluster of which the device runs all rows' at a time, as long as a
     // block has 4096 items; or the smallest one that keeps a row in registers
     int blocks = 8;
@@ -420,7 +437,7 @@ cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
     const int each = (columns + blocks - 1) / blocks;
     return each <= 1024 * 8    ? launch<1024, 8>(job, rows, blocks, stream)
            : each <= 1024 * 16 ? launch<1024, 16>(job, rows, blocks, stream)
-           : each <= 1024 * 20 ? launch<1024, 20>(job, rows, blocks, stream)
+           : each <= 1024 * 24 ? launch<1024, 24>(job, rows, blocks, stream)
            : each <= 1024 * 32 ? launch<1024, 32>(job, rows, blocks, stream)
                                : launch<1024, 0>(job, rows, blocks, stream);
 }
