@@ -14,6 +14,10 @@ namespace {
 
 constexpr int kGatherWarps = 4;
 
+// Blocks an SM, by what a lane holds of a record.
+template <int FMT, int D>
+constexpr int kGatherBlocks = D == 64 ? 8 : FMT == W4_KV_BF16 ? 4 : FMT == W4_KV_INT8 ? 5 : 8;
+
 struct Lists {
     KvPool to;                    // the pool, by the table of the new places
     const int32_t *counts;
@@ -35,7 +39,7 @@ struct Moved {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(32 * kGatherWarps)
+__global__ void __launch_bounds__(32 * kGatherWarps, kGatherBlocks<FMT, D>)
 gather_kernel(const KvPool from, const int32_t *lens, const Lists lists, const Moved m) {
     using L = KvLayout<FMT, D>;
     begin_after_previous();
@@ -186,19 +190,23 @@ cudaError_t launch_kv_gather(const KvPool &from, const KvPool &to, int format, i
     const long long room = (long long)to.width * to.page_records,
                     listed = ((long long)most + kRecTokens - 1) / kRecTokens;
     const long long units = (room < listed ? room : listed) * to.seqs * to.kv_heads;
-    const long long blocks = (units + kGatherWarps - 1) / kGatherWarps, limit = 8LL * num_sms;
-    const int grid = (int)(blocks < limit ? blocks : limit);
-    const auto run = [&](auto kernel) {
-        return launch_overlapped(kernel, dim3(grid), dim3(32 * kGatherWarps), 0, stream, from,
-                                 lens, lists, moved);
+    const long long blocks = (units + kGatherWarps - 1) / kGatherWarps;
+    const auto run = [&](auto kernel, int held) {
+        const long long most = (long long)held * num_sms;
+        return launch_overlapped(kernel, dim3((unsigned)(blocks < most ? blocks : most)),
+                                 dim3(32 * kGatherWarps), 0, stream, from, lens, lists, moved);
     };
     if (head_dim == 128)
-        return format == W4_KV_BF16   ? run(gather_kernel<W4_KV_BF16, 128>)
-               : format == W4_KV_INT8 ? run(gather_kernel<W4_KV_INT8, 128>)
-                                      : run(gather_kernel<W4_KV_INT4, 128>);
-    return format == W4_KV_BF16   ? run(gather_kernel<W4_KV_BF16, 64>)
-           : format == W4_KV_INT8 ? run(gather_kernel<W4_KV_INT8, 64>)
-                                  : run(gather_kernel<W4_KV_INT4, 64>);
+        return format == W4_KV_BF16
+                   ? run(gather_kernel<W4_KV_BF16, 128>, kGatherBlocks<W4_KV_BF16, 128>)
+               : format == W4_KV_INT8
+                   ? run(gather_kernel<W4_KV_INT8, 128>, kGatherBlocks<W4_KV_INT8, 128>)
+                   : run(gather_kernel<W4_KV_INT4, 128>, kGatherBlocks<W4_KV_INT4, 128>);
+    return format == W4_KV_BF16
+               ? run(gather_kernel<W4_KV_BF16, 64>, kGatherBlocks<W4_KV_BF16, 64>)
+           : format == W4_KV_INT8
+               ? run(gather_kernel<W4_KV_INT8, 64>, kGatherBlocks<W4_KV_INT8, 64>)
+               : run(gather_kernel<W4_KV_INT4, 64>, kGatherBlocks<W4_KV_INT4, 64>);
 }
 
 }  // namespace w4
