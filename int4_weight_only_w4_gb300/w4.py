@@ -647,20 +647,18 @@ def sparse_attn_f32(cache: "PagedCache", q, out, lens, table, blocks, counts, wo
 
 
 def _filled(t, shape, dtype, what: str) -> int:
-    """Address of a contiguous CUDA tensor of this shape and type."""
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or \
-            not t.is_contiguous():
+    """Address of a contiguous CUDA tensor of this shape (a tuple) and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous {dtype} CUDA tensor {list(shape)}")
     return t.data_ptr()
 
 
-def _new_tokens(cache: "PagedCache", q, table) -> tuple:
-    """(q_heads, new tokens of a sequence) of the queries of a call."""
+def _new_tokens(cache: "PagedCache", q, B: int) -> tuple:
+    """(rows, q_heads, new tokens of a sequence) of the queries of a call."""
     T, H, D = q.shape
-    B = table.shape[0]
     if not B or T % B or D != cache.head_dim:
         raise ValueError("q: expected [seqs * tokens, q_heads, head_dim]")
-    return H, T // B
+    return T, H, T // B
 
 
 def key_bounds(cache: "PagedCache", bounds, lens, table, tokens: int = 1, stream=None) -> None:
@@ -675,11 +673,8 @@ def key_bounds(cache: "PagedCache", bounds, lens, table, tokens: int = 1, stream
 def block_scores(cache: "PagedCache", bounds, q, lens, table, scores, stream=None) -> None:
     """w4_block_scores: how large q . k can be in every block of a sequence,
     float32 [seqs, kv_heads, columns]."""
-    H, M = _new_tokens(cache, q, table)
-    B = table.shape[0]
-    if scores.dim() != 3:
-        raise ValueError("scores: expected float32 [seqs, kv_heads, columns]")
-    columns = scores.shape[2]
+    B, columns = table.shape[0], scores.shape[-1]
+    _, H, M = _new_tokens(cache, q, B)
     _ok(_block_scores(cache.ref, _filled(bounds, cache.bounds_shape, torch.bfloat16, "bounds"),
                       _heads(q), H, M, _int32(lens, B, "lens"), _block_table(table),
                       _filled(scores, (B, cache.kv_heads, columns), torch.float32, "scores"),
@@ -692,11 +687,12 @@ def select(scores, lens, index, counts, unit: int = 1, first: int = 0, last: int
     [seqs, heads, columns], the first `first`, the last `last` and the best others,
     as many as a row of index has (int32 [seqs, heads, count]), ascending; how many
     there are goes into counts, int32 [seqs]."""
-    if scores.dim() != 3 or index.dim() != 3:
-        raise ValueError("scores, index: expected [seqs, heads, columns] and [seqs, heads, count]")
-    B, H, columns = scores.shape
-    count = index.shape[2]
-    _ok(_select(_filled(scores, (B, H, columns), torch.float32, "scores"), B, H, columns,
+    shape = scores.shape
+    if len(shape) != 3:
+        raise ValueError("scores: expected float32 [seqs, heads, columns]")
+    B, H, columns = shape
+    count = index.shape[-1]
+    _ok(_select(_filled(scores, shape, torch.float32, "scores"), B, H, columns,
                 _int32(lens, B, "lens"), unit, first, last, count,
                 _filled(index, (B, H, count), torch.int32, "index"),
                 _int32(counts, B, "counts"), _raw_stream(stream, scores)), "w4_select")
@@ -707,17 +703,15 @@ def attn_weights(cache: "PagedCache", q, lse, lens, table, weights, before=None,
     """w4_attn_weights: weights, float32 [seqs, kv_heads, columns], = decay * before (may
     be weights; None: 0) + what every cached token gets of the new tokens' attention,
     whose log-sum-exp is lse, float32 [seqs * tokens, q_heads]."""
-    H, M = _new_tokens(cache, q, table)
-    T, B, shape = q.shape[0], table.shape[0], weights.shape
-    if len(shape) != 3:
-        raise ValueError("weights: expected float32 [seqs, kv_heads, columns]")
-    expected = (B, cache.kv_heads, shape[2])
+    B, columns = table.shape[0], weights.shape[-1]
+    T, H, M = _new_tokens(cache, q, B)
+    expected = (B, cache.kv_heads, columns)
     _ok(_attn_weights(cache.ref, _heads(q), _filled(lse, (T, H), torch.float32, "lse"), H, M,
                       _int32(lens, B, "lens"), _block_table(table),
                       q.shape[2] ** -0.5 if scale is None else scale, window,
                       before if before is None else
                       _filled(before, expected, torch.float32, "before"), decay,
-                      _filled(weights, expected, torch.float32, "weights"), shape[2],
+                      _filled(weights, expected, torch.float32, "weights"), columns,
                       _raw_stream(stream, q)), "w4_attn_weights")
 
 
