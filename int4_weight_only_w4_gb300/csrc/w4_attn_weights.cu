@@ -10,8 +10,6 @@
 // tensor cores' column operands; its warps take every eighth record of the block's
 // stretch, each through a ring of its own that asynchronous copies fill, across the
 // heads' borders, with the records' keys and what their tokens had before.
-#include <limits.h>
-
 #include <atomic>
 
 #include "w4_attn_query.cuh"
@@ -137,6 +135,7 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
     constexpr unsigned FIRST = R == 4 ? 0x01010101u : R == 2 ? 0x00010001u : 1u;
     unsigned valid = 0;
     int page = -1, ahead_len = 0, seen_b = -1;
+    bool wanted = false;
     const int part = lane % LANES, own = lane / LANES;
     const auto look = [&]() {                                 // the page of the next record
         if (ahead.left <= 0) return;
@@ -144,16 +143,16 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
         const int r = R * ahead.u + own;
         // (no row sees a key before the window of the first one)
         const int upto = kRecTokens * (r + 1);
-        const bool there = upto - kRecTokens < ahead_len &&
-                           (a.window == 0 || upto > ahead_len - a.tokens - a.window + 1);
-        page = there ? a.pool.table[ahead.b * a.pool.stride + page_slot(a.pool, r)] : INT_MIN;
+        wanted = upto - kRecTokens < ahead_len &&
+                 (a.window == 0 || upto > ahead_len - a.tokens - a.window + 1);
+        if (wanted) page = a.pool.table[ahead.b * a.pool.stride + page_slot(a.pool, r)];
     };
     const auto fetch = [&](int put) {
         if (ahead.left > 0) {
             const uint32_t to = ring + put * S::kBytes;
             const int r = R * ahead.u + own;
             const char *rec = nullptr;
-            if (page != INT_MIN) rec = page_records(a.pool, page, ahead.h, L::kBytes);
+            if (wanted) rec = page_records(a.pool, page, ahead.h, L::kBytes);
             valid = (valid & ~(FIRST << put)) |
                     (__ballot_sync(0xFFFFFFFFu, rec != nullptr) & FIRST) << put;
             if (rec) {

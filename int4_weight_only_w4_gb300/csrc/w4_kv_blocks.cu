@@ -231,7 +231,8 @@ scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q
                 reinterpret_cast<const __nv_bfloat16 *>(q.data) +
                 (long long)(s.b * tokens + i) * q.token_stride +
                 (long long)(s.h * group + r - i * group) * q.head_stride) + t;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            // (two sums: half as many products wait for one another, and each rounds less)
+            float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < PIECES; ++j) {
                 const uint4 v = __ldg(row + 4 * j);
@@ -243,7 +244,7 @@ scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q
                 for (int z = 0; z < 2; ++z) {
                     const uint4 &k0 = a[z][0][j], &k1 = a[z][1][j], &b = z ? down : up;
                     mma_bf16_16816(d, k0.x, k1.x, k0.y, k1.y, b.x, b.y);
-                    mma_bf16_16816(d, k0.z, k1.z, k0.w, k1.w, b.z, b.w);
+                    mma_bf16_16816(e, k0.z, k1.z, k0.w, k1.w, b.z, b.w);
                 }
             }
 #pragma unroll
@@ -251,7 +252,7 @@ scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q
                 // (columns past the last row repeat it)
                 const int rc = min(r0 + 2 * t + (c & 1), rows - 1);
                 const int ic = group == 1 ? rc : (int)__umulhi((unsigned)rc, group_magic);
-                const float v = fabsf(d[c]) < INFINITY ? d[c] : INFINITY;
+                const float sum = d[c] + e[c], v = fabsf(sum) < INFINITY ? sum : INFINITY;
                 if (len - tokens + ic >= 0) best[c >> 1] = fmaxf(best[c >> 1], v);
             }
         }

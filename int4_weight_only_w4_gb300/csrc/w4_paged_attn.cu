@@ -687,24 +687,39 @@ __device__ __forceinline__ void copy_records(const AttnArgs &a, const Plan &plan
         const int h = c.item / plan.row_tiles;
         const int32_t *pages = a.pool.table + (more ? c.b : 0) * a.pool.stride;
         constexpr int AHEAD = 4;
-        int page[AHEAD], block[LISTED ? AHEAD : 1];
+        int page[AHEAD];
+        // LISTED: the block of page[x]; and the numbers of the one after, and of that
+        // before it in the list, asked for as much earlier again
+        constexpr int LISTS = LISTED ? AHEAD : 1;
+        int block[LISTS], asked[LISTS], before[LISTS];
         const int32_t *blocks = nullptr;
         if constexpr (LISTED)
             blocks = a.blocks + ((long long)(more ? c.b : 0) * a.pool.kv_heads + h) * a.most;
+        const auto ask = [&](int x, int u) {
+            asked[x] = before[x] = -1;
+            if (u < stop && kg < KG) {
+                const int slot = page_slot(a.pool, u);
+                asked[x] = blocks[slot];
+                if (slot > 0) before[x] = blocks[slot - 1];
+            }
+        };
         const auto fetch = [&](int x, int u) {
             if constexpr (LISTED) {
-                block[x] = -1, page[x] = -1;
-                if (u < stop && kg < KG) {
-                    const int slot = page_slot(a.pool, u), k = blocks[slot];
-                    const int last = slot > 0 ? blocks[slot - 1] : -1;
-                    if (k > last && k >= 0 && (long long)k * a.pool.page_tokens < seq.len)
-                        block[x] = k, page[x] = pages[k];
-                }
+                const int k = asked[x];
+                const bool valid = u < stop && k > before[x] && k >= 0 &&
+                                   (long long)k * a.pool.page_tokens < seq.len;
+                block[x] = valid ? k : -1;
+                page[x] = valid ? pages[k] : -1;
+                ask(x, u + AHEAD * KG);
             } else {
                 page[x] = u < stop && kg < KG ? pages[page_slot(a.pool, seq.first + u)] : 0;
             }
         };
         if (more) {
+            if constexpr (LISTED) {
+#pragma unroll
+                for (int x = 0; x < AHEAD; ++x) ask(x, c.u + kg + x * KG);
+            }
 #pragma unroll
             for (int x = 0; x < AHEAD; ++x) fetch(x, c.u + kg + x * KG);
         }

@@ -325,10 +325,8 @@ select_kernel(const Job j, int blocks) {
 
     // ---- how many are above it, or equal to it, before a warp's first item
     int n_above = 0, n_equal = 0;
-    each_key([&](uint32_t key, int) {
-        n_above += __popc(__ballot_sync(0xFFFFFFFFu, key > found));
-        n_equal += key == found;
-    });
+    each_key([&](uint32_t key, int) { n_above += key > found, n_equal += key == found; });
+    n_above = __reduce_add_sync(0xFFFFFFFFu, n_above);
     n_equal = __reduce_add_sync(0xFFFFFFFFu, n_equal);
     if (lane == 0) above[warp] = n_above, equal[warp] = n_equal;
     __syncthreads();
