@@ -6,10 +6,20 @@
 // all, and no token needs another one's result: nothing is joined.
 //
 // The blocks divide the list (sequence, head, record) evenly, from the lengths on
-// the device.  A block holds the queries of one head in shared memory as the
-// tensor cores' column operands; its warps take every eighth record of the block's
-// stretch, each through a ring of its own that asynchronous copies fill, across the
-// heads' borders, with the records' keys and what their tokens had before.
+// the device.  A warp takes every fourth unit of 1 to 4 records of its block's
+// stretch through a ring of its own, which asynchronous copies of 16 bytes fill
+// across the heads' borders, with the records' keys and what their tokens had
+// before; a record's lanes find its page.  One tile of 8 rows of queries stays in
+// registers, more of them are shared by the block's warps.
+//
+// Measured (28 query and 4 key/value heads of 128, one new token, captured calls):
+// 32 x 16384 tokens in bf16 86.8 us, 95 % of a copy's rate for keys and weights; 64
+// ragged sequences of up to 8192 in 8 bits 28.3 us (78 %), where the instructions
+// around 2 KB of codes count; in 4 bits 32 x 16384 39.5 us (61 %): conversion and
+// products, 230 instructions a record and warp.  Four blocks of four warps and rings of
+// two stages; two blocks of eight 29.9, 88.4 and 38.8 us; three stages 31.5, 91.9 and
+// 39.5; three blocks of eight at 80 registers 42.3, 88.8 and 56.5 (spills); units of
+// half the size 34.8 and 45.0 in 8 and 4 bits.
 #include <atomic>
 
 #include "w4_attn_query.cuh"
@@ -19,7 +29,9 @@ namespace w4 {
 namespace {
 
 constexpr int kTilesMax = 8;             // tiles of 8 rows that a launch takes
-constexpr int kWeightWarps = 8;          // of a block; two blocks an SM
+constexpr int kWeightWarps = 4;          // of a block
+constexpr int kWeightBlocks = 4;         // an SM
+constexpr int kWeightStages = 2;         // of a warp's ring
 
 struct Weights {
     const float *before;                 // NULL: none
@@ -40,7 +52,7 @@ struct SharedTile {
 
 // A unit is RECS neighbouring records, 4 KB of keys where D is 128: what a warp does
 // at a time.
-template <int FMT, int D, bool ONE>
+template <int FMT, int D>
 struct Stage {
     using L = KvLayout<FMT, D>;
     static constexpr int kRecs = L::kPart >= 4096 ? 1 : L::kPart >= 2048 ? 2 : 4;
@@ -48,7 +60,6 @@ struct Stage {
     // of a stage of a warp's ring: keys, their descriptors, weights before
     static constexpr int kMetaAt = kRecs * L::kPart, kBeforeAt = kMetaAt + 64 * kRecs,
                          kBytes = kBeforeAt + 4 * kTokens;
-    static constexpr int kStages = ONE ? 3 : 2;      // (more rows take longer over a unit)
 };
 
 // Units of a sequence.
@@ -111,17 +122,17 @@ __device__ __forceinline__ void quad_sums(float (&v)[R][2], float (&out)[2]) {
 
 // ONE: one tile of rows, whose operands stay in registers.
 template <int FMT, int D, bool ONE>
-__global__ void __launch_bounds__(32 * kWeightWarps, 2)
+__global__ void __launch_bounds__(32 * kWeightWarps, kWeightBlocks)
 weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
     using L = KvLayout<FMT, D>;
-    using S = Stage<FMT, D, ONE>;
+    using S = Stage<FMT, D>;
     constexpr int KS = D / 16, R = S::kRecs, LANES = 32 / R, WARPS = kWeightWarps;
     extern __shared__ __align__(128) unsigned char smem[];
     SharedTile<D> *tiles = reinterpret_cast<SharedTile<D> *>(smem);
     begin_after_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + n_tiles * (int)sizeof(SharedTile<D>) +
-                          warp * S::kStages * S::kBytes;
+                          warp * kWeightStages * S::kBytes;
     const int rows = a.tokens * a.group, heads = a.pool.kv_heads;
     const Units<S::kTokens> units = {a};
     Share s(units, a.pool.seqs, heads, blockIdx.x, gridDim.x);
@@ -182,7 +193,7 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
     };
     look();
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < kWeightStages - 1; ++i) fetch(i);
 
     int mine = warp;                                          // units until the warp's next one
     int b = 0, h = 0, len = 0, stop = 0, u = 0, stage = 0;
@@ -232,13 +243,13 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
             __syncthreads();
         }
         for (; u < stop; u += WARPS) {
-            copies_wait<S::kStages - 2>();
+            copies_wait<kWeightStages - 2>();
             __syncwarp();                                     // everyone's copies are there, and
                                                               // the stage before is free
             const unsigned here = valid >> stage;
-            fetch(stage == 0 ? S::kStages - 1 : stage - 1);
+            fetch(stage == 0 ? kWeightStages - 1 : stage - 1);
             const uint32_t at_stage = ring + stage * S::kBytes;
-            if (++stage == S::kStages) stage = 0;
+            if (++stage == kWeightStages) stage = 0;
             float sum[R][2];
 #pragma unroll
             for (int x = 0; x < R; ++x) {
@@ -352,9 +363,9 @@ weights_kernel(const AttnArgs a, const Weights out, int n_tiles) {
 template <int FMT, int D, bool ONE>
 cudaError_t launch(const AttnArgs &a, const Weights &out, int n_tiles, int num_sms,
                    cudaStream_t stream) {
-    using S = Stage<FMT, D, ONE>;
+    using S = Stage<FMT, D>;
     const auto bytes = [](int tiles) {
-        return tiles * (int)sizeof(SharedTile<D>) + kWeightWarps * S::kStages * S::kBytes;
+        return tiles * (int)sizeof(SharedTile<D>) + kWeightWarps * kWeightStages * S::kBytes;
     };
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
@@ -369,7 +380,8 @@ cudaError_t launch(const AttnArgs &a, const Weights &out, int n_tiles, int num_s
     const long long most = (long long)(a.most + S::kTokens - 1) / S::kTokens * a.pool.seqs *
                            a.pool.kv_heads;
     const long long blocks = (most + kWeightWarps - 1) / kWeightWarps;
-    const int grid = (int)(blocks < 2 * num_sms ? blocks : 2 * num_sms);
+    const long long held = (long long)kWeightBlocks * num_sms;
+    const int grid = (int)(blocks < held ? blocks : held);
     return launch_overlapped(weights_kernel<FMT, D, ONE>, dim3(grid), dim3(32 * kWeightWarps),
                              bytes(ONE ? 0 : n_tiles), stream, a, out, ONE ? 0 : n_tiles);
 }
