@@ -1,6 +1,6 @@
-// C ABI of the rotary positions, the paged key-value cache and the attention
-// over it (declared in include/w4.h): argument checks on the host, then the
-// launches.  Nothing here allocates device or pinned memory.
+// C ABI of the rotary positions, the paged key-value cache, the attention over it
+// and the calls for long contexts (declared in include/w4.h): argument checks on the
+// host, then the launches.  Nothing here allocates device or pinned memory.
 #include <math.h>
 
 #include <atomic>
