@@ -3,7 +3,9 @@ them rotary positions, the paged cache and the attention over it.
 
     qkv   = W_qkv norm(x)                 w4_gemv
     cache <- rotate(k), v; q <- rotate(q) w4_kv_append   (one launch)
-    a     = attention(q, cache)           w4_paged_attn
+    a     = attention(q, cache)           w4_paged_attn, or over the blocks that a bound of
+                                          q k selects: w4_key_bounds, w4_block_scores,
+                                          w4_select, w4_sparse_attn
     x     = x + W_o a                     w4_gemv
     x     = x + W_down swiglu(W_gate_up norm(x))   w4_gemv_swiglu, w4_gemv
 
@@ -16,6 +18,7 @@ workloads.
 
     python examples/decode_layer.py [--shape 0.5b|7b] [--cache bf16|int8|int4]
                                     [--seqs 4] [--prompt 100] [--steps 16] [--draft 1]
+                                    [--blocks 0]
 """
 from __future__ import annotations
 
@@ -63,10 +66,12 @@ def _norm(x: torch.Tensor) -> torch.Tensor:
 
 class Layer:
     """The layer's weights, its rotation table and its cache with a block table
-    of `seqs` sequences of up to `longest` tokens."""
+    of `seqs` sequences of up to `longest` tokens.  blocks: how many pages of each head
+    a step looks at (0: all; otherwise 3 or more, the first one and the last two among
+    them, in which the new tokens are)."""
 
     def __init__(self, shape: Shape, fmt: str, seqs: int, longest: int, page_tokens: int = 16,
-                 seed: int = 0):
+                 seed: int = 0, blocks: int = 0):
         s = self.shape = shape
         qkv = (s.q_heads + 2 * s.kv_heads) * s.head_dim
         self.qkv = w4.pack(*_canonical("layer.qkv", s.hidden, qkv, seed), s.hidden, qkv)
@@ -82,6 +87,11 @@ class Layer:
         gen = torch.Generator().manual_seed(seed)
         self.table = torch.randperm(seqs * pages, generator=gen).view(seqs, pages)
         self.table = self.table.to(torch.int32).cuda()
+        self.blocks = blocks
+        if blocks:
+            self.bounds = self.cache.new_bounds()
+            self.chosen = torch.zeros(seqs, s.kv_heads, blocks, dtype=torch.int32, device="cuda")
+            self.counts = torch.zeros(seqs, dtype=torch.int32, device="cuda")
 
     def _product(self, weight, x: torch.Tensor) -> torch.Tensor:
         """weight.gemv over any number of rows, 8 at a time."""
@@ -96,18 +106,26 @@ class Layer:
         q, k, v = rows.split([s.q_heads, s.kv_heads, s.kv_heads], 1)
         positions = (lens[:, None] - M + torch.arange(M, device=lens.device, dtype=torch.int32))
         self.cache.append(k, v, positions.reshape(-1), self.table, q=q, q_out=q, rope=self.rope)
-        a, _ = self.cache.attend(q, lens, self.table)
+        if self.blocks:
+            self.cache.key_bounds(self.bounds, lens, self.table, tokens=M)
+            scores = self.cache.block_scores(self.bounds, q, lens, self.table)
+            w4.select(scores, lens, self.chosen, self.counts, unit=self.cache.page_tokens, first=1,
+                      last=2)
+            a, _ = self.cache.attend_blocks(q, lens, self.table, self.chosen, self.counts)
+        else:
+            a, _ = self.cache.attend(q, lens, self.table)
         x = x + self._product(self.o, a.view(B * M, -1))
         return x + self._product(self.down, self._product(self.gate_up, _norm(x)))
 
 
 def run(shape: str = "0.5b", fmt: str = "int4", seqs: int = 4, prompt: int = 100, steps: int = 16,
-        draft: int = 1, seed: int = 0):
-    """The layer over a prompt and `steps` more tokens, `draft` at a time.
+        draft: int = 1, seed: int = 0, blocks: int = 0):
+    """The layer over a prompt and `steps` more tokens, `draft` at a time, each step
+    over `blocks` pages of every head (0: all).
     Returns its outputs [seqs, prompt + steps, hidden] and the seconds of a step."""
     s = SHAPES[shape]
     total = prompt + steps
-    layer = Layer(s, fmt, seqs, total, seed=seed)
+    layer = Layer(s, fmt, seqs, total, seed=seed, blocks=blocks)
     gen = torch.Generator(device="cuda").manual_seed(seed)
     x = torch.randn(seqs, total, s.hidden, generator=gen, device="cuda").to(torch.bfloat16)
     out = torch.empty_like(x)
@@ -134,12 +152,13 @@ def main() -> None:
     p.add_argument("--prompt", type=int, default=100)
     p.add_argument("--steps", type=int, default=16)
     p.add_argument("--draft", type=int, default=1)
+    p.add_argument("--blocks", type=int, default=0, help="pages a step looks at (0: all)")
     a = p.parse_args()
     exact, _ = run(a.shape, "bf16", a.seqs, a.prompt, a.steps, 1)
-    out, took = run(a.shape, a.cache, a.seqs, a.prompt, a.steps, a.draft)
+    out, took = run(a.shape, a.cache, a.seqs, a.prompt, a.steps, a.draft, blocks=a.blocks)
     off = (out.float() - exact.float()).norm() / exact.float().norm()
     print(f"{a.shape} layer, {a.seqs} sequences, {a.prompt} + {a.steps} tokens, {a.cache} cache, "
-          f"{a.draft} a step: {1e6 * took:.0f} us the last step, "
+          f"{a.draft} a step{f', {a.blocks} blocks' if a.blocks else ''}: {1e6 * took:.0f} us the last step, "
           f"{off:.2e} from single steps over a bf16 cache")
 
 

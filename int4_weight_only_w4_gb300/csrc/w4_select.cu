@@ -104,7 +104,7 @@ __device__ __forceinline__ int scan(int v, int *all) {
 }
 
 // KEYS items a thread, or (0) as many as it takes, which are read again by each
-// pass.  blocks: of a cluster, 1, 2, 4 or 8.
+// pass.  blocks: of a cluster, up to 8.
 template <int THREADS, int KEYS>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1)
 select_kernel(const Job j, int blocks) {

@@ -2,6 +2,7 @@
 ordinary step asks for: tables much wider than the sequences, many sequences, wide
 groups, large pages, first calls of a process under capture, graphs replayed side by
 side, one list for lengths and counts."""
+import importlib.util
 import os
 import subprocess
 import sys
@@ -124,6 +125,26 @@ def test_counts_are_the_new_lengths(w4):
         assert torch.equal(out[b, :, :n], w[b].gather(1, index[b, :, :n].long()))
         assert (out[b, :, n:] == 0).all()
     m.cache.check()
+
+
+@pytest.mark.parametrize("draft", [1, 3])
+def test_a_layer_over_selected_blocks(draft):
+    """The example's layer: with as many blocks as there are it is the whole layer up to
+    the order of sums; with few it runs."""
+    spec = importlib.util.spec_from_file_location(
+        "decode_layer", os.path.join(ROOT, "examples", "decode_layer.py"))
+    ex = sys.modules[spec.name] = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    whole, _ = ex.run("0.5b", "bf16", seqs=2, prompt=90, steps=6, draft=draft)
+    all_blocks, _ = ex.run("0.5b", "bf16", seqs=2, prompt=90, steps=6, draft=draft, blocks=6)
+    few, _ = ex.run("0.5b", "bf16", seqs=2, prompt=90, steps=6, draft=draft, blocks=3)
+    # the attention's outputs differ by a rounding to bf16 that falls the other way, 2^-8
+    # of a value at most and of few values; the products after it keep its size or less
+    # beside the residual sum
+    off = (all_blocks.float() - whole.float()).norm() / whole.float().norm()
+    assert off <= 2.0 ** -8
+    assert torch.isfinite(few.float()).all()
+    assert torch.equal(few[:, :48], all_blocks[:, :48])    # three blocks: all of them
 
 
 def _all_calls(w4):
