@@ -191,15 +191,22 @@ select_kernel(const Job j, int blocks) {
         } else {
             // (a warp whose keys all fall into one bin, as where all scores are
             // equal, does not add them one after another)
-            uint32_t ones = 0u, zeros = 0u;
+            bool alike = false;
             if constexpr (KEYS > 0) {
-                each_key([&](uint32_t key, int) { ones |= key, zeros |= ~key; });
-                ones = __reduce_or_sync(0xFFFFFFFFu, ones);
-                zeros = __reduce_or_sync(0xFFFFFFFFu, zeros);
+                const uint32_t one = __shfl_sync(0xFFFFFFFFu, keys[0], 0);
+                alike = __all_sync(0xFFFFFFFFu, (keys[0] ^ one) >> shift == 0u);
+                if (alike) {                                  // seldom by chance
+                    uint32_t other = 0u;
+                    each_key([&](uint32_t key, int) { other |= key ^ one; });
+                    alike = __all_sync(0xFFFFFFFFu, other >> shift == 0u);
+                }
+                if (alike && lane == 0 && one != 0u &&
+                    (top == 32 || one >> top == found >> top))
+                    add(one, 32 * KEYS);
             }
-            if (KEYS > 0 && (ones & zeros) >> shift == 0u) {
-                if (lane == 0 && ones != 0u && (top == 32 || ones >> top == found >> top))
-                    add(ones, 32 * rounds);
+            if (alike) {
+            } else if (top == 32 && inner) {
+                each_key([&](uint32_t key, int) { add(key, 1); });
             } else if (top == 32) {
                 each_key([&](uint32_t key, int) {
                     if (key != 0u) add(key, 1);
@@ -336,9 +343,12 @@ select_kernel(const Job j, int blocks) {
 
     // ---- how many are above it, or equal to it, before a warp's first item
     int n_above = 0, n_equal = 0;
-    each_key([&](uint32_t key, int) { n_above += key > found, n_equal += key == found; });
+    each_key([&](uint32_t key, int) { n_above += key > found; });
     n_above = __reduce_add_sync(0xFFFFFFFFu, n_above);
-    n_equal = __reduce_add_sync(0xFFFFFFFFu, n_equal);
+    if (need > 0) {
+        each_key([&](uint32_t key, int) { n_equal += key == found; });
+        n_equal = __reduce_add_sync(0xFFFFFFFFu, n_equal);
+    }
     if (lane == 0) above[warp] = n_above, equal[warp] = n_equal;
     __syncthreads();
     int all_above, all_equal;
