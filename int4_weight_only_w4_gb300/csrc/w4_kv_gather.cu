@@ -11,9 +11,10 @@
 // Bound by DRAM, and by what the layout makes it fetch.  bf16 rows are whole sectors:
 // 4096 of 16384 tokens of 16 sequences and 4 heads of 128 take 49.9 us, 81 % of a
 // copy's rate.  A quantised value's bytes lie in every second sector of its record's
-// values: with one token in eight kept, most of the cache passes through DRAM, whose
-// 43 us (4 bits, 32768 tokens) are what the 40.0 us of this kernel are to be compared
-// with, not the 11 of the tokens' own bytes; one in two kept 25.6 us; in 8 bits 63.7.
+// values, so in 4 bits a token that is kept by itself makes DRAM move 640 bytes for its
+// 136: 4096 of 32768 tokens, 200 MB and 30 us at a copy's rate instead of 11, take
+// 40.0 us (DRAM busy 63 % of them, all in single sectors); one in two kept 25.6 us;
+// in 8 bits 63.7.
 // What a unit comes from (list, then page) is asked for two and one units earlier:
 // without that, and with a grid larger than the device holds, 46.7 us.
 #include "w4_kv_work.cuh"

@@ -17,9 +17,9 @@
 // Nothing here is bound by memory (8192 of 131072 items in 16 rows are 1.3 us of it): a
 // dozen steps, each a microsecond or less, wait for one another.  Measured, captured
 // calls: 64 of up to 2048 items in 256 rows 5.7 us; 1024 of up to 8192 in 256 rows
-// 10.6; 8192 of 131072 in 16 rows 16.7 us, of which the first histogram takes 2, adding
+// 10.3; 8192 of 131072 in 16 rows 16.2 us, of which the first histogram takes 2, adding
 // those of a cluster 1.7, the listed keys 3, the places and the stores 3; 4096 of 131072
-// in 4 rows 13.2.  On the way there: loads of which each waited for a comparison 44.4
+// in 4 rows 12.7.  On the way there: loads of which each waited for a comparison 44.4
 // us (16 rows); all under way together, clusters that fit at a time 31.0; keys listed
 // after the first digit 25.6; a constant number of items a thread, without branches
 // around each, 17.0.  Blocks of 512 threads with 64 items each 40.2: fewer warps to

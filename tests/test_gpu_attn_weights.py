@@ -157,6 +157,28 @@ def test_each_row_adds_one(w4, fmt, M):
         assert np.allclose(total[b], want, rtol=1e-4)
 
 
+@pytest.mark.parametrize("fmt", list(kv.FMT))
+@pytest.mark.parametrize("power", [-60, 60])
+def test_queries_of_any_size(w4, fmt, power):
+    """Queries times a power of two with the scale divided by it: the same bits."""
+    s = Setup(w4, fmt, 64, 2, 7, 16, 2, [70, 33], seed=11)
+    lse = attend(s)
+    want = s.cache.attn_weights(s.gq, lse, s.glens, s.table)
+    got = s.cache.attn_weights(s.gq * 2.0 ** power, lse, s.glens, s.table,
+                               scale=64 ** -0.5 * 2.0 ** -power)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", list(kv.FMT))
+def test_keys_of_zero(w4, fmt):
+    """All scores are 0 whatever the queries are: every key of 50 gets 4 / 50."""
+    s = Setup(w4, fmt, 128, 1, 4, 16, 1, [50], seed=12, spread=0.0)
+    q = torch.full_like(s.gq, 1e35)
+    got = s.cache.attn_weights(q, s.cache.attend(q, s.glens, s.table)[1], s.glens, s.table)
+    # exp(-ln 50): the logarithm's rounding, 2^-22 of ln 50, and exp2's
+    assert (got[0, 0, :50] * 50 / 4 - 1).abs().max() <= 2.0 ** -19
+
+
 def test_decay_of_zero_reads_nothing(w4):
     s = Setup(w4, "int8", 64, 2, 2, 16, 2, [50, 20], seed=4)
     lse = attend(s)

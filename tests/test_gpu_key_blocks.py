@@ -149,6 +149,19 @@ def test_values_that_are_not_finite(w4):
     assert np.array_equal(host(scores)[0, 1], after[0, 1])
 
 
+def test_queries_of_any_size(w4):
+    """Scores scale with the queries, exactly, until they leave fp32."""
+    s = Setup(w4, "bf16", 128, 2, 3, 16, 2, [100, 33], seed=7)
+    bounds, scores = run_both(w4, s, 16, 100, 2)
+    for power in (-60, 60):
+        got = torch.full_like(scores, MARK)
+        w4.block_scores(s.cache, bounds, s.gq * 2.0 ** power, s.glens, s.table, got)
+        there = scores != MARK
+        assert torch.equal(got[there], scores[there] * 2.0 ** power)
+    w4.block_scores(s.cache, bounds * 1e30, s.gq * 1e30, s.glens, s.table, got)
+    assert torch.isposinf(got[there]).all()
+
+
 def test_bad_pages_and_lengths_are_recorded(w4):
     s = Setup(w4, "int8", 64, 2, 2, 16, 1, [40, 50], seed=8)
     table = s.table.clone()
