@@ -58,6 +58,7 @@ struct Plan {
     int stages;        // records of a group's ring
     int ring_bytes;    // of all rings
     int extra;         // what a head costs beside its records
+    int part;          // records of a group that a part of a head has at least
 };
 
 inline Plan plan_of(int D, int NT, int rows, int record_bytes) {
@@ -74,6 +75,7 @@ inline Plan plan_of(int D, int NT, int rows, int record_bytes) {
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.ring_bytes = p.KG * p.stages * record_bytes;
     p.extra = kHeadRecords / ((p.QG * NT + 1) / 2);
+    p.part = 4;
     return p;
 }
 
@@ -121,12 +123,12 @@ struct Division {
     int q, rest;           // work / blocks and its remainder
     unsigned magic;        // 2^32 / blocks, rounded up
 
-    // As many blocks as heads, or that many times the parts of at least 4
+    // As many blocks as heads, or that many times the parts of at least `part`
     // records a group that the mean head has (so heads of one length are cut
     // alike), while there are blocks.
     W4_HD void divide(const Plan &plan, int seqs, int all, int grid) {
         work = all;
-        const int heads = seqs * per_seq, parts = (work / heads - extra) / (4 * plan.KG);
+        const int heads = seqs * per_seq, parts = (work / heads - extra) / (plan.part * plan.KG);
         const int want = heads * (parts > 1 ? parts : 1);
         blocks = grid < want ? grid : want;
         q = work / blocks, rest = work - q * blocks;
