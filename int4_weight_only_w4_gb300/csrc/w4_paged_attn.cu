@@ -58,7 +58,7 @@
 // the others each record's own first key, so that everything else is as above.
 // Measured: 64 ragged sequences reading 4096 tokens each in 8 bits 50.6 us (numbers and
 // pages asked for in one go 52.4; the whole attention over 64 x 4096 tokens 51.9);
-// 64 blocks of 64 out of 131072 tokens in bf16, one sequence, 10.2.
+// 64 blocks of 64 out of 131072 tokens in bf16, one sequence, 10.6.
 //
 // Measured (28 query and 4 key/value heads of 128, one new token, captured calls;
 // a copy reaches 6788 GB/s).  bf16, bound by HBM: 32 x 16384 tokens 160 us =

@@ -890,7 +890,8 @@ class PagedCache:
         return out, lse
 
     def new_bounds(self) -> torch.Tensor:
-        """Bounds of the keys of all pages, for key_bounds() to fill."""
+        """Bounds of the keys of all pages, for key_bounds() to fill (made on torch's
+        current stream)."""
         return torch.zeros(self.bounds_shape, dtype=torch.bfloat16, device=self.pool.device)
 
     def key_bounds(self, bounds, lens, table, tokens: int = 1, stream=None) -> torch.Tensor:
