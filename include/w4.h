@@ -797,7 +797,8 @@ w4_status w4_attn_weights(const w4_kv_cache *cache, const w4_heads *q, const flo
  * Indices may be in any order and repeat.  A place whose index is negative, or no
  * token of the sequence (W4_KV_ERR_POSITION), stays as it was, and so do other
  * places of the records that are touched.  With the lists of w4_select, counts are
- * the new lengths; the old pages are free afterwards.
+ * the new lengths; the old pages are free afterwards.  (The new pages' keys have no
+ * bounds yet: w4_key_bounds, with as many tokens.)
  *   table, to : of the same cache, with as many sequences.  No page that is
  *             written may be one that is read (two tables at one address are
  *             refused)
@@ -806,15 +807,15 @@ w4_status w4_attn_weights(const w4_kv_cache *cache, const w4_heads *q, const flo
  *   counts  : device int32 [seqs]; taken as 0 below it; above most or the room of
  *             `to` cut (W4_KV_ERR_LENGTH)
  *   weights : device float [seqs][kv_heads][columns], tokens from columns on are
- *             not there; weights_out : device float [seqs][kv_heads][most], must
- *             not overlap it; or both NULL
+ *             not there; weights_out : device float [seqs][kv_heads][columns_out],
+ *             columns_out >= most, must not overlap it; or both NULL
  * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim, sizes as for
  * w4_key_bounds), W4_ERR_CUDA.
  */
 w4_status w4_kv_gather(const w4_kv_cache *cache, const w4_block_table *table,
                        const int32_t *lens, const int32_t *index, const int32_t *counts, int most,
                        const w4_block_table *to, const float *weights, int columns,
-                       float *weights_out, w4_stream_t stream);
+                       float *weights_out, int columns_out, w4_stream_t stream);
 
 #ifdef __cplusplus
 }

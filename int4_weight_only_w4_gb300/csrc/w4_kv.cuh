@@ -129,8 +129,8 @@ cudaError_t launch_block_scores(const KvPool &pool, int head_dim, const void *bo
 
 cudaError_t launch_kv_gather(const KvPool &from, const KvPool &to, int format, int head_dim,
                              const int32_t *lens, const int32_t *index, const int32_t *counts,
-                             int most, const float *weights, float *weights_out, int columns,
-                             int num_sms, cudaStream_t stream);
+                             int most, const float *weights, int columns, float *weights_out,
+                             int columns_out, int num_sms, cudaStream_t stream);
 cudaError_t launch_select(const float *scores, int seqs, int heads, int columns,
                           const int32_t *lens, int unit, int first, int last, int count,
                           int32_t *index, int32_t *counts, int num_sms, cudaStream_t stream);

@@ -449,7 +449,7 @@ w4_status w4_attn_weights(const w4_kv_cache *cache, const w4_heads *q, const flo
 w4_status w4_kv_gather(const w4_kv_cache *cache, const w4_block_table *table,
                        const int32_t *lens, const int32_t *index, const int32_t *counts, int most,
                        const w4_block_table *to, const float *weights, int columns,
-                       float *weights_out, w4_stream_t stream) {
+                       float *weights_out, int columns_out, w4_stream_t stream) {
     w4_status st = walk_ok(cache, table, lens);
     if (st == W4_OK) st = walk_ok(cache, to, lens);
     if (st != W4_OK) return st;
@@ -457,13 +457,13 @@ w4_status w4_kv_gather(const w4_kv_cache *cache, const w4_block_table *table,
         to->seqs != table->seqs || to->pages == table->pages)
         return W4_ERR_INVALID_ARG;
     if (!weights != !weights_out || !aligned(weights, 4) || !aligned(weights_out, 4) ||
-        (weights && (columns < 1 || weights == weights_out)))
+        (weights && (columns < 1 || columns_out < most || weights == weights_out)))
         return W4_ERR_INVALID_ARG;
     const int sms = device_sms();
     if (sms <= 0) return W4_ERR_CUDA;
     return cuda_status(w4::launch_kv_gather(pool_of(cache, table), pool_of(cache, to),
                                             cache->format, cache->head_dim, lens, index, counts,
-                                            most, weights, weights_out, columns, sms,
+                                            most, weights, columns, weights_out, columns_out, sms,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 

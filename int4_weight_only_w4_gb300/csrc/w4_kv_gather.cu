@@ -45,7 +45,7 @@ struct Moved {
     const int32_t *index;
     const float *weights;         // NULL: none
     float *weights_out;
-    int columns;
+    int columns, columns_out;
 };
 
 template <int FMT, int D>
@@ -111,7 +111,7 @@ gather_kernel(const KvPool from, const int32_t *lens, const Lists lists, const M
             if (src) {
                 src += in_page / kRecTokens * L::kBytes, src_r = in_page % kRecTokens;
                 if (m.weights && lane < 16)
-                    m.weights_out[row * lists.most + first + r] =
+                    m.weights_out[row * m.columns_out + first + r] =
                         m.weights[row * m.columns + now.token];
             }
         }
@@ -193,10 +193,10 @@ gather_kernel(const KvPool from, const int32_t *lens, const Lists lists, const M
 
 cudaError_t launch_kv_gather(const KvPool &from, const KvPool &to, int format, int head_dim,
                              const int32_t *lens, const int32_t *index, const int32_t *counts,
-                             int most, const float *weights, float *weights_out, int columns,
-                             int num_sms, cudaStream_t stream) {
+                             int most, const float *weights, int columns, float *weights_out,
+                             int columns_out, int num_sms, cudaStream_t stream) {
     const Lists lists = {to, counts, most};
-    const Moved moved = {index, weights, weights_out, columns};
+    const Moved moved = {index, weights, weights_out, columns, columns_out};
     const long long room = (long long)to.width * to.page_records,
                     listed = ((long long)most + kRecTokens - 1) / kRecTokens;
     const long long units = (room < listed ? room : listed) * to.seqs * to.kv_heads;

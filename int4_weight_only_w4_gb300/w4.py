@@ -461,7 +461,7 @@ _block_scores = _decl("w4_block_scores", _ST, _P, _P, _P, _I, _I, _P, _P, _P, _I
 _select = _decl("w4_select", _ST, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P)
 _attn_weights = _decl("w4_attn_weights", _ST, _P, _P, _P, _I, _I, _P, _P, ctypes.c_float, _I, _P,
                       ctypes.c_float, _P, _I, _P)
-_kv_gather = _decl("w4_kv_gather", _ST, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P)
+_kv_gather = _decl("w4_kv_gather", _ST, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _I, _P)
 
 
 def _heads(t, dtype=torch.bfloat16) -> bytes | None:
@@ -719,20 +719,20 @@ def kv_gather(cache: "PagedCache", table, lens, index, counts, to, weights=None,
               weights_out=None, stream=None) -> None:
     """w4_kv_gather: place i of sequence b in the pages of `to` gets token index[b, h, i]
     of those of `table`, for i < counts[b] and every key/value head h (index int32
-    [seqs, kv_heads, most]); weights_out[b, h, i] (float32 [seqs, kv_heads, most]) its
-    entry of weights (float32 [seqs, kv_heads, columns])."""
+    [seqs, kv_heads, most]); weights_out[b, h, i] (float32 [seqs, kv_heads, most or more])
+    its entry of weights (float32 [seqs, kv_heads, columns])."""
     B, H = table.shape[0], cache.kv_heads
-    most, columns = index.shape[-1], 0
+    most, columns, columns_out = index.shape[-1], 0, 0
     if (weights is None) != (weights_out is None):
         raise ValueError("weights, weights_out: expected both or neither")
     if weights is not None:
-        columns = weights.shape[-1]
+        columns, columns_out = weights.shape[-1], weights_out.shape[-1]
         weights = _filled(weights, (B, H, columns), torch.float32, "weights")
-        weights_out = _filled(weights_out, (B, H, most), torch.float32, "weights_out")
+        weights_out = _filled(weights_out, (B, H, columns_out), torch.float32, "weights_out")
     _ok(_kv_gather(cache.ref, _block_table(table), _int32(lens, B, "lens"),
                    _filled(index, (B, H, most), torch.int32, "index"),
                    _int32(counts, B, "counts"), most, _block_table(to), weights, columns,
-                   weights_out, _raw_stream(stream, index)), "w4_kv_gather")
+                   weights_out, columns_out, _raw_stream(stream, index)), "w4_kv_gather")
 
 
 class RopeTable:
@@ -931,11 +931,13 @@ class PagedCache:
                stream=None):
         """Move listed tokens to other pages: place i of sequence b in `to` gets token
         index[b, h, i] in `table`, for i < counts[b] and every head; returns weights_out, the
-        tokens' weights (default, where weights are given: a new tensor, made on
-        `stream`, 0 past the counts)."""
+        tokens' weights (default, where weights are given: a new tensor of their shape,
+        or as wide as the list where that is wider, made on `stream`, 0 past the counts)."""
         if weights is not None and weights_out is None:
+            columns = max(weights.shape[-1], index.shape[-1])
             with _on(stream, index.device):
-                weights_out = torch.zeros(index.shape, dtype=torch.float32, device=index.device)
+                weights_out = torch.zeros((*index.shape[:2], columns), dtype=torch.float32,
+                                          device=index.device)
         kv_gather(self, table, lens, index, counts, to, weights, weights_out, stream)
         return weights_out
 

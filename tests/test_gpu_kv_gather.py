@@ -94,7 +94,7 @@ class Moving:
                         host.move(h, (table[b, j // self.P], j % self.P),
                                   (to[b, i // self.P], i % self.P))
                         want[b, h, i] = w[b, h, j]
-        out = torch.full(want.shape, MARK, device="cuda")
+        out = torch.full((*want.shape[:2], self.most + self.most % 3), MARK, device="cuda")
         pair = dict(weights=torch.from_numpy(w).cuda(), weights_out=out) if weights else {}
         self.cache.gather(self.s.table, self.s.glens, i32(index), i32(counts), self.to, **pair,
                           **kw)
@@ -102,7 +102,8 @@ class Moving:
         got = self.cache.pool.cpu().numpy().reshape(host.bytes.shape)
         assert np.array_equal(got, host.bytes)
         if weights:
-            assert np.array_equal(out.cpu().numpy(), want)
+            got = out.cpu().numpy()
+            assert np.array_equal(got[..., :self.most], want) and (got[..., self.most:] == MARK).all()
 
 
 LENS = [0, 1, 2, 15, 16, 17, 31, 33, 64, 100, 257]
@@ -207,12 +208,15 @@ def test_an_eviction(w4, fmt):
             dS = kv.score_error(fmt, s.q, s.keys, s.scales, lens, D ** -0.5)
             kv.check_attention(out[b:b + 1, 3 * h:3 * h + 3].float().cpu().numpy(),
                                lse[b:b + 1, 3 * h:3 * h + 3].cpu().numpy(), *ref, fmt, dS, 48, True)
-    # the next token goes behind the kept ones
+    # the next token goes behind the kept ones, whose weights go on from what they were
     k = to_gpu(m.rng.standard_normal((B, H, D)).astype(np.float32))
     c.append(k, k, counts, m.to)
-    c.attn_weights(s.gq, c.attend(s.gq, counts + 1, m.to)[1], counts + 1, m.to)
-    back, _ = c.read(counts, m.to)
-    assert torch.isfinite(back.float()).all()
+    lens, before = counts + 1, kept.clone()
+    c.attn_weights(s.gq, c.attend(s.gq, lens, m.to)[1], lens, m.to, before=kept, weights=kept)
+    added = (kept - before).double().sum(-1)
+    assert kept.shape == weights.shape and ((added - 3).abs() <= 1e-4).all()   # one a row
+    for b, n in enumerate(lens.tolist()):
+        assert (kept[b, :, :n] >= before[b, :, :n]).all() and (kept[b, :, n:] == 0).all()
     c.check()
 
 
@@ -275,11 +279,12 @@ def test_refusals(w4):
     call()
     for kw in (dict(index=index[:1]), dict(index=index.long()), dict(counts=counts[:1]),
                dict(lens=m.s.glens[:1]), dict(weights=None), dict(weights_out=None),
-               dict(weights_out=out[..., :10].contiguous()), dict(weights=w[:1]),
+               dict(weights=w[:1]), dict(weights_out=out[:1]),
                dict(weights=w.double()), dict(index=index.cpu()), dict(to=m.to.long())):
         with pytest.raises(ValueError):
             call(**kw)
-    for kw in (dict(to=m.to[:1]), dict(to=m.s.table)):
+    for kw in (dict(to=m.to[:1]), dict(to=m.s.table),
+               dict(weights_out=out[..., :10].contiguous())):
         with pytest.raises(w4.W4Error) as e:
             call(**kw)
         assert e.value.status == w4.Status.INVALID_ARG

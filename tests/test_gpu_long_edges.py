@@ -123,7 +123,7 @@ def test_counts_are_the_new_lengths(w4):
     assert lens.tolist() == [50, 30, 0]
     for b, n in enumerate(lens.tolist()):
         assert torch.equal(out[b, :, :n], w[b].gather(1, index[b, :, :n].long()))
-        assert (out[b, :, n:] == 0).all()
+        assert (out[b, :, n:] == 0).all() and out.shape == w.shape
     m.cache.check()
 
 

@@ -105,10 +105,10 @@ def test_attn_weights_errors(lib, kw, want):  # noqa: F811
 
 
 def gather(lib, c=cache(), t=table(), lens=FAKE, index=FAKE, counts=FAKE, most=4,  # noqa: F811
-           to=table(FAKE + 64), w=None, columns=0, out=None):
-    lib.w4_kv_gather.argtypes = [P, P, P, P, P, I, P, P, I, P, P]
+           to=table(FAKE + 64), w=None, columns=0, out=None, columns_out=4):
+    lib.w4_kv_gather.argtypes = [P, P, P, P, P, I, P, P, I, P, I, P]
     return lib.w4_kv_gather(ref(c), ref(t), lens, index, counts, most, ref(to), w, columns, out,
-                            None)
+                            columns_out, None)
 
 
 @pytest.mark.parametrize("kw,want", WALK + [
@@ -117,7 +117,8 @@ def gather(lib, c=cache(), t=table(), lens=FAKE, index=FAKE, counts=FAKE, most=4
     (dict(to=table(FAKE + 64, seqs=2)), 1), (dict(to=table(FAKE + 66)), 1),
     (dict(to=table(FAKE + 64, width=1 << 27, stride=1 << 27)), 2), (dict(w=FAKE, columns=9), 1),
     (dict(out=FAKE, columns=9), 1), (dict(w=FAKE, out=FAKE, columns=9), 1),
-    (dict(w=FAKE, out=FAKE + 64, columns=0), 1), (dict(w=FAKE + 2, out=FAKE + 64, columns=9), 1),
+    (dict(w=FAKE, out=FAKE + 64, columns=0), 1),
+    (dict(w=FAKE, out=FAKE + 64, columns=9, columns_out=3), 1), (dict(w=FAKE + 2, out=FAKE + 64, columns=9), 1),
     (dict(w=FAKE, out=FAKE + 65, columns=9), 1)])
 def test_gather_errors(lib, kw, want):  # noqa: F811
     assert gather(lib, **kw) == want
