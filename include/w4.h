@@ -667,7 +667,9 @@ w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w
  *
  * A decode step that reads a part of the cache:
  *   w4_kv_append, w4_key_bounds (the blocks that got new keys), w4_block_scores,
- *   w4_select (unit = page_tokens), w4_sparse_attn.
+ *   w4_select (unit = page_tokens), w4_sparse_attn.  New tokens see themselves and
+ *   one another where their blocks are listed: 1 + (tokens + page_tokens - 2) /
+ *   page_tokens last ones hold them.
  * Cutting a cache down to `count` tokens a head:
  *   w4_paged_attn, w4_attn_weights over the steps, then w4_select (unit = 1),
  *   w4_kv_gather into other pages; its counts are the sequences' new lengths.
@@ -746,7 +748,8 @@ w4_status w4_select(const float *scores, int seqs, int heads, int columns, const
  * device only.
  *   blocks : device int32 [seqs][kv_heads][most], ascending; an entry that is not
  *            above the one before it, or no block of the sequence, is left out
- *            (W4_KV_ERR_BLOCK)
+ *            (W4_KV_ERR_BLOCK; a block that a list out of order names again later
+ *            counts again)
  *   counts : device int32 [seqs]; taken as 0 below it, as most above it
  *   most   : >= 1
  * The other arguments, a row that sees no key, and the errors are those of
@@ -768,7 +771,8 @@ w4_status w4_sparse_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const 
  *   weights[b][h][j] = (j < lens[b] - tokens ? decay * before[b][h][j] : 0)
  *                      + sum over the rows that see key j of exp(scale q . k_j - lse)
  * for j < lens[b], the rows being those of w4_paged_attn (new tokens x query heads
- * of h) with its window, and lse what it returned for them: each row adds 1 in all.
+ * of h) with its window, and lse what it returned for them (not w4_sparse_attn, which
+ * leaves keys out): each row adds 1 in all.
  * The new tokens' own places start at 0, so weights need not be cleared.  Entries
  * from lens[b] on are left as they were.  A row whose lse is infinite gives
  * nothing; a key that no row sees, or whose page is not in the pool, gets nothing.
