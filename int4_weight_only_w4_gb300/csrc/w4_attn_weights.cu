@@ -5,6 +5,10 @@
 // y the scores in units of log2, so the keys are read once more, the values not at
 // all, and no token needs another one's result: nothing is joined.
 //
+// Roundings.  Operands are those of the attention (bf16, or exact codes against binary16
+// queries), scores, exponents and sums fp32; exp2 is off by 2^-22, and what it gives
+// under 2^-126 is 0.  No probability is rounded to fewer bits.
+//
 // The blocks divide the list (sequence, head, record) evenly, from the lengths on
 // the device.  A warp takes every fourth unit of 1 to 4 records of its block's
 // stretch through a ring of its own, which asynchronous copies of 16 bytes fill

@@ -6,6 +6,11 @@
 // That is one product of 2 D values, (q+, q-) . (hi, lo), and goes to the tensor cores
 // with 16 blocks as its rows and 8 rows of queries as its columns.
 //
+// Roundings.  Bounds are bfloat16, half the bytes of fp32 for a score that only ranks
+// blocks: exact for a bf16 cache; of a quantised key, (q - z) s rounded to nearest as it
+// is read back, so a product with the unrounded key may pass the bound by 2^-9 of its
+// terms.  A score's products are exact and its sum is fp32.
+//
 // Both kernels move little and are a chain of trips to memory (length, page, bounds or
 // keys).  What counts is how few trips there are and how many warps make them at a
 // time: while there are few units, each has a worker of its own that needs no sum over
