@@ -59,9 +59,23 @@ struct Plan {
     int ring_bytes;    // of all rings
     int extra;         // what a head costs beside its records
     int part;          // records of a group that a part of a head has at least
+    int least;         // records that are not cut off a head
 };
 
-inline Plan plan_of(int D, int NT, int rows, int record_bytes) {
+constexpr int kPart = 4;               // of the whole attention
+
+// Of listed blocks, whose lists are short: how many records a part has costs more or
+// less latency.  Measured, in us with 4, 3, 2, 1 records a group: 64 blocks of one
+// sequence, of 64 tokens in bf16 10.2, 10.5, 10.9, 10.9, in 4 bits 12.6, 12.1, 10.3,
+// 11.1, of 32 tokens in bf16 of 64 11.3, 11.3, 9.7, 8.9; of four sequences in 8 bits
+// 13.8, 13.5, 12.1, 11.2; of two with 4 new tokens in bf16 15.5, 14.2, 14.1, 14.8; 64
+// of 4096 tokens in 8 bits 50.7 whatever it is.  One sequence's short lists, where two
+// records cut a head and four do not: 80 records in 4 bits 11.5 and 10.8, 111 12.1 and
+// 12.6, 103 in 8 bits 11.9 and 12.1, 39 for 4 new tokens 13.2 and 14.7, 143 of 64 in 4
+// bits 10.2 and 12.0.
+inline int listed_part(bool bf16, int D) { return bf16 && D == 128 ? 3 : 2; }
+
+inline Plan plan_of(int D, int NT, int rows, int record_bytes, int part = kPart) {
     const int warps = compute_warps(D, NT);
     const int tiles = (rows + 8 * NT - 1) / (8 * NT), most = kRowsMax / (8 * NT);
     Plan p;
@@ -75,14 +89,26 @@ inline Plan plan_of(int D, int NT, int rows, int record_bytes) {
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.ring_bytes = p.KG * p.stages * record_bytes;
     p.extra = kHeadRecords / ((p.QG * NT + 1) / 2);
-    p.part = 4;
+    p.part = part;
+    p.least = p.KG > p.extra / 2 ? p.KG : p.extra / 2;
     return p;
 }
 
-// One sequence that is too short for a second part of a head: no head is cut.
+// Whether no head of a call of one sequence is cut, however few of the records that
+// there is room for it has, so that there is nothing to join.  By Division::divide a
+// head makes k parts from k * part * KG records on; by Division::cut_inside the last of
+// its cuts, at (k - 1) / k of what it costs, stays in it if `least` records are ahead
+// of it.
 inline bool nothing_to_join(const Plan &p, int seqs, int kv_heads, long long table_records,
                             int grid) {
-    return seqs == 1 && table_records < 8 * p.KG && kv_heads * p.row_tiles <= grid;
+    const long long heads = (long long)kv_heads * p.row_tiles, each = (long long)p.part * p.KG;
+    if (seqs != 1 || heads > grid) return false;
+    for (long long k = 2; k * each <= table_records; ++k) {
+        const long long cut = (k * (p.least + p.extra) + k - 2) / (k - 1) - p.extra;
+        const long long first = cut > k * each ? cut : k * each;
+        if (k * heads > grid || (first < (k + 1) * each && first <= table_records)) return false;
+    }
+    return true;
 }
 
 // The records of a sequence that a call looks at.
@@ -119,7 +145,7 @@ W4_HD bool has_more(const Cut &c, const Cut &to, int seqs) {
 struct Division {
     int extra, per_seq;    // heads (x row tiles) of a sequence
     int work;              // what all items cost
-    int blocks, least;     // blocks that have a stretch, records that are not cut off
+    int blocks, least;     // blocks that have a stretch; as the plan has it
     int q, rest;           // work / blocks and its remainder
     unsigned magic;        // 2^32 / blocks, rounded up
 
@@ -133,7 +159,7 @@ struct Division {
         blocks = grid < want ? grid : want;
         q = work / blocks, rest = work - q * blocks;
         magic = 0xFFFFFFFFu / (unsigned)blocks + 1;
-        least = plan.KG > extra / 2 ? plan.KG : extra / 2;
+        least = plan.least;
     }
 
     // Start of block c's stretch.  rest * c < 2^16, so the product with magic

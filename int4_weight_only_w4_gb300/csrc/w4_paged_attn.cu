@@ -954,14 +954,8 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t stream) {
         if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
     }
     const int rows = a.tokens * a.group;
-    Plan p = plan_of(D, NT, rows, bytes);
-    // Lists are short, and how many records a part has costs more or less latency.
-    // Measured, in us with 4, 3, 2, 1 records a group: 64 blocks of one sequence, of 64
-    // tokens in bf16 10.2, 10.5, 10.9, 10.9, in 4 bits 12.6, 12.1, 10.3, 11.1, of 32
-    // tokens in bf16 of 64 11.3, 11.3, 9.7, 8.9; of four sequences in 8 bits 13.8, 13.5,
-    // 12.1, 11.2; of two with 4 new tokens in bf16 15.5, 14.2, 14.1, 14.8; 64 of 4096
-    // tokens in 8 bits 50.7 whatever it is.
-    if (LISTED) p.part = FMT == W4_KV_BF16 && D == 128 ? 3 : 2;
+    const Plan p =
+        plan_of(D, NT, rows, bytes, LISTED ? listed_part(FMT == W4_KV_BF16, D) : kPart);
     const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
     e = launch_overlapped(attn_kernel<FMT, D, NT, LISTED>, dim3(grid), dim3(32 * (WARPS + kCopyWarps)),
                           kSharedBytes, stream, a, p);
