@@ -17,10 +17,10 @@
 // the lengths.  Measured, captured calls: bounds of one step of 64 sequences 3.5 us
 // (each worker summing the lengths first, a warp a block of 64 tokens: 4.9), of 16384
 // tokens in 8 bits 4.8 us (8.2; a copy's rate is 1.4); scores of 64 ragged sequences of
-// up to 512 blocks 9.8 us (11.5; a copy's rate 5.1: two rounds of 16 warps an SM), of 8
-// x 8192 blocks 25.0 us = 81 % of a copy's rate.  With hi and lo one after the other
-// in 64 registers, and twice as many warps, these two took 9.4 and 26.7 us, 8 new tokens
-// 18.6 instead of 17.1: not kept.
+// up to 512 blocks 9.5 us (11.5; a copy's rate 5.1: two rounds of 16 warps an SM), of 8
+// x 8192 blocks 24.7 us = 82 % of a copy's rate.  With hi and lo one after the other
+// in 64 registers, and twice as many warps, these two took 9.4 and 26.7 us (9.8 and 25.0
+// then), 8 new tokens 18.6 (17.1): not kept.
 #include "w4_device.cuh"
 #include "w4_kv_work.cuh"
 
@@ -215,7 +215,7 @@ struct Tiles {
 // lane t takes the 16-byte pieces t, t + 4, ... of a row as they lie in memory.
 template <int D>
 __global__ void __launch_bounds__(32 * kBlockWarps)
-scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q, int group,
+scores_kernel(const Tiles tiles, const uint4 *bounds, const Heads q, int group,
               unsigned group_magic, int tokens, float *scores, int columns, int most) {
     constexpr int PIECES = D / 32;
     begin_after_previous();
@@ -228,23 +228,31 @@ scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q
     for (; s.left > 0; s.next(tiles, pool.kv_heads)) {
         const int len = tiles.len(s.b), blocks = tiles.blocks(len);
         uint4 a[2][2][PIECES];                                // hi, lo of blocks g, g + 8
-        bool valid[2];
+        bool there[2], valid[2];
+        int page[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const int block = 16 * s.u + g + 8 * y;
-            const int page = block < blocks ? pool.table[s.b * pool.stride + block] : -1;
-            valid[y] = page >= 0 && page < pool.pages;
-            if (block < blocks && !valid[y] && pool.error) atomicOr(pool.error, W4_KV_ERR_PAGE);
+            there[y] = block < blocks;
+            page[y] = there[y] ? pool.table[s.b * pool.stride + block] : -1;
+        }
+        // (ordinary loads: what they read may still be written when this kernel starts)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            valid[y] = page[y] >= 0 && page[y] < pool.pages;
             const uint4 *row =
-                bounds + ((long long)(valid[y] ? page : 0) * pool.kv_heads + s.h) * (D / 4) + t;
+                bounds + ((long long)(valid[y] ? page[y] : 0) * pool.kv_heads + s.h) * (D / 4) + t;
 #pragma unroll
             for (int z = 0; z < 2; ++z)
 #pragma unroll
                 for (int j = 0; j < PIECES; ++j)
-                    a[z][y][j] = valid[y] ? __ldg(row + z * (D / 8) + 4 * j)
-                                          : make_uint4(0u, 0u, 0u, 0u);
+                    a[z][y][j] = valid[y] ? row[z * (D / 8) + 4 * j] : make_uint4(0u, 0u, 0u, 0u);
         }
+        if (pool.error && ((there[0] && !valid[0]) || (there[1] && !valid[1])))
+            atomicOr(pool.error, W4_KV_ERR_PAGE);
         float best[2] = {-INFINITY, -INFINITY};
+        // (two rounds together: 8 new tokens 16.9 us, 18.2 one by one)
+#pragma unroll 2
         for (int r0 = 0; r0 < rows; r0 += 8) {
             const int r = min(r0 + g, rows - 1);
             const int i = group == 1 ? r : (int)__umulhi((unsigned)r, group_magic);
@@ -252,11 +260,14 @@ scores_kernel(const Tiles tiles, const uint4 *__restrict__ bounds, const Heads q
                 reinterpret_cast<const __nv_bfloat16 *>(q.data) +
                 (long long)(s.b * tokens + i) * q.token_stride +
                 (long long)(s.h * group + r - i * group) * q.head_stride) + t;
+            uint4 piece[PIECES];                              // all under way together
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) piece[j] = row[4 * j];
             // (two sums: half as many products wait for one another, and each rounds less)
             float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < PIECES; ++j) {
-                const uint4 v = __ldg(row + 4 * j);
+                const uint4 v = piece[j];
                 const uint4 up = make_uint4(max2(v.x, 0u), max2(v.y, 0u), max2(v.z, 0u),
                                             max2(v.w, 0u));
                 const uint4 down = make_uint4(min2(v.x, 0u), min2(v.y, 0u), min2(v.z, 0u),

@@ -41,7 +41,7 @@ rope_table_kernel(const __grid_constant__ Turns turns, int pairs, double amplitu
 // rotated ones.
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(Heads x, Heads y, int tokens, int heads, int head_dim,
-            const int32_t *__restrict__ positions, Rotation rot, uint32_t *error) {
+            const int32_t *positions, Rotation rot, uint32_t *error) {
     begin_after_previous();
     const int units = rot.pairs + head_dim - 2 * rot.pairs;
     const long long n = (long long)tokens * heads * units;
@@ -82,7 +82,7 @@ rope_kernel(Heads x, Heads y, int tokens, int heads, int head_dim,
 template <int LAYOUT, int HEADS>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_wide_kernel(Heads x, Heads y, unsigned units_all, int heads, unsigned groups, unsigned units,
-                 const int32_t *__restrict__ positions, Rotation rot, uint32_t *error) {
+                 const int32_t *positions, Rotation rot, uint32_t *error) {
     begin_after_previous();
     const unsigned e = blockIdx.x * kRopeThreads + threadIdx.x;
     if (e >= units_all) return;
