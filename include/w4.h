@@ -690,8 +690,9 @@ w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w
  *   bounds : device, bfloat16 [pages][kv_heads][2][head_dim], 16-byte aligned
  *   tokens : >= 1
  *   lens   : device int32 [table->seqs]; negative counts as 0
- * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim; 2^31 or more
- * tokens x heads in the table's room), W4_ERR_CUDA.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (head_dim; a table with room for
+ * more than 2^31 - 2^21 tokens a sequence, or for 2^31 or more records of 16
+ * tokens, those of every head), W4_ERR_CUDA.
  */
 w4_status w4_key_bounds(const w4_kv_cache *cache, uint16_t *bounds, int tokens,
                         const int32_t *lens, const w4_block_table *table, w4_stream_t stream);

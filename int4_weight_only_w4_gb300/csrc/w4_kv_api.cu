@@ -108,13 +108,14 @@ w4_status queries_ok(const w4_kv_cache *cache, const w4_heads *q, int q_heads, i
 }
 
 // The cache, its table and the lengths of a call that walks all sequences: what
-// it counts in 32 bits are a sequence's tokens, and records of all heads.
+// it counts in 32 bits are a sequence's tokens, to which kernels add a page (2^20
+// tokens at most) or a unit of records, and records of all heads.
 w4_status walk_ok(const w4_kv_cache *cache, const w4_block_table *table, const int32_t *lens) {
     const w4_status st = cache_ok(cache, true);
     if (st != W4_OK) return st;
     if (!table_ok(table) || !lens || !aligned(lens, 4)) return W4_ERR_INVALID_ARG;
     const long long room = (long long)table->width * cache->page_tokens;
-    if (room >= (1LL << 31) || (room / w4::kRecTokens * table->seqs) >= (1LL << 31) ||
+    if (room > (1LL << 31) - (1 << 21) || (room / w4::kRecTokens * table->seqs) >= (1LL << 31) ||
         room / w4::kRecTokens * table->seqs * cache->kv_heads >= (1LL << 31))
         return W4_ERR_UNSUPPORTED;
     return W4_OK;
