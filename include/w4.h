@@ -645,8 +645,9 @@ w4_status w4_paged_attn_workspace_bytes(const w4_kv_cache *cache, size_t *bytes)
  *   window : >= 0; 0, or as many as the table has room for, leave nothing out
  *   workspace : device, 256-byte aligned; calls that overlap on the device must
  *            not share one; what it holds between calls does not matter
- * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, or a table
- * and heads that allow 2^31 or more visits of records), W4_ERR_CUDA.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED (tokens, head_dim, a table with
+ * room for more than 2^31 - 256 tokens a sequence, or one that with the heads
+ * allows 2^31 or more visits of records), W4_ERR_CUDA.
  */
 w4_status w4_paged_attn(const w4_kv_cache *cache, const w4_heads *q, const w4_heads *out,
                         int q_heads, int tokens, const int32_t *lens,

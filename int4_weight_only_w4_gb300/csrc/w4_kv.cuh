@@ -95,6 +95,10 @@ cudaError_t launch_kv_read(const KvPool &pool, int format, int head_dim, const H
                            const Heads &v, const TokenList &list, int num_sms,
                            cudaStream_t stream);
 
+// First key of a record that is not there.  The host refuses tables with room for a
+// longer sequence, so it is past every length.
+constexpr int kAbsent = 0x7FFFFF00;
+
 struct AttnArgs {
     KvPool pool;
     Heads q, out;

@@ -140,7 +140,7 @@ w4_status paged_attn_common(const w4_kv_cache *cache, const w4_heads *q, const w
     if (!rows_aligned(q, 2) || !rows_aligned(out, f32_out ? 4 : 2) || !aligned(lens, 4) ||
         !aligned(lse, 4) || !aligned(workspace, 256))
         return W4_ERR_INVALID_ARG;
-    if ((long long)table->width * cache->page_tokens >= (1LL << 31) ||
+    if ((long long)table->width * cache->page_tokens > w4::kAbsent ||
         (long long)table->seqs * q_heads * tokens >= (1LL << 31))
         return W4_ERR_UNSUPPORTED;
     // records that the call could visit, counted in 32 bits (a head costs up to

@@ -75,7 +75,6 @@
 namespace w4 {
 namespace {
 
-constexpr int kAbsent = 0x7FFFFF00;    // first key of a record that is not there: past any length
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen no key
 constexpr float kLn2 = 0.693147180559945309417f;
 
