@@ -687,7 +687,9 @@ w4_status w4_paged_attn_f32(const w4_kv_cache *cache, const w4_heads *q, const w
  *   bounds[page][head][0][d] = max, bounds[page][head][1][d] = min
  * over the block's tokens j < lens[b] of value d of key j, as w4_kv_read returns
  * it; if one of them is NaN, both are.  They go by page: a page that several
- * sequences share should be full in all of them, or it gets the bounds of one.
+ * sequences share has to hold as many tokens in each of them (a full one does).
+ * Otherwise every value is that of any one of them, and the bounds may hold for
+ * none.
  *   bounds : device, bfloat16 [pages][kv_heads][2][head_dim], 16-byte aligned
  *   tokens : >= 1
  *   lens   : device int32 [table->seqs]; negative counts as 0
