@@ -16,11 +16,13 @@
 // time: while there are few units, each has a worker of its own that needs no sum over
 // the lengths.  Measured, captured calls: bounds of one step of 64 sequences 3.5 us
 // (each worker summing the lengths first, a warp a block of 64 tokens: 4.9), of 16384
-// tokens in 8 bits 4.8 us (8.2; a copy's rate is 1.4); scores of 64 ragged sequences of
-// up to 512 blocks 9.5 us (11.5; a copy's rate 5.1: two rounds of 16 warps an SM), of 8
-// x 8192 blocks 24.7 us = 82 % of a copy's rate.  With hi and lo one after the other
-// in 64 registers, and twice as many warps, these two took 9.4 and 26.7 us (9.8 and 25.0
-// then), 8 new tokens 18.6 (17.1): not kept.
+// tokens in 8 bits 4.8 us (8.2; a copy's rate is 1.4), of 16 such prompts in bf16 63 us
+// (a copy's rate 41), in 8 and 4 bits, where the conversion of the codes sets the time,
+// 60 and 67 (22 and 12); scores of 64 ragged sequences of up to 512 blocks 9.5 us (11.5;
+// a copy's rate 5.1: two rounds of 16 warps an SM), of 8 x 8192 blocks 24.7 us = 82 % of a
+// copy's rate.  With hi and lo one after the other in 64 registers, and twice as many
+// warps, these two took 9.4 and 26.7 us (9.8 and 25.0 then), 8 new tokens 18.6 (17.1): not
+// kept.
 #include "w4_device.cuh"
 #include "w4_kv_work.cuh"
 

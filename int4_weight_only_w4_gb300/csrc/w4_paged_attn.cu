@@ -56,7 +56,7 @@
 // Listed blocks (w4_sparse_attn).  A sequence's records are those of its listed
 // blocks; the copying warps find their numbers, and the pages by these, ahead, and tell
 // the others each record's own first key, so that everything else is as above.
-// Measured: 64 ragged sequences reading 4096 tokens each in 8 bits 50.6 us (numbers and
+// Measured: 64 ragged sequences reading 4096 tokens each in 8 bits 51.0 us (numbers and
 // pages asked for in one go 52.4; the whole attention over 64 x 4096 tokens 51.9);
 // 64 blocks of 64 out of 131072 tokens in bf16, one sequence, 10.6.
 //

@@ -19,7 +19,10 @@
 // calls: 64 of up to 2048 items in 256 rows 5.7 us; 1024 of up to 8192 in 256 rows
 // 10.3; 8192 of 131072 in 16 rows 16.2 us, of which the first histogram takes 2, adding
 // those of a cluster 1.7, the listed keys 3, the places and the stores 3; 4096 of 131072
-// in 4 rows 12.7.  On the way there: loads of which each waited for a comparison 44.4
+// in 4 rows 12.7.  Many long rows are the slowest beside their bytes: 4096 of 32768 in
+// 256 rows 39 to 42 us (bytes 5.7), as rows that do not fit as clusters take a block of
+// 1024 threads with 32 keys each, which spills (284 bytes of stores) and has an SM to
+// itself: two waves.  On the way there: loads of which each waited for a comparison 44.4
 // us (16 rows); all under way together, clusters that fit at a time 31.0; keys listed
 // after the first digit 25.6; a constant number of items a thread, without branches
 // around each, 17.0.  Blocks of 512 threads with 64 items each 40.2: fewer warps to
